@@ -50,14 +50,35 @@ typedef int mgw_status;
 /* Bits OR-ed into *status_dev by the kernels (the caller zeroes it). */
 #define MGW_DEV_BAD_OFFSETS 1 /* expert_off[0] != 0, decreasing, or expert_off[E] != M/rows */
 #define MGW_DEV_TIMEOUT 2     /* an internal pipeline wait exceeded 1 s; outputs undefined */
-#define MGW_DEV_BAD_INDEX 4   /* mgw_mxfp8_quantize_gather: a row index outside the source */
+#define MGW_DEV_BAD_INDEX 4   /* a row index (quantizers, combine) or expert index (router, dispatch) out of range */
 #define MGW_DEV_BOUNDS 8      /* diagnostic library only (mgw_diag.h): a computed address outside its tensor */
+#define MGW_DEV_BAD_LOGIT 16  /* mgw_moe_route: a logit that is not a number */
 
 #define MGW_MAX_EXPERTS 1024
 
 /* Scale rules of mgw_mxfp8_quantize. */
 #define MGW_SCALE_FLOOR 0    /* OCP MX: 2^(floor(log2 amax) - 8), saturate to +-448 */
 #define MGW_SCALE_CEIL_448 1 /* post-attn page's RoundUp: ceil_pow2(amax * fp32(1/448)) */
+
+/* Element types of the router's logits and of the combine's rows. */
+#define MGW_TYPE_BF16 0
+#define MGW_TYPE_F32 1
+
+/* Router scores. */
+#define MGW_SCORE_SOFTMAX 0
+#define MGW_SCORE_SIGMOID 1
+
+/* Activations of mgw_grouped_fprop_mxfp8_act.  The gated ones take the product's N columns as
+ * N/2 gate columns followed by N/2 up columns: y = silu(gate) * up, gelu(gate) * up. */
+#define MGW_ACT_NONE 0
+#define MGW_ACT_RELU 1
+#define MGW_ACT_GELU 2 /* x * Phi(x), Phi the normal distribution function */
+#define MGW_ACT_SILU 3 /* x / (1 + exp(-x)) */
+#define MGW_ACT_SWIGLU 4
+#define MGW_ACT_GEGLU 5
+
+#define MGW_MAX_TOP_K 32
+#define MGW_MAX_GROUPS 32
 
 /* Human-readable name of a return code (static string). */
 const char *mgw_status_string(mgw_status s);
@@ -316,6 +337,138 @@ mgw_status mgw_grouped_dgrad_mxfp8(const void *dyq, const void *dys, const void 
                                    const void *wts, const int32_t *expert_off, int E, int M,
                                    int N, int K, size_t Mcap, size_t Mw, void *dx_bf16,
                                    int *status_dev, void *stream);
+
+/* ------------------------------------------------------------- the routed layer
+ * What surrounds the grouped products of a Mixture-of-Experts layer: the router, the row
+ * tables every entry point above takes (expert_off, row_index), the expert product with its
+ * bias, activation and residual, and the way back to token order.  Each with its backward
+ * pass. */
+
+/* mgw_moe_route -- the top_k experts of every token and their weights.
+ *   s[t, e] = softmax over e of logits[t, :], or 1 / (1 + exp(-logits[t, e]))
+ *   v[t, e] = s[t, e] + bias[e] with a balance bias; without one the logits themselves (both
+ *             scores grow with the logit, so the order is that of the logits)
+ *   groups > 1: experts fall into `groups` runs of E / groups; a run's value is its largest v,
+ *             or with group_best 2 the sum of its two largest (of s + bias; of s without a
+ *             bias); only experts of the top_groups best runs can be chosen
+ *   expert_idx[t, :] = the top_k largest v in descending order, ties to the lower index
+ *   weights[t, k] = scale * s_k, with renorm scale * s_k / sum of the chosen s (0 when that
+ *             sum is 0); the bias moves the choice, never the weights
+ * An expert whose logit is -inf is masked for that token: its score is 0 and it is never
+ * chosen.  Where fewer than top_k experts are left, the remaining slots are expert -1 with
+ * weight 0 (mgw_moe_dispatch drops them).  A logit that is not a number counts as masked and
+ * sets MGW_DEV_BAD_LOGIT.
+ *
+ * logits     device, [T, E] row-major, of `dtype` (MGW_TYPE_BF16 or MGW_TYPE_F32); T >= 0.
+ * E          1 .. MGW_MAX_EXPERTS; a multiple of groups (else MGW_ERR_UNSUPPORTED).
+ * bias       device fp32 [E], nullable, finite.
+ * top_k      1 .. min(MGW_MAX_TOP_K, E).
+ * groups     1 .. MGW_MAX_GROUPS; top_groups 1 .. groups; group_best 1 or 2.
+ * expert_idx device int32 [T, top_k], weights device fp32 [T, top_k]: fully written.
+ * scores     device fp32 [T, E], nullable: s, for an auxiliary loss.
+ * All arithmetic is fp32.  Selection values that differ by less than their fp32 rounding may
+ * be taken in either order; equal logits (without a bias) never are. */
+mgw_status mgw_moe_route(const void *logits, int dtype, int T, int E, const float *bias, int top_k,
+                         int score, int groups, int top_groups, int group_best, int renorm,
+                         float scale, int32_t *expert_idx, float *weights, float *scores,
+                         int *status_dev, void *stream);
+
+/* mgw_moe_route_backward -- the gradient of the weights, and of the scores, to the logits.
+ * The choice itself has no gradient, so bias and groups do not enter.
+ * logits, dtype, T, E, top_k, score, renorm, scale and expert_idx as in the forward call.
+ * dweights   device fp32 [T, top_k], nullable (no gradient from the weights); entries of
+ *            slots with expert -1 are not used.
+ * dscores    device fp32 [T, E], nullable; entries of masked experts are not used.
+ * dlogits    device, [T, E] of the logits' type, fully written; 0 for masked experts.
+ * A token's experts are distinct.  An expert outside [-1, E) sets MGW_DEV_BAD_INDEX and counts
+ * as -1. */
+mgw_status mgw_moe_route_backward(const void *logits, int dtype, int T, int E, int top_k, int score,
+                                  int renorm, float scale, const int32_t *expert_idx,
+                                  const float *dweights, const float *dscores, void *dlogits,
+                                  int *status_dev, void *stream);
+
+/* mgw_moe_dispatch -- the row tables of a routing: a stable sort of the T * top_k (token,
+ * slot) pairs by expert.
+ * expert_idx device int32 [T, top_k]; -1 drops the pair.  Anything else outside [0, E) sets
+ *            MGW_DEV_BAD_INDEX and drops the pair too.
+ * expert_off device int32 [E+1]: rows of expert e are expert_off[e] .. expert_off[e+1]-1.
+ *            expert_off[E] = T * top_k less the dropped pairs: the M (rows) of the calls
+ *            above.  With nothing dropped the caller knows it without reading it back.
+ * row_index  device int32 [T * top_k]: the token of every row, ascending within an expert;
+ *            -1 past expert_off[E].  The row_index of the gathering quantizers.
+ * row_of     device int32 [T, top_k]: the row of every pair, -1 for a dropped one.
+ * workspace  device, 16-byte aligned, mgw_moe_dispatch_workspace_bytes bytes; need not be
+ *            initialised, null when that is 0.
+ * T >= 0, 1 <= top_k <= MGW_MAX_TOP_K, T * top_k <= 2^30 (else MGW_ERR_UNSUPPORTED). */
+mgw_status mgw_moe_dispatch(const int32_t *expert_idx, int T, int top_k, int E, int32_t *expert_off,
+                            int32_t *row_index, int32_t *row_of, void *workspace,
+                            size_t workspace_bytes, int *status_dev, void *stream);
+/* Host only; 0 for small calls and for invalid sizes. */
+size_t mgw_moe_dispatch_workspace_bytes(int T, int top_k, int E);
+
+/* mgw_grouped_fprop_mxfp8_act -- mgw_grouped_fprop_mxfp8 with bias, activation and residual:
+ *   z[r, n] = sum_k deq(x)[r, k] * deq(W)[e(r), n, k] + bias[e(r), n]
+ *   y[r, j] = act(z)[r, j] + residual[r, j]
+ * in one pass over fp32 accumulators; y and z are each rounded once (act sees the unrounded z).
+ * xq, xs, wq, ws, expert_off, E, M, N, K, Mcap, Mw as in mgw_grouped_fprop_mxfp8.  The output
+ * has F columns: F = N, or N / 2 for the gated activations (N stays a multiple of 256).
+ * act        MGW_ACT_*.
+ * bias       device fp32 [E, N], nullable.
+ * residual   device, bf16 [M, F], nullable; may be y itself.
+ * y_bf16     device, bf16 [M, F], fully written.
+ * z_bf16     device, bf16 [M, N], nullable: the pre-activation for the backward pass. */
+mgw_status mgw_grouped_fprop_mxfp8_act(const void *xq, const void *xs, const void *wq,
+                                       const void *ws, const int32_t *expert_off, int E, int M,
+                                       int N, int K, size_t Mcap, size_t Mw, int act,
+                                       const float *bias, const void *residual, void *y_bf16,
+                                       void *z_bf16, int *status_dev, void *stream);
+
+/* mgw_grouped_act_backward -- the backward pass of that epilogue:
+ *   dz[r, n] = dy[r, n] * act'(z[r, n]); gated: dz of the gate columns dy * up * act'(gate),
+ *              of the up columns dy * act(gate)
+ *   dbias[e, n] = sum over the rows r of expert e of dz[r, n] (fp32, before dz is rounded;
+ *              0 for an expert without rows)
+ * (dz then goes to the quantizers of the data and weight gradients; the residual's gradient is
+ * dy.)
+ * dy_bf16    device, bf16 [M, F].
+ * z_bf16     device, bf16 [M, N]; null for MGW_ACT_NONE.
+ * N          a positive multiple of 128 (of 256 for the gated activations).
+ * dz_bf16    device, bf16 [M, N], fully written; null for MGW_ACT_NONE (dz is dy).
+ * dbias      device fp32 [E, N], nullable.  The sum's order is fixed by the sizes.
+ * workspace  device, 16-byte aligned, mgw_grouped_act_backward_workspace_bytes bytes when dbias
+ *            is given; need not be initialised. */
+mgw_status mgw_grouped_act_backward(const void *dy_bf16, const void *z_bf16,
+                                    const int32_t *expert_off, int E, int M, int N, int act,
+                                    void *dz_bf16, float *dbias, void *workspace,
+                                    size_t workspace_bytes, int *status_dev, void *stream);
+/* Host only; 0 for invalid sizes. */
+size_t mgw_grouped_act_backward_workspace_bytes(int E, int M, int N);
+
+/* mgw_moe_combine -- routed rows back to token order:
+ *   out[t, h] = residual[t, h] + sum_k weights[t, k] * y[row_of[t, k], h]
+ * in fp32, slot by slot, rounded once.  With null weights every weight is 1, which is also the
+ * gradient of the gather: d hidden[t] = sum_k dx[row_of[t, k]].
+ * y          device, [M, H] row-major, of `dtype`; may be null when M is 0.
+ * row_of     device int32 [T, top_k]; -1 drops the pair.  Anything else outside [0, M) sets
+ *            MGW_DEV_BAD_INDEX and drops the pair too.
+ * weights    device fp32 [T, top_k], nullable; those of dropped pairs are not used.
+ * residual   device, [T, H] of `dtype`, nullable; may be out itself.
+ * out        device, [T, H] of `dtype`, fully written.
+ * T >= 0, M >= 0, 1 <= top_k <= MGW_MAX_TOP_K, 1 <= H <= 2^23 (else MGW_ERR_UNSUPPORTED). */
+mgw_status mgw_moe_combine(const void *y, int dtype, int M, const int32_t *row_of,
+                           const float *weights, const void *residual, int T, int top_k, int H,
+                           void *out, int *status_dev, void *stream);
+
+/* mgw_moe_combine_backward --
+ *   dy[row_of[t, k], h] = weights[t, k] * dout[t, h]
+ *   dweights[t, k]      = sum_h dout[t, h] * y[row_of[t, k], h]   (0 for a dropped pair)
+ * No two pairs name one row (as mgw_moe_dispatch makes them); rows that no pair names are not
+ * written.  The residual's gradient is dout.
+ * y          needed with dweights only.  dweights: device fp32 [T, top_k], nullable.
+ * dy         device, [M, H] of `dtype`.  Everything else as in the forward call. */
+mgw_status mgw_moe_combine_backward(const void *dout, const void *y, int dtype, int M,
+                                    const int32_t *row_of, const float *weights, int T, int top_k,
+                                    int H, void *dy, float *dweights, int *status_dev, void *stream);
 
 #ifdef __cplusplus
 }

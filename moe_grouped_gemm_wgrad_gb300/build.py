@@ -25,7 +25,8 @@ LIB_TESTHOOKS = os.path.join(HERE, "libmgw_testhooks.so")
 # MGW_DEV_BOUNDS.  The other objects are shared with libmgw.so.
 LIB_DIAG = os.path.join(HERE, "libmgw_diag.so")
 DIAG_SOURCES = ["api.cu", "wgrad.cu", "dgrad.cu", "dgrad_pair.cu"]
-SOURCES = ["api.cu", "quantize.cu", "quantize_rows.cu", "wgrad.cu", "wgrad_balanced.cu", "wgrad_noalloc.cu", "grouped_mm.cu", "dgrad.cu", "dgrad_pair.cu"]
+SOURCES = ["api.cu", "quantize.cu", "quantize_rows.cu", "wgrad.cu", "wgrad_balanced.cu", "wgrad_noalloc.cu", "grouped_mm.cu", "dgrad.cu", "dgrad_pair.cu",
+           "route.cu", "dispatch.cu", "combine.cu", "grouped_act.cu", "act_backward.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -573,6 +573,288 @@ mgw_status mgw_grouped_dgrad_mxfp8(const void* dyq, const void* dys, const void*
 
 }  // extern "C"
 
+// ------------------------------------------------------------------- the routed layer
+namespace {
+
+bool element_type(int dtype) { return dtype == MGW_TYPE_BF16 || dtype == MGW_TYPE_F32; }
+bool gated(int act) { return act == MGW_ACT_SWIGLU || act == MGW_ACT_GEGLU; }
+
+mgw_status route_check(const void* logits, int dtype, int T, int E, int top_k, int score,
+                       const void* expert_idx) {
+  if (T > 0 && (!logits || !expert_idx)) return MGW_ERR_INVALID_ARG;
+  if (T < 0 || E < 1 || E > MGW_MAX_EXPERTS || !element_type(dtype)) return MGW_ERR_INVALID_ARG;
+  if (top_k < 1 || top_k > MGW_MAX_TOP_K || top_k > E) return MGW_ERR_INVALID_ARG;
+  if (score != MGW_SCORE_SOFTMAX && score != MGW_SCORE_SIGMOID) return MGW_ERR_INVALID_ARG;
+  return MGW_OK;
+}
+
+mgw_status combine_check(int dtype, int M, const void* row_of, int T, int top_k, int H) {
+  if (!element_type(dtype) || T < 0 || M < 0 || H < 1 || top_k < 1 || top_k > MGW_MAX_TOP_K ||
+      (T > 0 && !row_of))
+    return MGW_ERR_INVALID_ARG;
+  if (H > (1 << 23)) return MGW_ERR_UNSUPPORTED;
+  return MGW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mgw_status mgw_moe_route(const void* logits, int dtype, int T, int E, const float* bias, int top_k,
+                         int score, int groups, int top_groups, int group_best, int renorm,
+                         float scale, int32_t* expert_idx, float* weights, float* scores,
+                         int* status_dev, void* stream) {
+  mgw_status st = route_check(logits, dtype, T, E, top_k, score, expert_idx);
+  if (st != MGW_OK) return st;
+  if (T > 0 && !weights) return MGW_ERR_INVALID_ARG;
+  if (groups < 1 || groups > MGW_MAX_GROUPS || top_groups < 1 || top_groups > groups ||
+      (group_best != 1 && group_best != 2))
+    return MGW_ERR_INVALID_ARG;
+  if (E % groups != 0) return MGW_ERR_UNSUPPORTED;
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(expert_idx) ||
+      !aligned16(weights) || !aligned16(scores))
+    return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK || T == 0) return st;
+  mgw::RouteArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.expert_idx = expert_idx;
+  a.weights = weights;
+  a.scores = scores;
+  a.T = T;
+  a.E = E;
+  a.top_k = top_k;
+  a.groups = top_groups < groups ? groups : 1;  // every group kept: no restriction
+  a.top_groups = top_groups;
+  a.group_best = group_best;
+  a.scale = scale;
+  a.status = status_dev;
+  const cudaError_t err = mgw::launch_route(a, dtype == MGW_TYPE_F32, score == MGW_SCORE_SIGMOID,
+                                            renorm != 0, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+mgw_status mgw_moe_route_backward(const void* logits, int dtype, int T, int E, int top_k, int score,
+                                  int renorm, float scale, const int32_t* expert_idx,
+                                  const float* dweights, const float* dscores, void* dlogits,
+                                  int* status_dev, void* stream) {
+  mgw_status st = route_check(logits, dtype, T, E, top_k, score, expert_idx);
+  if (st != MGW_OK) return st;
+  if (T > 0 && !dlogits) return MGW_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(expert_idx) || !aligned16(dweights) ||
+      !aligned16(dscores) || !aligned16(dlogits))
+    return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK || T == 0) return st;
+  mgw::RouteBwdArgs a;
+  a.logits = logits;
+  a.expert_idx = expert_idx;
+  a.dweights = dweights;
+  a.dscores = dscores;
+  a.dlogits = dlogits;
+  a.T = T;
+  a.E = E;
+  a.top_k = top_k;
+  a.scale = scale;
+  a.status = status_dev;
+  const cudaError_t err =
+      mgw::launch_route_backward(a, dtype == MGW_TYPE_F32, score == MGW_SCORE_SIGMOID, renorm != 0,
+                                 static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+size_t mgw_moe_dispatch_workspace_bytes(int T, int top_k, int E) {
+  if (T < 0 || top_k < 1 || top_k > MGW_MAX_TOP_K || E < 1 || E > MGW_MAX_EXPERTS) return 0;
+  const int blocks = mgw::dispatch_blocks(static_cast<long long>(T) * top_k, E);
+  return blocks > 1 ? sizeof(int) * static_cast<size_t>(blocks) * static_cast<size_t>(E) : 0;
+}
+
+mgw_status mgw_moe_dispatch(const int32_t* expert_idx, int T, int top_k, int E, int32_t* expert_off,
+                            int32_t* row_index, int32_t* row_of, void* workspace,
+                            size_t workspace_bytes, int* status_dev, void* stream) {
+  if (!expert_off || (T > 0 && (!expert_idx || !row_index || !row_of))) return MGW_ERR_INVALID_ARG;
+  if (T < 0 || top_k < 1 || top_k > MGW_MAX_TOP_K || E < 1 || E > MGW_MAX_EXPERTS)
+    return MGW_ERR_INVALID_ARG;
+  const long long pairs = static_cast<long long>(T) * top_k;
+  if (pairs > (1ll << 30)) return MGW_ERR_UNSUPPORTED;
+  if (!aligned16(expert_idx) || !aligned16(expert_off) || !aligned16(row_index) ||
+      !aligned16(row_of) || !aligned16(workspace))
+    return MGW_ERR_INVALID_ARG;
+  const size_t need = mgw_moe_dispatch_workspace_bytes(T, top_k, E);
+  if (need > 0 && !workspace) return MGW_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MGW_ERR_CAPACITY;
+  DeviceInfo dev;
+  const mgw_status st = current_device(&dev);
+  if (st != MGW_OK) return st;
+  mgw::DispatchArgs a;
+  a.expert_idx = expert_idx;
+  a.expert_off = expert_off;
+  a.row_index = row_index;
+  a.row_of = row_of;
+  a.counts = static_cast<int32_t*>(workspace);
+  a.pairs = static_cast<int>(pairs);
+  a.top_k = top_k;
+  a.E = E;
+  a.status = status_dev;
+  const cudaError_t err = mgw::launch_dispatch(a, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+mgw_status mgw_grouped_fprop_mxfp8_act(const void* xq, const void* xs, const void* wq,
+                                       const void* ws, const int32_t* expert_off, int E, int M,
+                                       int N, int K, size_t Mcap, size_t Mw, int act,
+                                       const float* bias, const void* residual, void* y_bf16,
+                                       void* z_bf16, int* status_dev, void* stream) {
+  if (!xq || !xs || !wq || !ws || !expert_off || (M > 0 && !y_bf16)) return MGW_ERR_INVALID_ARG;
+  if (M < 0 || N <= 0 || K <= 0 || E < 1 || E > MGW_MAX_EXPERTS) return MGW_ERR_INVALID_ARG;
+  if (act < MGW_ACT_NONE || act > MGW_ACT_GEGLU) return MGW_ERR_INVALID_ARG;
+  if (N % 256 != 0 || K % 128 != 0) return MGW_ERR_UNSUPPORTED;
+  if (Mcap % 128 != 0 || Mcap < mgw_mxfp8_token_capacity(M, E) || Mcap > (size_t(1) << 31))
+    return MGW_ERR_CAPACITY;
+  if (Mw % 128 != 0 || Mw < static_cast<size_t>(E) * N || Mw > (size_t(1) << 31))
+    return MGW_ERR_CAPACITY;
+  // work items are counted in 32 bits
+  if ((static_cast<long long>(M) / (2 * mgw::act_row_box()) + E) * (N / 256) >= (1ll << 30))
+    return MGW_ERR_UNSUPPORTED;
+  if (!aligned16(xq) || !aligned16(xs) || !aligned16(wq) || !aligned16(ws) ||
+      !aligned16(bias) || !aligned16(residual) || !aligned16(y_bf16) ||
+      !aligned16(z_bf16))
+    return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  const mgw_status st = current_device(&dev);
+  if (st != MGW_OK) return st;
+  mgw::ActMmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const uint32_t row_box = static_cast<uint32_t>(mgw::act_row_box());
+  if (!make_map_2d(&a.tm_w, u8, wq, K, Mw, K, 128, gated(act) ? 16 : 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_2d(&a.tm_x, u8, xq, K, Mcap, K, 128, row_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_2d(&a.tm_x16, u8, xq, K, Mcap, K, 128, 16, CU_TENSOR_MAP_SWIZZLE_128B))
+    return MGW_ERR_CUDA;
+  a.ws = static_cast<const uint8_t*>(ws);
+  a.xs = static_cast<const uint8_t*>(xs);
+  a.expert_off = expert_off;
+  a.bias = bias;
+  a.residual = residual;
+  a.y = y_bf16;
+  a.z = z_bf16;
+  a.E = E;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.Mcap = static_cast<long long>(Mcap);
+  a.Mw = static_cast<long long>(Mw);
+  a.status = status_dev;
+  const cudaError_t err = mgw::launch_grouped_act(a, act, dev.sms, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+size_t mgw_grouped_act_backward_workspace_bytes(int E, int M, int N) {
+  if (E < 1 || E > MGW_MAX_EXPERTS || M < 0 || N <= 0) return 0;
+  // one row of sums per 128-row tile of an expert
+  const size_t tiles = static_cast<size_t>(M) / 128 + static_cast<size_t>(M < E ? M : E);
+  return sizeof(float) * tiles * static_cast<size_t>(N);
+}
+
+mgw_status mgw_grouped_act_backward(const void* dy_bf16, const void* z_bf16,
+                                    const int32_t* expert_off, int E, int M, int N, int act,
+                                    void* dz_bf16, float* dbias, void* workspace,
+                                    size_t workspace_bytes, int* status_dev, void* stream) {
+  if (!expert_off || (M > 0 && !dy_bf16)) return MGW_ERR_INVALID_ARG;
+  if (M < 0 || N <= 0 || E < 1 || E > MGW_MAX_EXPERTS) return MGW_ERR_INVALID_ARG;
+  if (act < MGW_ACT_NONE || act > MGW_ACT_GEGLU) return MGW_ERR_INVALID_ARG;
+  if (M > 0 && act != MGW_ACT_NONE && (!z_bf16 || !dz_bf16)) return MGW_ERR_INVALID_ARG;
+  if (N % (gated(act) ? 256 : 128) != 0 || N > (1 << 23)) return MGW_ERR_UNSUPPORTED;
+  // rows on the padded axis are counted in 32 bits
+  if (mgw_mxfp8_token_capacity(M, E) >= (size_t(1) << 31)) return MGW_ERR_UNSUPPORTED;
+  if (!aligned16(dy_bf16) || !aligned16(z_bf16) || !aligned16(dz_bf16) ||
+      !aligned16(dbias) || !aligned16(workspace))
+    return MGW_ERR_INVALID_ARG;
+  if (dbias) {
+    const size_t need = mgw_grouped_act_backward_workspace_bytes(E, M, N);
+    if (need > 0 && !workspace) return MGW_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MGW_ERR_CAPACITY;
+  }
+  DeviceInfo dev;
+  const mgw_status st = current_device(&dev);
+  if (st != MGW_OK) return st;
+  mgw::ActBwdArgs a;
+  a.dy = dy_bf16;
+  a.z = z_bf16;
+  a.expert_off = expert_off;
+  a.dz = dz_bf16;
+  a.dbias = dbias;
+  a.partial = static_cast<float*>(workspace);
+  a.E = E;
+  a.M = M;
+  a.N = N;
+  a.status = status_dev;
+  const cudaError_t err = mgw::launch_act_backward(a, act, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+mgw_status mgw_moe_combine(const void* y, int dtype, int M, const int32_t* row_of,
+                           const float* weights, const void* residual, int T, int top_k, int H,
+                           void* out, int* status_dev, void* stream) {
+  mgw_status st = combine_check(dtype, M, row_of, T, top_k, H);
+  if (st != MGW_OK) return st;
+  if ((M > 0 && !y) || (T > 0 && !out)) return MGW_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(row_of) || !aligned16(weights) ||
+      !aligned16(residual) || !aligned16(out))
+    return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK || T == 0) return st;
+  mgw::CombineArgs a;
+  a.y = y;
+  a.row_of = row_of;
+  a.weights = weights;
+  a.residual = residual;
+  a.out = out;
+  a.M = M;
+  a.T = T;
+  a.top_k = top_k;
+  a.H = H;
+  a.status = status_dev;
+  const cudaError_t err =
+      mgw::launch_combine(a, dtype == MGW_TYPE_F32, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+mgw_status mgw_moe_combine_backward(const void* dout, const void* y, int dtype, int M,
+                                    const int32_t* row_of, const float* weights, int T, int top_k,
+                                    int H, void* dy, float* dweights, int* status_dev, void* stream) {
+  mgw_status st = combine_check(dtype, M, row_of, T, top_k, H);
+  if (st != MGW_OK) return st;
+  if ((T > 0 && !dout) || (M > 0 && !dy) || (M > 0 && dweights && !y)) return MGW_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(row_of) ||
+      !aligned16(weights) || !aligned16(dy) || !aligned16(dweights))
+    return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK || T == 0) return st;
+  mgw::CombineBwdArgs a;
+  a.dout = dout;
+  a.y = y;
+  a.row_of = row_of;
+  a.weights = weights;
+  a.dy = dy;
+  a.dweights = dweights;
+  a.M = M;
+  a.T = T;
+  a.top_k = top_k;
+  a.H = H;
+  a.status = status_dev;
+  const cudaError_t err =
+      mgw::launch_combine_backward(a, dtype == MGW_TYPE_F32, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+}  // extern "C"
+
 #ifdef MGW_DIAG
 extern "C" {
 

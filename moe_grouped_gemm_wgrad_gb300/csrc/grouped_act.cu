@@ -1,0 +1,505 @@
+// Grouped MXFP8 product with bias, activation and residual in its epilogue:
+//
+//   z[r, n] = sum_k x[r, k] W[e(r)][n, k] + bias[e(r), n]
+//   y[r, :] = act(z[r, :]) + residual[r, :]          (gated: act(z[:, :F]) * z[:, F:])
+//
+// The weights are the tensor cores' M side and the routed rows the N side: D^T = W x^T.  An
+// expert's rows then need no padding to a tile: they are cut into ceil(c / 208) tiles of equal
+// width w (a multiple of 16), and the MMA's N is w.  A 1024-row expert runs as 5 tiles of 208
+// instead of 8 of 128, and a decode step's few rows cost an N of 16, so its time is that of
+// reading the weights.  In the accumulator a TMEM lane is an output feature and a column is a
+// row of x: the bias is one register per thread, a warp's store of one row is 64 contiguous
+// bytes, and rows past the expert's last one are masked per column.
+//
+// A CTA pair (tcgen05 cta_group::2) owns 256 weight rows (128 per CTA) x w routed rows (w / 2
+// of them staged per CTA).  Gated products take 128 gate and 128 up rows per pair, interleaved
+// in blocks of 16 (TMA boxes of 16 rows), so that a feature's gate and up values sit in lanes
+// l and l + 16 of one warp and meet by one shuffle.
+//
+// TMEM: two accumulators of 208 columns (the epilogue of one item overlaps the MMAs of the
+// next; 2 x 256 columns would leave no room for scale factors) and six 16-column scale slots.
+//
+// Roles (448 threads per CTA):
+//   warp 0       TMA producer (both CTAs): weight rows, half of the routed rows, scale atoms.
+//   warp 1       MMA issuer (even CTA).
+//   warps 2-9    epilogue: two warps per TMEM lane quarter, taking 16-column groups in turn.
+//   warps 10-13  scale writers (one TMEM lane quarter each): place the stage's scale words in
+//                TMEM; rows are gathered word by word, which is what lets a tile start at any
+//                multiple of 16 rows and the gate / up rows interleave.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mgw {
+namespace {
+
+constexpr int kW = 208;       // widest row tile (MMA N)
+constexpr int BL = 128;       // contraction elements per pipeline stage
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * BL;              // this CTA's 128 weight rows
+constexpr int kBBytes = (kW / 2) * BL;         // this CTA's half of the routed rows
+constexpr int kStageBytes = kABytes + kBBytes; // 29 KB, 1024-aligned
+constexpr int kSfA = 1024;                     // weight scale atoms (two when gated)
+constexpr int kSfB = 1536;                     // scale atoms covering 208 rows from any start
+constexpr int kSfStage = kSfA + kSfB;
+constexpr int kOffSf = kStages * kStageBytes;
+constexpr int kOffBar = kOffSf + kStages * kSfStage;
+// full[], empty[], sf_full[], sf_ready[], acc_full[2], acc_empty[2], done
+constexpr int kNumBars = 4 * kStages + 5;
+constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) & ~15;
+constexpr int kOffTable = kOffMisc + 16;
+constexpr int kEpiWarps = 8;
+constexpr int kSfWarp0 = 10;
+constexpr int kThreads = 14 * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSfCol0 = 2 * kW;
+static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+static_assert(kSfCol0 + 16 * kStages <= kTmemCols, "TMEM budget");
+
+// Tables: expert_off, padded starts and first row tile of every expert, E+1 ints each.
+__host__ __device__ constexpr size_t act_smem_bytes(int E) {
+  return static_cast<size_t>(kOffTable) + sizeof(int) * 3 * (static_cast<size_t>(E) + 1) + 1024;
+}
+static_assert(act_smem_bytes(kMaxExperts) <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
+  int never = 0;
+  (void)mbar_wait(bar, parity, &never);
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// One work item: an expert's row tile x 256 weight rows.
+struct Item {
+  int e;      // expert
+  int ft;     // feature tile
+  int row0;   // first routed row
+  int p0;     // its row on the padded axis
+  int nrows;  // rows of the tile (1 .. 208)
+  int width;  // nrows rounded up to 16: the MMA's N
+};
+
+__device__ __forceinline__ Item decode(int it, int tiles_f, const int* s_off, const int* s_pad,
+                                       const int* s_tile, int E) {
+  const int t = it / tiles_f;
+  int lo = 0, hi = E - 1;  // the largest e with s_tile[e] <= t: an expert with rows
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_tile[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int cnt = s_off[lo + 1] - s_off[lo];
+  const int tiles = s_tile[lo + 1] - s_tile[lo];
+  const int w = ((cnt + tiles - 1) / tiles + 15) & ~15;
+  const int r = (t - s_tile[lo]) * w;
+  Item x;
+  x.e = lo;
+  x.ft = it - t * tiles_f;
+  x.row0 = s_off[lo] + r;
+  x.p0 = s_pad[lo] + r;
+  x.nrows = max(min(w, cnt - r), 0);  // rounding w up can leave a last tile without rows
+  x.width = (x.nrows + 15) & ~15;
+  return x;
+}
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_act_kernel(const __grid_constant__ ActMmArgs args) {
+  constexpr bool kGated = act_gated(ACT);
+  constexpr int kInner = act_inner(ACT);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int E = args.E;
+  int* s_misc = reinterpret_cast<int*>(smem + kOffMisc);  // [0] tmem base [1] abort [2] flag
+  int* s_off = reinterpret_cast<int*>(smem + kOffTable);
+  int* s_pad = s_off + (E + 1);
+  int* s_tile = s_pad + (E + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&s_misc[1]);
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const uint32_t lane = lane_id();
+  const uint32_t rank = cluster_ctarank();  // 0: issues the pair MMAs
+  const bool leader = rank == 0;
+
+  if (tid == 0) s_misc[1] = 0;
+  // Both CTAs read the same offsets, so both return here or neither does.
+  if (!load_offsets(args.expert_off, E, args.M, s_off, s_pad, &s_misc[2], args.status)) return;
+
+  const uint32_t bar0 = sbase + kOffBar;
+  auto bar_full = [&](int st) { return bar0 + 8u * st; };                   // even CTA
+  auto bar_empty = [&](int st) { return bar0 + 8u * (kStages + st); };
+  auto bar_sf_full = [&](int st) { return bar0 + 8u * (2 * kStages + st); };
+  auto bar_sf_ready = [&](int st) { return bar0 + 8u * (3 * kStages + st); };  // even CTA
+  auto bar_acc_full = [&](int b) { return bar0 + 8u * (4 * kStages + b); };
+  auto bar_acc_empty = [&](int b) { return bar0 + 8u * (4 * kStages + 2 + b); };  // even CTA
+  const uint32_t bar_done = bar0 + 8u * (4 * kStages + 4);
+  if (warp == 0) {
+    // first row tile of every expert: an exclusive scan of ceil(count / 208)
+    int carry = 0;
+    if (lane == 0) s_tile[0] = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + static_cast<int>(lane);
+      int v = e < E ? (s_off[e + 1] - s_off[e] + kW - 1) / kW : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= static_cast<uint32_t>(d)) v += y;
+      }
+      if (e < E) s_tile[e + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  } else if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&s_misc[0]), kTmemCols);
+    tmem_relinquish_pair();
+  } else if (warp == 2 && lane == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(bar_full(st), 1);
+      mbar_init(bar_empty(st), 1);
+      mbar_init(bar_sf_full(st), 1);
+      mbar_init(bar_sf_ready(st), 8);  // four writer warps in each CTA
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_acc_full(b), 1);
+      mbar_init(bar_acc_empty(b), 2 * kEpiWarps);
+    }
+    mbar_init(bar_done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&args.tm_w);
+    tma_prefetch_desc(&args.tm_x);
+    tma_prefetch_desc(&args.tm_x16);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(s_misc[0]);
+  const uint32_t peer_abort = map_to_cta(smem_u32(&s_misc[1]), rank ^ 1u);
+  auto abort_both = [&]() {
+    *abort_flag = 1;
+    st_cluster_u32(peer_abort, 1u);
+    if (args.status) atomicOr(args.status, kDevTimeout);
+  };
+
+  const int N = args.N;
+  const int F = kGated ? N / 2 : N;  // output columns
+  const int tiles_f = N / 256;
+  const int nch = args.K / BL;
+  const int total = s_tile[E] * tiles_f;  // < 2^31: the C ABI checks the sizes
+  const int npairs = static_cast<int>(gridDim.x >> 1);
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int filled[kStages];
+      uint32_t filled_phase[kStages];
+      for (int st = 0; st < kStages; ++st) filled[st] = 0, filled_phase[st] = 0;
+      bool ok = true;
+      const uint32_t full0_leader = map_to_cta(bar_full(0), 0);
+      const long long a_tiles = args.Mw / 128;   // 128-row tiles of the weights' scale layout
+      const long long b_tiles = args.Mcap / 128;
+      for (int it = pair; it < total && ok; it += npairs) {
+        const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
+        if (x.nrows == 0) continue;
+        // this CTA's weight rows: 128 plain ones, or 64 gate and 64 up rows
+        const int f0 = kGated ? x.ft * 128 + 64 * static_cast<int>(rank)
+                              : x.ft * 256 + 128 * static_cast<int>(rank);
+        const int wrow = x.e * N + f0;
+        const int half = x.width / 2;
+        const int xrow = x.p0 + static_cast<int>(rank) * half;
+        // more than 48 rows come as one 104-row box (the rows past `half` are not used), fewer
+        // in boxes of 16
+        const bool tall = half > 48;
+        const int boxes = (half + 15) / 16;
+        const uint32_t xbytes = tall ? kBBytes : static_cast<uint32_t>(boxes) * 16 * BL;
+        const int xt0 = x.p0 / 128;
+        const uint32_t sfb_bytes = static_cast<uint32_t>((x.p0 + x.width - 1) / 128 - xt0 + 1) * 512;
+        for (int c = 0; c < nch; ++c) {
+          if (!mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(bar_full(stage), 2 * (kABytes + xbytes));
+          const uint32_t fb = full0_leader + 8u * stage;  // the even CTA's full barrier
+          const uint32_t sa = sbase + stage * kStageBytes;
+          if constexpr (kGated) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              tma_load_2d_pair(sa + b * 4096, &args.tm_w, c * BL, wrow + 16 * b, fb);
+              tma_load_2d_pair(sa + b * 4096 + 2048, &args.tm_w, c * BL, wrow + F + 16 * b, fb);
+            }
+          } else {
+            tma_load_2d_pair(sa, &args.tm_w, c * BL, wrow, fb);
+          }
+          if (tall) {
+            tma_load_2d_pair(sa + kABytes, &args.tm_x, c * BL, xrow, fb);
+          } else {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(sa + kABytes + b * 2048, &args.tm_x16, c * BL, xrow + 16 * b, fb);
+          }
+          const uint32_t sfbar = bar_sf_full(stage);
+          mbar_arrive_expect_tx(sfbar, (kGated ? 1024u : 512u) + sfb_bytes);
+          const uint32_t ssf = sbase + kOffSf + stage * kSfStage;
+          bulk_load(ssf, args.ws + (c * a_tiles + wrow / 128) * 512, 512, sfbar);
+          if constexpr (kGated)
+            bulk_load(ssf + 512, args.ws + (c * a_tiles + (wrow + F) / 128) * 512, 512, sfbar);
+          bulk_load(ssf + kSfA, args.xs + (c * b_tiles + xt0) * 512, sfb_bytes, sfbar);
+          filled[stage] = 1;
+          filled_phase[stage] = phase;
+          if (++stage == kStages) stage = 0, phase ^= 1u;
+        }
+      }
+      if (!ok) abort_both();
+      // Every stage this CTA filled is released by the MMAs that read it (or, after an abort,
+      // the wait gives up after its time limit, long after any copy has landed).
+      for (int st = 0; st < kStages; ++st)
+        if (filled[st]) mbar_wait_drain(bar_empty(st), filled_phase[st]);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA issuer (even CTA only)
+    if (leader && lane == 0) {
+      int stage = 0, n = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      constexpr uint16_t kBoth = 0x3;
+      const uint64_t a_desc0 = sdesc_kmajor_sw128(sbase);
+      for (int it = pair; it < total && ok; it += npairs) {
+        const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
+        if (x.nrows == 0) continue;
+        const int buf = n & 1;
+        if (!mbar_wait_spin(bar_acc_empty(buf), ((n >> 1) & 1) ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++n;
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * kW);
+        const uint32_t idesc = idesc_mxf8_e4m3(256, x.width, 0, 0);
+        for (int c = 0; c < nch; ++c) {
+          if (!mbar_wait_spin(bar_full(stage), phase, abort_flag) ||
+              !mbar_wait_spin(bar_sf_ready(stage), phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tsf = tmem + kSfCol0 + 16u * stage;
+          const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (kStageBytes >> 4));
+          const uint64_t bd = ad + (kABytes >> 4);
+#pragma unroll
+          for (uint32_t kb = 0; kb < 4; ++kb)
+            mma_mxf8_block32_pair(d, ad + 2 * kb, bd + 2 * kb, idesc | (kb << 4) | (kb << 29), tsf,
+                                  tsf + 8, (c | static_cast<int>(kb)) != 0);
+          mma_commit_pair(bar_empty(stage), kBoth);
+          if (++stage == kStages) stage = 0, phase ^= 1u;
+        }
+        if (!ok) break;
+        mma_commit_pair(bar_acc_full(buf), kBoth);
+      }
+      if (!ok) abort_both();
+      // All MMAs issued by this thread complete before TMEM is released.
+      mma_commit_pair(bar_done, 0x1);
+      mbar_wait_drain(bar_done, 0);
+    }
+  } else if (warp >= kSfWarp0) {
+    // ----------------------------------- scale writers: TMEM lane quarter warp % 4
+    // tcgen05.mma reads the scale of operand row j from lane j % 32, column j / 32 of every
+    // lane quarter, one byte per 32-element block.
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    const uint32_t sf_ready0 = map_to_cta(bar_sf_ready(0), 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = pair; it < total && ok; it += npairs) {
+      const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
+      if (x.nrows == 0) continue;
+      uint32_t oa[4], ob[8];
+#pragma unroll
+      for (int r1 = 0; r1 < 4; ++r1) {
+        if constexpr (kGated) {
+          // row 32 r1 + lane of the interleaved tile: block r1 of 16 gate (up) rows
+          const uint32_t row = (rank & 1u) * 64u + 16u * r1 + (lane & 15u);
+          oa[r1] = (lane >> 4) * 512u + 16u * (row & 31u) + 4u * (row >> 5);
+        } else {
+          oa[r1] = 16u * lane + 4u * r1;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        // 7 columns hold 208 rows; the 8th repeats the 7th and is not read
+        const uint32_t row = static_cast<uint32_t>(x.p0 & 127) + 32u * (q < 7 ? q : 6) + lane;
+        ob[q] = kSfA + (row >> 7) * 512u + 16u * (row & 31u) + 4u * ((row & 127u) >> 5);
+      }
+      for (int c = 0; c < nch; ++c) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_sf_full(stage), phase, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint32_t ssf = sbase + kOffSf + stage * kSfStage;
+        uint32_t a[4], b[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = ld_shared_u32(ssf + oa[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = ld_shared_u32(ssf + ob[j]);
+        const uint32_t tsf = tmem + (quarter * 32u << 16) + kSfCol0 + 16u * stage;
+        tmem_st_x4(tsf, a);
+        tmem_st_x8(tsf + 8, b);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(sf_ready0 + 8u * stage);
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+      }
+    }
+    if (!ok && lane == 0) abort_both();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - 2;
+    const int quarter = warp & 3;  // TMEM lanes this warp may access
+    const int part = ew >> 2;      // even or odd 16-column groups
+    const uint32_t acc_empty0 = map_to_cta(bar_acc_empty(0), 0);
+    int n = 0;
+    for (int it = pair; it < total; it += npairs) {
+      const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
+      if (x.nrows == 0) continue;
+      // this lane's column of z and of y
+      int zc, yc;
+      if constexpr (kGated) {
+        yc = x.ft * 128 + 64 * static_cast<int>(rank) + 16 * quarter + static_cast<int>(lane & 15u);
+        zc = lane < 16 ? yc : F + yc;
+      } else {
+        yc = zc = x.ft * 256 + 128 * static_cast<int>(rank) + 32 * quarter + static_cast<int>(lane);
+      }
+      const float bias = args.bias != nullptr ? args.bias[static_cast<size_t>(x.e) * N + zc] : 0.0f;
+      const int buf = n & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_acc_full(buf), (n >> 1) & 1, abort_flag))) {
+        if (lane == 0) abort_both();
+        break;
+      }
+      ++n;
+      tc_fence_after();
+      const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * kW);
+      for (int g = part; g * 16 < x.nrows; g += 2) {
+        uint32_t r[16];
+        tmem_ld_x16(ta + 16u * g, r);
+        tmem_wait_ld();
+        const int left = x.nrows - 16 * g;  // rows of this group that exist
+        const size_t row = static_cast<size_t>(x.row0) + 16 * g;
+        float z[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(r[j]) + bias;
+        if (args.z != nullptr) {
+          __nv_bfloat16* zp = static_cast<__nv_bfloat16*>(args.z) + row * N + zc;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < left) zp[static_cast<size_t>(j) * N] = __float2bfloat16_rn(z[j]);
+        }
+        if constexpr (kGated) {
+          // lanes 0-15 take the even rows of each pair, lanes 16-31 the odd ones
+          const int odd = static_cast<int>(lane >> 4);
+          const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(args.residual) + (row + odd) * F + yc;
+          __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(args.y) + (row + odd) * F + yc;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? z[2 * j] : z[2 * j + 1], 16);
+            const float gate = odd ? other : z[2 * j];
+            const float up = odd ? z[2 * j + 1] : other;
+            float h = act_value<kInner>(gate) * up;
+            if (2 * j + odd < left) {
+              if (args.residual != nullptr) h += __bfloat162float(rp[static_cast<size_t>(2 * j) * F]);
+              yp[static_cast<size_t>(2 * j) * F] = __float2bfloat16_rn(h);
+            }
+          }
+        } else {
+          const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(args.residual) + row * F + yc;
+          __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(args.y) + row * F + yc;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float h = act_value<kInner>(z[j]);
+            if (j < left) {
+              if (args.residual != nullptr) h += __bfloat162float(rp[static_cast<size_t>(j) * F]);
+              yp[static_cast<size_t>(j) * F] = __float2bfloat16_rn(h);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(acc_empty0 + 8u * buf);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no pair MMA reads this CTA's shared memory or writes its TMEM any more
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+template <int ACT>
+cudaError_t launch(const ActMmArgs& a, int num_sms, cudaStream_t stream) {
+  static thread_local uint64_t attr_ctx = 0;
+  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(grouped_act_kernel<ACT>),
+                                             act_smem_bytes(kMaxExperts), &attr_ctx);
+  if (err != cudaSuccess) return err;
+  // At most one pair per item; the exact number of row tiles is known on the device only.
+  const long long experts = a.M < a.E ? a.M : a.E;
+  const long long total = (static_cast<long long>(a.M) / kW + experts) * (a.N / 256);
+  long long pairs = num_sms / 2;
+  if (pairs > total) pairs = total;
+  if (pairs < 1) pairs = 1;
+  grouped_act_kernel<ACT><<<static_cast<unsigned>(2 * pairs), kThreads, act_smem_bytes(a.E), stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int act_row_box() { return kW / 2; }
+
+cudaError_t launch_grouped_act(const ActMmArgs& a, int act, int num_sms, cudaStream_t stream) {
+  switch (act) {
+    case kActNone: return launch<kActNone>(a, num_sms, stream);
+    case kActRelu: return launch<kActRelu>(a, num_sms, stream);
+    case kActGelu: return launch<kActGelu>(a, num_sms, stream);
+    case kActSilu: return launch<kActSilu>(a, num_sms, stream);
+    case kActSwiglu: return launch<kActSwiglu>(a, num_sms, stream);
+    case kActGeglu: return launch<kActGeglu>(a, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace mgw

@@ -104,6 +104,103 @@ struct MmArgs {
 };
 cudaError_t launch_grouped_mm_mxfp8(const MmArgs& a, int num_sms, cudaStream_t stream);
 
+// Grouped MXFP8 product with a fused epilogue (grouped_act.cu): CTA pairs, 256 weight rows x
+// up to 2 * act_row_box() routed rows per tile.
+struct ActMmArgs {
+  CUtensorMap tm_w;    // W e4m3 [Mw, K], box 128 x 128 rows (16 rows when gated), 128B swizzle
+  CUtensorMap tm_x;    // x e4m3 [Mcap, K], box 128 x act_row_box() rows, 128B swizzle
+  CUtensorMap tm_x16;  // the same, box 128 x 16 rows
+  const uint8_t* ws;   // W scale atoms, (chunk * Mw/128 + row tile) * 512
+  const uint8_t* xs;   // x scale atoms, (chunk * Mcap/128 + row tile) * 512
+  const int32_t* expert_off;
+  const float* bias;      // [E, N] or null
+  const void* residual;   // bf16 [M, F] or null (F = N, or N / 2 when gated)
+  void* y;                // bf16 [M, F]
+  void* z;                // bf16 [M, N] or null
+  int E, M, N, K;
+  long long Mcap, Mw;
+  int* status;
+};
+int act_row_box();
+cudaError_t launch_grouped_act(const ActMmArgs& a, int act, int num_sms, cudaStream_t stream);
+
+// Backward pass of the epilogue (act_backward.cu).  Partial bias sums of every 128-row tile of
+// an expert go to `partial` [tiles, N] (null without dbias) and are summed in tile order.
+struct ActBwdArgs {
+  const void* dy;      // bf16 [M, F]
+  const void* z;       // bf16 [M, N]; null for the identity
+  const int32_t* expert_off;
+  void* dz;            // bf16 [M, N]; null for the identity
+  float* dbias;        // [E, N] or null
+  float* partial;
+  int E, M, N;
+  int* status;
+};
+cudaError_t launch_act_backward(const ActBwdArgs& a, int act, cudaStream_t stream);
+
+// Router (route.cu).  top_k <= 32 (one selected expert per lane), groups <= 32.
+constexpr int kMaxTopK = 32;
+constexpr int kMaxGroups = 32;
+struct RouteArgs {
+  const void* logits;  // [T, E] bf16 or fp32
+  const float* bias;   // [E] or null
+  int32_t* expert_idx; // [T, top_k]
+  float* weights;      // [T, top_k]
+  float* scores;       // [T, E] or null
+  int T, E, top_k, groups, top_groups, group_best;
+  float scale;
+  int* status;
+};
+cudaError_t launch_route(const RouteArgs& a, bool f32, bool sigmoid, bool renorm, cudaStream_t stream);
+struct RouteBwdArgs {
+  const void* logits;
+  const int32_t* expert_idx;
+  const float* dweights;  // [T, top_k] or null
+  const float* dscores;   // [T, E] or null
+  void* dlogits;          // [T, E], the logits' type
+  int T, E, top_k;
+  float scale;
+  int* status;
+};
+cudaError_t launch_route_backward(const RouteBwdArgs& a, bool f32, bool sigmoid, bool renorm,
+                                  cudaStream_t stream);
+
+// Row tables (dispatch.cu).  `blocks` CTAs; more than one needs blocks * E ints of workspace.
+struct DispatchArgs {
+  const int32_t* expert_idx;  // [pairs]
+  int32_t* expert_off;        // [E + 1]
+  int32_t* row_index;         // [pairs]
+  int32_t* row_of;            // [pairs]
+  int32_t* counts;            // workspace [blocks, E]
+  int pairs, top_k, E;
+  int* status;
+};
+int dispatch_blocks(long long pairs, int E);
+cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t stream);
+
+// Combine (combine.cu).
+struct CombineArgs {
+  const void* y;           // [M, H] bf16 or fp32
+  const int32_t* row_of;   // [T, top_k]
+  const float* weights;    // [T, top_k] or null
+  const void* residual;    // [T, H] or null
+  void* out;               // [T, H]
+  int M, T, top_k, H;
+  int* status;
+};
+cudaError_t launch_combine(const CombineArgs& a, bool f32, cudaStream_t stream);
+struct CombineBwdArgs {
+  const void* dout;        // [T, H]
+  const void* y;           // [M, H]; null without dweights
+  const int32_t* row_of;
+  const float* weights;    // or null
+  void* dy;                // [M, H]
+  float* dweights;         // [T, top_k] or null
+  int M, T, top_k, H;
+  int* status;
+};
+cudaError_t launch_combine_backward(const CombineBwdArgs& a, bool f32, cudaStream_t stream);
+
 struct DgradArgs {
   CUtensorMap tm_w;    // W fp32 [E*out_f, in_f], box 256 columns x 32 rows, no swizzle
   CUtensorMap tm_dy;   // dy fp32 [rows, out_f], box 32 columns x 128 rows, 128B swizzle

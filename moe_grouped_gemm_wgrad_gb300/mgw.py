@@ -31,10 +31,23 @@ MGW_DEV_BAD_OFFSETS = 1
 MGW_DEV_TIMEOUT = 2
 MGW_DEV_BAD_INDEX = 4
 MGW_DEV_BOUNDS = 8   # diagnostic library only
+MGW_DEV_BAD_LOGIT = 16
 DIAG_KERNELS = {1: "grouped_wgrad_pair_kernel", 2: "grouped_dgrad_kernel", 3: "grouped_dgrad_pair_kernel"}
 MAX_EXPERTS = 1024
 SCALE_FLOOR = 0      # OCP MX rule 2^(floor(log2 amax) - 8)
 SCALE_CEIL_448 = 1   # the post-attn page's RoundUp rule ceil_pow2(amax / 448)
+TYPE_BF16 = 0
+TYPE_F32 = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2         # x * Phi(x)
+ACT_SILU = 3
+ACT_SWIGLU = 4       # silu(gate) * up, the product's columns being gate then up
+ACT_GEGLU = 5        # gelu(gate) * up
+GATED_ACTS = (ACT_SWIGLU, ACT_GEGLU)
+MAX_TOP_K = 32
 
 EXPORTS = (
     "mgw_status_string", "mgw_version", "mgw_mxfp8_token_capacity", "mgw_mxfp8_scale_bytes",
@@ -42,6 +55,9 @@ EXPORTS = (
     "mgw_grouped_dgrad_f32", "mgw_mxfp8_quantize_rows", "mgw_grouped_fprop_mxfp8",
     "mgw_grouped_dgrad_mxfp8", "mgw_grouped_wgrad_mxfp8_balanced",
     "mgw_grouped_wgrad_workspace_bytes", "mgw_grouped_wgrad_mxfp8_balanced_noalloc",
+    "mgw_moe_route", "mgw_moe_route_backward", "mgw_moe_dispatch",
+    "mgw_moe_dispatch_workspace_bytes", "mgw_grouped_fprop_mxfp8_act", "mgw_grouped_act_backward",
+    "mgw_grouped_act_backward_workspace_bytes", "mgw_moe_combine", "mgw_moe_combine_backward",
 )
 
 
@@ -94,6 +110,25 @@ def bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mgw_grouped_wgrad_workspace_bytes.restype = SZ
     lib.mgw_grouped_wgrad_mxfp8_balanced_noalloc.argtypes = [P, P, P, P, P, I, I, I, I, SZ, P, P, P]
     lib.mgw_grouped_wgrad_mxfp8_balanced_noalloc.restype = I
+    FL = ctypes.c_float
+    lib.mgw_moe_route.argtypes = [P, I, I, I, P, I, I, I, I, I, I, FL, P, P, P, P, P]
+    lib.mgw_moe_route.restype = I
+    lib.mgw_moe_route_backward.argtypes = [P, I, I, I, I, I, I, FL, P, P, P, P, P, P]
+    lib.mgw_moe_route_backward.restype = I
+    lib.mgw_moe_dispatch.argtypes = [P, I, I, I, P, P, P, P, SZ, P, P]
+    lib.mgw_moe_dispatch.restype = I
+    lib.mgw_moe_dispatch_workspace_bytes.argtypes = [I, I, I]
+    lib.mgw_moe_dispatch_workspace_bytes.restype = SZ
+    lib.mgw_grouped_fprop_mxfp8_act.argtypes = [P, P, P, P, P, I, I, I, I, SZ, SZ, I, P, P, P, P, P, P]
+    lib.mgw_grouped_fprop_mxfp8_act.restype = I
+    lib.mgw_grouped_act_backward.argtypes = [P, P, P, I, I, I, I, P, P, P, SZ, P, P]
+    lib.mgw_grouped_act_backward.restype = I
+    lib.mgw_grouped_act_backward_workspace_bytes.argtypes = [I, I, I]
+    lib.mgw_grouped_act_backward_workspace_bytes.restype = SZ
+    lib.mgw_moe_combine.argtypes = [P, I, I, P, P, P, I, I, I, P, P, P]
+    lib.mgw_moe_combine.restype = I
+    lib.mgw_moe_combine_backward.argtypes = [P, P, I, I, P, P, I, I, I, P, P, P, P]
+    lib.mgw_moe_combine_backward.restype = I
     return lib
 
 
@@ -471,3 +506,266 @@ def grouped_dgrad_mxfp8(dyq: torch.Tensor, dys: torch.Tensor, wtq: torch.Tensor,
                                             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_dgrad_mxfp8")
     return out
+
+
+# ------------------------------------------------------------------- the routed layer
+def _element_type(t: torch.Tensor, name: str) -> int:
+    """The C ABI's code of a bf16 or fp32 tensor's type."""
+    if not isinstance(t, torch.Tensor):
+        raise MgwError(f"{name} must be a CUDA tensor")
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    if t.dtype == torch.float32:
+        return TYPE_F32
+    raise MgwError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _shaped(t: torch.Tensor, shape, dtype, name: str) -> None:
+    """``t`` is a contiguous device tensor of exactly ``shape``."""
+    _dev_tensor(t, dtype, name, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise MgwError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None,
+              score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,
+              group_best: int = 1, renorm: bool = True, scale: float = 1.0,
+              with_scores: bool = False, expert_idx: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None, scores: torch.Tensor | None = None,
+              status: torch.Tensor | None = None, stream=None):
+    """The top_k experts of every token of ``logits`` [T, E] (bf16 or fp32) and their weights
+    -> (expert_idx int32 [T, top_k], weights fp32 [T, top_k]), and the scores fp32 [T, E] as a
+    third value when ``with_scores`` (or ``scores``) is given.
+
+    ``bias`` (fp32 [E]) moves the choice but not the weights.  With ``groups`` > 1 only experts
+    of the ``top_groups`` best of ``groups`` equal runs can be chosen, a run's value being its
+    best expert's or (``group_best`` 2) the sum of its two best.  Logits of -inf are masked;
+    slots that no expert is left for hold -1 with weight 0."""
+    dt = _element_type(logits, "logits")
+    _dev_tensor(logits, logits.dtype, "logits", 2)
+    T, E = logits.shape
+    top_k = int(top_k)
+    if top_k < 1 or top_k > min(MAX_TOP_K, E):
+        raise MgwError(f"top_k must be 1 .. {min(MAX_TOP_K, E)}, got {top_k}")
+    if bias is not None:
+        _shaped(bias, (E,), torch.float32, "bias")
+    _status(status)
+    dev = _one_device(logits, bias, expert_idx, weights, scores, status)
+    expert_idx = _out(expert_idx, (T, top_k), torch.int32, dev, "expert_idx")
+    weights = _out(weights, (T, top_k), torch.float32, dev, "weights")
+    if with_scores or scores is not None:
+        scores = _out(scores, (T, E), torch.float32, dev, "scores")
+    with _device(dev):
+        st = load().mgw_moe_route(_ptr(logits), dt, T, E, _ptr(bias), top_k, int(score),
+                                  int(groups), int(top_groups), int(group_best), int(bool(renorm)),
+                                  float(scale), _ptr(expert_idx), _ptr(weights), _ptr(scores),
+                                  _ptr(status), _stream(stream))
+    _check(st, "mgw_moe_route")
+    return (expert_idx, weights) if scores is None else (expert_idx, weights, scores)
+
+
+def moe_route_backward(logits: torch.Tensor, expert_idx: torch.Tensor,
+                       dweights: torch.Tensor | None, dscores: torch.Tensor | None = None,
+                       score: int = SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
+                       dlogits: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """dlogits [T, E] (the logits' type) from the gradients of :func:`moe_route`'s weights and,
+    when the scores are used too, of its scores.  ``logits``, ``expert_idx``, ``score``,
+    ``renorm`` and ``scale`` as in the forward call."""
+    dt = _element_type(logits, "logits")
+    _dev_tensor(logits, logits.dtype, "logits", 2)
+    T, E = logits.shape
+    _dev_tensor(expert_idx, torch.int32, "expert_idx", 2)
+    top_k = expert_idx.shape[1]
+    _shaped(expert_idx, (T, top_k), torch.int32, "expert_idx")
+    if dweights is not None:
+        _shaped(dweights, (T, top_k), torch.float32, "dweights")
+    if dscores is not None:
+        _shaped(dscores, (T, E), torch.float32, "dscores")
+    _status(status)
+    dev = _one_device(logits, expert_idx, dweights, dscores, dlogits, status)
+    dlogits = _out(dlogits, (T, E), logits.dtype, dev, "dlogits")
+    with _device(dev):
+        st = load().mgw_moe_route_backward(_ptr(logits), dt, T, E, top_k, int(score),
+                                           int(bool(renorm)), float(scale), _ptr(expert_idx),
+                                           _ptr(dweights), _ptr(dscores), _ptr(dlogits),
+                                           _ptr(status), _stream(stream))
+    _check(st, "mgw_moe_route_backward")
+    return dlogits
+
+
+def moe_dispatch(expert_idx: torch.Tensor, E: int, expert_off: torch.Tensor | None = None,
+                 row_index: torch.Tensor | None = None, row_of: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 stream=None):
+    """The row tables of a routing ``expert_idx`` int32 [T, top_k] (-1: dropped) over E experts
+    -> (expert_off int32 [E+1], row_index int32 [T*top_k], row_of int32 [T, top_k]).
+
+    ``expert_off`` and ``row_index`` are what the quantizers and grouped products take, with
+    M = expert_off[E] rows (T * top_k when nothing is dropped); ``row_of`` is what
+    :func:`moe_combine` takes.  ``workspace`` (uint8) is allocated when a large call needs one
+    and none is given."""
+    _dev_tensor(expert_idx, torch.int32, "expert_idx", 2)
+    T, top_k = expert_idx.shape
+    E = int(E)
+    if E < 1:
+        raise MgwError(f"E must be at least 1, got {E}")
+    _status(status)
+    dev = _one_device(expert_idx, expert_off, row_index, row_of, workspace, status)
+    lib = load()
+    need = int(lib.mgw_moe_dispatch_workspace_bytes(T, top_k, E))
+    workspace = _out(workspace, (need,), torch.uint8, dev, "workspace") \
+        if need or workspace is not None else None
+    expert_off = _out(expert_off, (E + 1,), torch.int32, dev, "expert_off")
+    row_index = _out(row_index, (T * top_k,), torch.int32, dev, "row_index")
+    row_of = _out(row_of, (T, top_k), torch.int32, dev, "row_of")
+    with _device(dev):
+        st = lib.mgw_moe_dispatch(_ptr(expert_idx), T, top_k, E, _ptr(expert_off), _ptr(row_index),
+                                  _ptr(row_of), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(), _ptr(status),
+                                  _stream(stream))
+    _check(st, "mgw_moe_dispatch")
+    return expert_off, row_index, row_of
+
+
+def grouped_fprop_mxfp8_act(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor,
+                            ws: torch.Tensor, expert_off: torch.Tensor, M: int, N: int,
+                            act: int = ACT_NONE, bias: torch.Tensor | None = None,
+                            residual: torch.Tensor | None = None, save_preact: bool = False,
+                            out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                            status: torch.Tensor | None = None, stream=None):
+    """y [M, F] bf16 = act(x[r] . W[e(r)]^T + bias[e(r)]) + residual, F = N (N / 2 for the gated
+    activations, whose gate columns come first), from the operands of
+    :func:`grouped_fprop_mxfp8`.  With ``save_preact`` (or ``preact``) returns (y, z), z [M, N]
+    bf16 being the pre-activation that :func:`grouped_act_backward` takes."""
+    for t, n in ((xq, "xq"), (wq, "wq")):
+        _dev_tensor(t, torch.uint8, n, 2)
+    for t, n in ((xs, "xs"), (ws, "ws")):
+        _dev_tensor(t, torch.uint8, n)
+    E = _offsets(expert_off)
+    _status(status)
+    Mcap, K = xq.shape
+    Mw, K_w = wq.shape
+    if K_w != K:
+        raise MgwError(f"wq [Mw, {K_w}] and xq [Mcap, {K}] must share the contraction width")
+    _need(xs, scale_bytes(K, Mcap), "xs")
+    _need(ws, scale_bytes(K, Mw), "ws")
+    M, N, act = int(M), int(N), int(act)
+    F = N // 2 if act in GATED_ACTS else N
+    if bias is not None:
+        _shaped(bias, (E, N), torch.float32, "bias")
+    if residual is not None:
+        _shaped(residual, (M, F), torch.bfloat16, "residual")
+    dev = _one_device(xq, xs, wq, ws, expert_off, bias, residual, out, preact, status)
+    out = _out(out, (M, F), torch.bfloat16, dev, "out")
+    if save_preact or preact is not None:
+        preact = _out(preact, (M, N), torch.bfloat16, dev, "preact")
+    with _device(dev):
+        st = load().mgw_grouped_fprop_mxfp8_act(
+            _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(expert_off), E, M, N, K, Mcap, Mw, act,
+            _ptr(bias), _ptr(residual), _ptr(out), _ptr(preact), _ptr(status), _stream(stream))
+    _check(st, "mgw_grouped_fprop_mxfp8_act")
+    return out if preact is None else (out, preact)
+
+
+def grouped_act_backward(dy: torch.Tensor, z: torch.Tensor | None, expert_off: torch.Tensor,
+                         act: int, with_dbias: bool = False, dz: torch.Tensor | None = None,
+                         dbias: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None):
+    """-> (dz bf16 [M, N], dbias fp32 [E, N] or None): the backward pass of
+    :func:`grouped_fprop_mxfp8_act`'s epilogue from dy [M, F] bf16 and the saved pre-activation
+    z [M, N] bf16.  For ACT_NONE z is None and dz is dy itself.  ``workspace`` (uint8) is
+    allocated when dbias is asked for and none is given."""
+    act = int(act)
+    _dev_tensor(dy, torch.bfloat16, "dy", 2)
+    M, F = dy.shape
+    N = 2 * F if act in GATED_ACTS else F
+    if act == ACT_NONE:
+        if z is not None or dz is not None:
+            raise MgwError("ACT_NONE takes no z and no dz: dz is dy")
+    else:
+        if z is None:
+            raise MgwError("z (the saved pre-activation) is needed for this activation")
+        _shaped(z, (M, N), torch.bfloat16, "z")
+    E = _offsets(expert_off)
+    _status(status)
+    dev = _one_device(dy, z, expert_off, dz, dbias, workspace, status)
+    if act != ACT_NONE:
+        dz = _out(dz, (M, N), torch.bfloat16, dev, "dz")
+    lib = load()
+    if with_dbias or dbias is not None:
+        dbias = _out(dbias, (E, N), torch.float32, dev, "dbias")
+        need = int(lib.mgw_grouped_act_backward_workspace_bytes(E, M, N))
+        workspace = _out(workspace, (need,), torch.uint8, dev, "workspace")
+    with _device(dev):
+        st = lib.mgw_grouped_act_backward(_ptr(dy), _ptr(z), _ptr(expert_off), E, M, N, act,
+                                          _ptr(dz), _ptr(dbias), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel(),
+                                          _ptr(status), _stream(stream))
+    _check(st, "mgw_grouped_act_backward")
+    return (dy if act == ACT_NONE else dz), dbias
+
+
+def moe_combine(y: torch.Tensor, row_of: torch.Tensor, weights: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out [T, H] = residual[t] + sum_k weights[t, k] * y[row_of[t, k]], y [M, H] bf16 or fp32,
+    row_of int32 [T, top_k] (-1: dropped) from :func:`moe_dispatch`.  Without weights every
+    weight is 1: the gradient of gathering the routed rows."""
+    dt = _element_type(y, "y")
+    _dev_tensor(y, y.dtype, "y", 2)
+    M, H = y.shape
+    _dev_tensor(row_of, torch.int32, "row_of", 2)
+    T, top_k = row_of.shape
+    if weights is not None:
+        _shaped(weights, (T, top_k), torch.float32, "weights")
+    if residual is not None:
+        _shaped(residual, (T, H), y.dtype, "residual")
+    _status(status)
+    dev = _one_device(y, row_of, weights, residual, out, status)
+    out = _out(out, (T, H), y.dtype, dev, "out")
+    with _device(dev):
+        st = load().mgw_moe_combine(_ptr(y), dt, M, _ptr(row_of), _ptr(weights), _ptr(residual), T,
+                                    top_k, H, _ptr(out), _ptr(status), _stream(stream))
+    _check(st, "mgw_moe_combine")
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: torch.Tensor,
+                         weights: torch.Tensor | None = None, M: int | None = None,
+                         dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None):
+    """-> (dy [M, H], dweights fp32 [T, top_k] or None): the backward pass of
+    :func:`moe_combine`.  Without weights there is no dweights, y may be None and M is given
+    instead.  Rows of dy that no pair of ``row_of`` names are not written."""
+    dt = _element_type(dout, "dout")
+    _dev_tensor(dout, dout.dtype, "dout", 2)
+    T, H = dout.shape
+    _dev_tensor(row_of, torch.int32, "row_of", 2)
+    top_k = row_of.shape[1]
+    _shaped(row_of, (T, top_k), torch.int32, "row_of")
+    if weights is not None:
+        _shaped(weights, (T, top_k), torch.float32, "weights")
+        if y is None:
+            raise MgwError("y is needed for the gradient of the weights")
+    elif dweights is not None:
+        raise MgwError("dweights needs weights")
+    if y is not None:
+        _dev_tensor(y, dout.dtype, "y", 2)
+        if y.shape[1] != H or (M is not None and y.shape[0] != int(M)):
+            raise MgwError(f"y {tuple(y.shape)} does not match dout [T, {H}] or M")
+        M = y.shape[0]
+    elif M is None:
+        raise MgwError("M (the number of routed rows) is needed without y")
+    M = int(M)
+    _status(status)
+    dev = _one_device(dout, y, row_of, weights, dy, dweights, status)
+    dy = _out(dy, (M, H), dout.dtype, dev, "dy")
+    if weights is not None:
+        dweights = _out(dweights, (T, top_k), torch.float32, dev, "dweights")
+    with _device(dev):
+        st = load().mgw_moe_combine_backward(_ptr(dout), _ptr(y), dt, M, _ptr(row_of),
+                                             _ptr(weights), T, top_k, H, _ptr(dy), _ptr(dweights),
+                                             _ptr(status), _stream(stream))
+    _check(st, "mgw_moe_combine_backward")
+    return dy, dweights
