@@ -8,24 +8,25 @@
 // width w (a multiple of 16), and the MMA's N is w.  A 1024-row expert runs as 5 tiles of 208
 // instead of 8 of 128, and a decode step's few rows cost an N of 16, so its time is that of
 // reading the weights.  In the accumulator a TMEM lane is an output feature and a column is a
-// row of x: the bias is one register per thread, a warp's store of one row is 64 contiguous
-// bytes, and rows past the expert's last one are masked per column.
+// row of x; the epilogue turns 16-column groups by stmatrix.trans into row-major 16-byte
+// pieces, so rows past the expert's last one are masked per piece.
 //
 // A CTA pair (tcgen05 cta_group::2) owns 256 weight rows (128 per CTA) x w routed rows (w / 2
 // of them staged per CTA).  Gated products take 128 gate and 128 up rows per pair, interleaved
-// in blocks of 16 (TMA boxes of 16 rows), so that a feature's gate and up values sit in lanes
-// l and l + 16 of one warp and meet by one shuffle.
+// in blocks of 16 (TMA boxes of 16 rows): lanes 0-15 of a TMEM lane quarter are gate rows and
+// lanes 16-31 the same features' up rows, so the two 16-lane loads of a group give every thread
+// the gate and the up value of its elements.
 //
 // TMEM: two accumulators of 208 columns (the epilogue of one item overlaps the MMAs of the
 // next; 2 x 256 columns would leave no room for scale factors) and six 16-column scale slots.
 //
-// Roles (448 threads per CTA):
+// Roles (576 threads per CTA):
 //   warp 0       TMA producer (both CTAs): weight rows, half of the routed rows, scale atoms.
 //   warp 1       MMA issuer (even CTA).
 //   warps 2-9    epilogue: two warps per TMEM lane quarter, taking 16-column groups in turn.
-//   warps 10-13  scale writers (one TMEM lane quarter each): place the stage's scale words in
-//                TMEM; rows are gathered word by word, which is what lets a tile start at any
-//                multiple of 16 rows and the gate / up rows interleave.
+//   warps 10-17  scale writers: warps 10-13 the even stages, 14-17 the odd ones, one TMEM lane
+//                quarter each.  They place the stage's scale words in TMEM, which is what lets
+//                a tile start at any multiple of 16 rows and the gate / up rows interleave.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -51,10 +52,14 @@ constexpr int kOffBar = kOffSf + kStages * kSfStage;
 // full[], empty[], sf_full[], sf_ready[], acc_full[2], acc_empty[2], done
 constexpr int kNumBars = 4 * kStages + 5;
 constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) & ~15;
-constexpr int kOffTable = kOffMisc + 16;
 constexpr int kEpiWarps = 8;
+// Per epilogue warp: 16 rows of y (or z) by 32 features in bf16, rows 80 bytes apart so that
+// the 8 rows of a matrix meet 8 different bank groups (48 bytes for a gated product's 16).
+constexpr int kTurnBytes = 16 * 80;
+constexpr int kOffTurn = kOffMisc + 16;
+constexpr int kOffTable = kOffTurn + kEpiWarps * kTurnBytes;
 constexpr int kSfWarp0 = 10;
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = 18 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 2 * kW;
 static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
@@ -70,11 +75,6 @@ __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
   int never = 0;
   (void)mbar_wait(bar, parity, &never);
 }
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&v)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
                "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -89,16 +89,124 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
+// 16 lanes x 16 columns: r[4 b + 2 h + i] is lane lane_id / 4 + 8 h, column 8 b + 2 (lane_id % 4) + i.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
+// Waits for the loads into r; naming r keeps its uses behind the wait.
+__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values between fragments (lane l: row l / 4, columns
+// 2 (l % 4) + {0, 1}) and shared memory, transposed: lane l gives the address of memory row
+// l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+}
+
+// A warp's staging tile of 16 rows x (8 CH) features, CH 16-byte chunks per row, and the bf16
+// matrix [.., pitch] it is a piece of: rows row0 .. row0 + left - 1 exist, features from col.
+template <int CH>
+struct Turn {
+  static constexpr int kStride = CH == 4 ? 80 : 48;
+  // Fragment f[4 b + i] of rows 8 b .., chunk i (CH == 4), or f[2 b + i] (CH == 2).
+  static __device__ __forceinline__ void put(uint32_t tile, const uint32_t* f) {
+    const uint32_t l = lane_id();
+    if constexpr (CH == 4) {
+      const uint32_t a = tile + (l & 7u) * kStride + (l >> 3) * 16u;
+      stmatrix_x4_trans(a, f);
+      stmatrix_x4_trans(a + 8 * kStride, f + 4);
+    } else {
+      stmatrix_x4_trans(tile + ((l & 7u) + 8u * (l >> 4)) * kStride + ((l >> 3) & 1u) * 16u, f);
+    }
+    __syncwarp();
+  }
+  static __device__ __forceinline__ void get(uint32_t tile, uint32_t* f) {
+    const uint32_t l = lane_id();
+    if constexpr (CH == 4) {
+      const uint32_t a = tile + (l & 7u) * kStride + (l >> 3) * 16u;
+      ldmatrix_x4_trans(a, f);
+      ldmatrix_x4_trans(a + 8 * kStride, f + 4);
+    } else {
+      ldmatrix_x4_trans(tile + ((l & 7u) + 8u * (l >> 4)) * kStride + ((l >> 3) & 1u) * 16u, f);
+    }
+    __syncwarp();
+  }
+  static __device__ __forceinline__ int row_of(int p) {
+    return (CH == 4 ? 8 * p : 0) + static_cast<int>(lane_id() / CH);
+  }
+  static __device__ __forceinline__ void store(uint32_t tile, __nv_bfloat16* m, size_t row0, int pitch,
+                                               int col, int left) {
+    const int chunk = static_cast<int>(lane_id() % CH);
+#pragma unroll
+    for (int p = 0; p < CH / 2; ++p) {
+      const int r = row_of(p);
+      const uint4 v = ld_shared_v4(tile + r * kStride + chunk * 16);
+      if (r < left)
+        *reinterpret_cast<uint4*>(m + (row0 + r) * static_cast<size_t>(pitch) + col + 8 * chunk) = v;
+    }
+    __syncwarp();  // the tile is free again
+  }
+  static __device__ __forceinline__ void load(const __nv_bfloat16* m, size_t row0, int pitch, int col,
+                                              int left, uint4 (&v)[CH / 2]) {
+    const int chunk = static_cast<int>(lane_id() % CH);
+#pragma unroll
+    for (int p = 0; p < CH / 2; ++p) {
+      const int r = row_of(p);
+      v[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < left)
+        v[p] = *reinterpret_cast<const uint4*>(m + (row0 + r) * static_cast<size_t>(pitch) + col + 8 * chunk);
+    }
+  }
+  static __device__ __forceinline__ void fill(uint32_t tile, const uint4 (&v)[CH / 2]) {
+#pragma unroll
+    for (int p = 0; p < CH / 2; ++p)
+      st_shared_v4(tile + row_of(p) * kStride + (lane_id() % CH) * 16u, v[p]);
+    __syncwarp();
+  }
+};
 
 // One work item: an expert's row tile x 256 weight rows.
 struct Item {
@@ -125,12 +233,14 @@ __device__ __forceinline__ Item decode(int it, int tiles_f, const int* s_off, co
   const int tiles = s_tile[lo + 1] - s_tile[lo];
   const int w = ((cnt + tiles - 1) / tiles + 15) & ~15;
   const int r = (t - s_tile[lo]) * w;
+  lo = __shfl_sync(0xffffffffu, lo, 0);
   Item x;
   x.e = lo;
   x.ft = it - t * tiles_f;
-  x.row0 = s_off[lo] + r;
-  x.p0 = s_pad[lo] + r;
-  x.nrows = max(min(w, cnt - r), 0);  // rounding w up can leave a last tile without rows
+  x.row0 = __shfl_sync(0xffffffffu, s_off[lo] + r, 0);
+  x.p0 = __shfl_sync(0xffffffffu, s_pad[lo] + r, 0);
+  // rounding w up can leave a last tile without rows
+  x.nrows = __shfl_sync(0xffffffffu, max(min(w, cnt - r), 0), 0);
   x.width = (x.nrows + 15) & ~15;
   return x;
 }
@@ -150,7 +260,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* s_tile = s_pad + (E + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&s_misc[1]);
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // The same value in every lane, in a form the compiler knows to be: the producer and the MMA
+  // warp then keep addresses, descriptors and coordinates in uniform registers, which is what
+  // their TMA and tcgen05 instructions take.
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t lane = lane_id();
   const uint32_t rank = cluster_ctarank();  // 0: issues the pair MMAs
   const bool leader = rank == 0;
@@ -206,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised before any remote arrive
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(s_misc[0]);
+  const uint32_t tmem = static_cast<uint32_t>(__shfl_sync(0xffffffffu, s_misc[0], 0));
   const uint32_t peer_abort = map_to_cta(smem_u32(&s_misc[1]), rank ^ 1u);
   auto abort_both = [&]() {
     *abort_flag = 1;
@@ -218,46 +331,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int F = kGated ? N / 2 : N;  // output columns
   const int tiles_f = N / 256;
   const int nch = args.K / BL;
-  const int total = s_tile[E] * tiles_f;  // < 2^31: the C ABI checks the sizes
+  const int total = __shfl_sync(0xffffffffu, s_tile[E], 0) * tiles_f;  // < 2^31: the C ABI checks the sizes
   const int npairs = static_cast<int>(gridDim.x >> 1);
   const int pair = static_cast<int>(blockIdx.x >> 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int filled[kStages];
-      uint32_t filled_phase[kStages];
-      for (int st = 0; st < kStages; ++st) filled[st] = 0, filled_phase[st] = 0;
-      bool ok = true;
-      const uint32_t full0_leader = map_to_cta(bar_full(0), 0);
-      const long long a_tiles = args.Mw / 128;   // 128-row tiles of the weights' scale layout
-      const long long b_tiles = args.Mcap / 128;
-      for (int it = pair; it < total && ok; it += npairs) {
-        const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
-        if (x.nrows == 0) continue;
-        // this CTA's weight rows: 128 plain ones, or 64 gate and 64 up rows
-        const int f0 = kGated ? x.ft * 128 + 64 * static_cast<int>(rank)
-                              : x.ft * 256 + 128 * static_cast<int>(rank);
-        const int wrow = x.e * N + f0;
-        const int half = x.width / 2;
-        const int xrow = x.p0 + static_cast<int>(rank) * half;
-        // more than 48 rows come as one 104-row box (the rows past `half` are not used), fewer
-        // in boxes of 16
-        const bool tall = half > 48;
-        const int boxes = (half + 15) / 16;
-        const uint32_t xbytes = tall ? kBBytes : static_cast<uint32_t>(boxes) * 16 * BL;
-        const int xt0 = x.p0 / 128;
-        const uint32_t sfb_bytes = static_cast<uint32_t>((x.p0 + x.width - 1) / 128 - xt0 + 1) * 512;
-        for (int c = 0; c < nch; ++c) {
-          if (!mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+    // The whole warp walks the loop, one lane issues (measured against one lane walking it
+    // alone: 103 instead of NN cycles per copy).
+    const bool issue = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t chunks = 0;
+    bool ok = true;
+    const uint32_t full0_leader = map_to_cta(bar_full(0), 0);
+    const long long a_tiles = args.Mw / 128;   // 128-row tiles of the weights' scale layout
+    const long long b_tiles = args.Mcap / 128;
+    for (int it = pair; it < total && ok; it += npairs) {
+      const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
+      if (x.nrows == 0) continue;
+      // this CTA's weight rows: 128 plain ones, or 64 gate and 64 up rows
+      const int f0 = kGated ? x.ft * 128 + 64 * static_cast<int>(rank)
+                            : x.ft * 256 + 128 * static_cast<int>(rank);
+      const int wrow = x.e * N + f0;
+      const int half = x.width / 2;
+      const int xrow = x.p0 + static_cast<int>(rank) * half;
+      // more than 48 rows come as one 104-row box (the rows past `half` are not used), fewer
+      // in boxes of 16
+      const bool tall = half > 48;
+      const int boxes = (half + 15) / 16;
+      const uint32_t xbytes = tall ? kBBytes : static_cast<uint32_t>(boxes) * 16 * BL;
+      const int xt0 = x.p0 / 128;
+      const uint32_t sfb_bytes = static_cast<uint32_t>((x.p0 + x.width - 1) / 128 - xt0 + 1) * 512;
+      const uint8_t* wsf = args.ws + static_cast<size_t>(wrow / 128) * 512;
+      const uint8_t* wsf_up = args.ws + static_cast<size_t>((wrow + F) / 128) * 512;
+      const uint8_t* xsf = args.xs + static_cast<size_t>(xt0) * 512;
+      for (int c = 0; c < nch; ++c) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = full0_leader + 8u * stage;  // the even CTA's full barrier
+        const uint32_t sa = sbase + stage * kStageBytes;
+        const uint32_t sfbar = bar_sf_full(stage);
+        const uint32_t ssf = sbase + kOffSf + stage * kSfStage;
+        if (issue) {
           if (leader) mbar_arrive_expect_tx(bar_full(stage), 2 * (kABytes + xbytes));
-          const uint32_t fb = full0_leader + 8u * stage;  // the even CTA's full barrier
-          const uint32_t sa = sbase + stage * kStageBytes;
+          mbar_arrive_expect_tx(sfbar, (kGated ? 1024u : 512u) + sfb_bytes);
+          bulk_load(ssf, wsf, 512, sfbar);
+          if constexpr (kGated) bulk_load(ssf + 512, wsf_up, 512, sfbar);
+          bulk_load(ssf + kSfA, xsf, sfb_bytes, sfbar);
           if constexpr (kGated) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -273,27 +396,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int b = 0; b < boxes; ++b)
               tma_load_2d_pair(sa + kABytes + b * 2048, &args.tm_x16, c * BL, xrow + 16 * b, fb);
           }
-          const uint32_t sfbar = bar_sf_full(stage);
-          mbar_arrive_expect_tx(sfbar, (kGated ? 1024u : 512u) + sfb_bytes);
-          const uint32_t ssf = sbase + kOffSf + stage * kSfStage;
-          bulk_load(ssf, args.ws + (c * a_tiles + wrow / 128) * 512, 512, sfbar);
-          if constexpr (kGated)
-            bulk_load(ssf + 512, args.ws + (c * a_tiles + (wrow + F) / 128) * 512, 512, sfbar);
-          bulk_load(ssf + kSfA, args.xs + (c * b_tiles + xt0) * 512, sfb_bytes, sfbar);
-          filled[stage] = 1;
-          filled_phase[stage] = phase;
-          if (++stage == kStages) stage = 0, phase ^= 1u;
         }
+        wsf += a_tiles * 512;
+        wsf_up += a_tiles * 512;
+        xsf += b_tiles * 512;
+        ++chunks;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
-      if (!ok) abort_both();
-      // Every stage this CTA filled is released by the MMAs that read it (or, after an abort,
-      // the wait gives up after its time limit, long after any copy has landed).
-      for (int st = 0; st < kStages; ++st)
-        if (filled[st]) mbar_wait_drain(bar_empty(st), filled_phase[st]);
+    }
+    if (!ok && lane == 0) abort_both();
+    // Every stage this CTA filled is released by the MMAs that read it (or, after an abort,
+    // the wait gives up after its time limit, long after any copy has landed).
+    const uint32_t filled = chunks < kStages ? chunks : kStages;
+    for (uint32_t i = 0; i < filled; ++i) {
+      const uint32_t c = chunks - 1 - i;
+      mbar_wait_drain(bar_empty(static_cast<int>(c % kStages)), (c / kStages) & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer (even CTA only)
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool issue = elect_one();
       int stage = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -303,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
         if (x.nrows == 0) continue;
         const int buf = n & 1;
-        if (!mbar_wait_spin(bar_acc_empty(buf), ((n >> 1) & 1) ^ 1u, abort_flag)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_acc_empty(buf), ((n >> 1) & 1) ^ 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -311,8 +433,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + static_cast<uint32_t>(buf * kW);
         const uint32_t idesc = idesc_mxf8_e4m3(256, x.width, 0, 0);
         for (int c = 0; c < nch; ++c) {
-          if (!mbar_wait_spin(bar_full(stage), phase, abort_flag) ||
-              !mbar_wait_spin(bar_sf_ready(stage), phase, abort_flag)) {
+          const bool full = mbar_wait(bar_full(stage), phase, abort_flag);
+          const bool scales = mbar_wait(bar_sf_ready(stage), phase, abort_flag);
+          if (!__all_sync(0xffffffffu, full && scales)) {
             ok = false;
             break;
           }
@@ -320,26 +443,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t tsf = tmem + kSfCol0 + 16u * stage;
           const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (kStageBytes >> 4));
           const uint64_t bd = ad + (kABytes >> 4);
+          if (issue) {
 #pragma unroll
-          for (uint32_t kb = 0; kb < 4; ++kb)
-            mma_mxf8_block32_pair(d, ad + 2 * kb, bd + 2 * kb, idesc | (kb << 4) | (kb << 29), tsf,
-                                  tsf + 8, (c | static_cast<int>(kb)) != 0);
-          mma_commit_pair(bar_empty(stage), kBoth);
+            for (uint32_t kb = 0; kb < 4; ++kb)
+              mma_mxf8_block32_pair(d, ad + 2 * kb, bd + 2 * kb, idesc | (kb << 4) | (kb << 29), tsf,
+                                    tsf + 8, (c | static_cast<int>(kb)) != 0);
+            mma_commit_pair(bar_empty(stage), kBoth);
+          }
+          __syncwarp();
           if (++stage == kStages) stage = 0, phase ^= 1u;
         }
         if (!ok) break;
-        mma_commit_pair(bar_acc_full(buf), kBoth);
+        if (issue) mma_commit_pair(bar_acc_full(buf), kBoth);
+        __syncwarp();
       }
-      if (!ok) abort_both();
-      // All MMAs issued by this thread complete before TMEM is released.
-      mma_commit_pair(bar_done, 0x1);
-      mbar_wait_drain(bar_done, 0);
+      if (!ok && lane == 0) abort_both();
+      // All MMAs issued by this warp's lane complete before TMEM is released.
+      if (issue) {
+        mma_commit_pair(bar_done, 0x1);
+        mbar_wait_drain(bar_done, 0);
+      }
+      __syncwarp();
     }
   } else if (warp >= kSfWarp0) {
     // ----------------------------------- scale writers: TMEM lane quarter warp % 4
     // tcgen05.mma reads the scale of operand row j from lane j % 32, column j / 32 of every
     // lane quarter, one byte per 32-element block.
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    const uint32_t parity = static_cast<uint32_t>(warp - kSfWarp0) >> 2;  // this warp's stages
     const uint32_t sf_ready0 = map_to_cta(bar_sf_ready(0), 0);
     int stage = 0;
     uint32_t phase = 0;
@@ -347,42 +478,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int it = pair; it < total && ok; it += npairs) {
       const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
       if (x.nrows == 0) continue;
-      uint32_t oa[4], ob[8];
-#pragma unroll
-      for (int r1 = 0; r1 < 4; ++r1) {
-        if constexpr (kGated) {
-          // row 32 r1 + lane of the interleaved tile: block r1 of 16 gate (up) rows
-          const uint32_t row = (rank & 1u) * 64u + 16u * r1 + (lane & 15u);
-          oa[r1] = (lane >> 4) * 512u + 16u * (row & 31u) + 4u * (row >> 5);
-        } else {
-          oa[r1] = 16u * lane + 4u * r1;
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        // 7 columns hold 208 rows; the 8th repeats the 7th and is not read
-        const uint32_t row = static_cast<uint32_t>(x.p0 & 127) + 32u * (q < 7 ? q : 6) + lane;
-        ob[q] = kSfA + (row >> 7) * 512u + 16u * (row & 31u) + 4u * ((row & 127u) >> 5);
-      }
+      // Row p0 + 32 q + lane of x is word (shift + q) of this lane's row of the atoms: 16 bytes
+      // per atom hold the four rows r0, r0 + 32, r0 + 64, r0 + 96.
+      const uint32_t start = static_cast<uint32_t>(x.p0 & 127) + lane;
+      const uint32_t r0 = start & 31u, shift = start >> 5;
+      const bool by1 = shift & 1u, by2 = shift & 2u, by4 = shift & 4u;
       for (int c = 0; c < nch; ++c) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_sf_full(stage), phase, abort_flag))) {
+        const int st = stage;
+        const uint32_t ph = phase;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if ((st & 1) != static_cast<int>(parity)) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_sf_full(st), ph, abort_flag))) {
           ok = false;
           break;
         }
-        const uint32_t ssf = sbase + kOffSf + stage * kSfStage;
-        uint32_t a[4], b[8];
+        const uint32_t ssf = sbase + kOffSf + st * kSfStage;
+        uint32_t a[4], b[12];
+        if constexpr (kGated) {
+          // tile row 32 r1 + lane is row 64 rank + 16 r1 + lane % 16 of the gate (up) atom
+          const uint32_t src = ssf + (lane >> 4) * 512u + (lane & 15u) * 16u + rank * 8u;
+          const uint2 even = ld_shared_v2(src), odd = ld_shared_v2(src + 256u);
+          a[0] = even.x, a[1] = odd.x, a[2] = even.y, a[3] = odd.y;
+        } else {
+          const uint4 v = ld_shared_v4(ssf + 16u * lane);
+          a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = ld_shared_u32(ssf + oa[j]);
+        for (int j = 0; j < 3; ++j) {
+          const uint4 v = ld_shared_v4(ssf + kSfA + 512u * j + 16u * r0);
+          b[4 * j] = v.x, b[4 * j + 1] = v.y, b[4 * j + 2] = v.z, b[4 * j + 3] = v.w;
+        }
+        // seven words from `shift` (0 .. 4) on; the eighth column is not read by the MMA
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = ld_shared_u32(ssf + ob[j]);
-        const uint32_t tsf = tmem + (quarter * 32u << 16) + kSfCol0 + 16u * stage;
+        for (int j = 0; j < 8; ++j) b[j] = by4 ? b[j + 4] : b[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = by2 ? b[j + 2] : b[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = by1 ? b[j + 1] : b[j];
+        const uint32_t tsf = tmem + (quarter * 32u << 16) + kSfCol0 + 16u * st;
         tmem_st_x4(tsf, a);
-        tmem_st_x8(tsf + 8, b);
+        tmem_st_x8(tsf + 8, *reinterpret_cast<uint32_t(*)[8]>(&b[0]));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(sf_ready0 + 8u * stage);
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if (lane == 0) mbar_arrive_remote(sf_ready0 + 8u * st);
       }
     }
     if (!ok && lane == 0) abort_both();
@@ -392,19 +531,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     const int part = ew >> 2;      // even or odd 16-column groups
     const uint32_t acc_empty0 = map_to_cta(bar_acc_empty(0), 0);
+    const uint32_t tile = sbase + kOffTurn + static_cast<uint32_t>(ew) * kTurnBytes;
+    constexpr int kCh = kGated ? 2 : 4;  // 16-byte chunks of y per row and warp
+    const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(args.residual);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(args.y);
+    __nv_bfloat16* zout = static_cast<__nv_bfloat16*>(args.z);
     int n = 0;
     for (int it = pair; it < total; it += npairs) {
       const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
       if (x.nrows == 0) continue;
-      // this lane's column of z and of y
-      int zc, yc;
-      if constexpr (kGated) {
-        yc = x.ft * 128 + 64 * static_cast<int>(rank) + 16 * quarter + static_cast<int>(lane & 15u);
-        zc = lane < 16 ? yc : F + yc;
-      } else {
-        yc = zc = x.ft * 256 + 128 * static_cast<int>(rank) + 32 * quarter + static_cast<int>(lane);
-      }
-      const float bias = args.bias != nullptr ? args.bias[static_cast<size_t>(x.e) * N + zc] : 0.0f;
+      // the warp's first column of y; of z too (gated: gate columns, up columns F further)
+      const int col = kGated ? x.ft * 128 + 64 * static_cast<int>(rank) + 16 * quarter
+                             : x.ft * 256 + 128 * static_cast<int>(rank) + 32 * quarter;
+      // bias[h][i]: z column of lane 16 h + 8 i + lane_id / 4
+      float bias[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          bias[h][i] = args.bias == nullptr
+                           ? 0.0f
+                           : args.bias[static_cast<size_t>(x.e) * N + col + h * (kGated ? F : 16) +
+                                       8 * i + static_cast<int>(lane >> 2)];
       const int buf = n & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(bar_acc_full(buf), (n >> 1) & 1, abort_flag))) {
         if (lane == 0) abort_both();
@@ -413,49 +561,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++n;
       tc_fence_after();
       const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * kW);
+      uint32_t r[16];
+      if (part * 16 < x.nrows) {
+        tmem_ld_16x256b_x2(ta + 16u * part, r);
+        tmem_ld_16x256b_x2(ta + (16u << 16) + 16u * part, r + 8);
+      }
       for (int g = part; g * 16 < x.nrows; g += 2) {
-        uint32_t r[16];
-        tmem_ld_x16(ta + 16u * g, r);
-        tmem_wait_ld();
         const int left = x.nrows - 16 * g;  // rows of this group that exist
         const size_t row = static_cast<size_t>(x.row0) + 16 * g;
-        float z[16];
+        uint4 rv[kCh / 2];
+        if (res != nullptr) Turn<kCh>::load(res, row, F, col, left, rv);
+        tmem_wait_ld_regs(r);
+        // z[h][b][j]: lane 16 h + 8 (j / 2) + lane_id / 4, row 8 b + 2 (lane_id % 4) + j % 2
+        float z[2][2][4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(r[j]) + bias;
-        if (args.z != nullptr) {
-          __nv_bfloat16* zp = static_cast<__nv_bfloat16*>(args.z) + row * N + zc;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < left) zp[static_cast<size_t>(j) * N] = __float2bfloat16_rn(z[j]);
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[h][b][j] = __uint_as_float(r[8 * h + 4 * b + j]) + bias[h][j >> 1];
+        if ((g + 2) * 16 < x.nrows) {
+          tmem_ld_16x256b_x2(ta + 16u * (g + 2), r);
+          tmem_ld_16x256b_x2(ta + (16u << 16) + 16u * (g + 2), r + 8);
         }
-        if constexpr (kGated) {
-          // lanes 0-15 take the even rows of each pair, lanes 16-31 the odd ones
-          const int odd = static_cast<int>(lane >> 4);
-          const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(args.residual) + (row + odd) * F + yc;
-          __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(args.y) + (row + odd) * F + yc;
+        uint32_t f[8];
+        if (zout != nullptr) {
+          if constexpr (kGated) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? z[2 * j] : z[2 * j + 1], 16);
-            const float gate = odd ? other : z[2 * j];
-            const float up = odd ? z[2 * j + 1] : other;
-            float h = act_value<kInner>(gate) * up;
-            if (2 * j + odd < left) {
-              if (args.residual != nullptr) h += __bfloat162float(rp[static_cast<size_t>(2 * j) * F]);
-              yp[static_cast<size_t>(2 * j) * F] = __float2bfloat16_rn(h);
-            }
-          }
-        } else {
-          const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(args.residual) + row * F + yc;
-          __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(args.y) + row * F + yc;
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float h = act_value<kInner>(z[j]);
-            if (j < left) {
-              if (args.residual != nullptr) h += __bfloat162float(rp[static_cast<size_t>(j) * F]);
-              yp[static_cast<size_t>(j) * F] = __float2bfloat16_rn(h);
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) f[2 * b + i] = pack_bf16(z[h][b][2 * i], z[h][b][2 * i + 1]);
+              Turn<2>::put(tile, f);
+              Turn<2>::store(tile, zout, row, N, col + h * F, left);
             }
+          } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                f[4 * b + i] = pack_bf16(z[i >> 1][b][2 * (i & 1)], z[i >> 1][b][2 * (i & 1) + 1]);
+            Turn<4>::put(tile, f);
+            Turn<4>::store(tile, zout, row, N, col, left);
           }
         }
+        // y in z's place: [0][b][j] when gated
+#pragma unroll
+        for (int h = 0; h < (kGated ? 1 : 2); ++h)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              z[h][b][j] = act_value<kInner>(z[h][b][j]);
+              if constexpr (kGated) z[h][b][j] *= z[1][b][j];
+            }
+        if (res != nullptr) {
+          Turn<kCh>::fill(tile, rv);
+          Turn<kCh>::get(tile, f);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < kCh; ++i) {
+              const float2 v = unpack_bf16(f[kCh * b + i]);
+              z[i >> 1][b][2 * (i & 1)] += v.x;
+              z[i >> 1][b][2 * (i & 1) + 1] += v.y;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < kCh; ++i)
+            f[kCh * b + i] = pack_bf16(z[i >> 1][b][2 * (i & 1)], z[i >> 1][b][2 * (i & 1) + 1]);
+        Turn<kCh>::put(tile, f);
+        Turn<kCh>::store(tile, y, row, F, col, left);
       }
       tc_fence_before();
       __syncwarp();

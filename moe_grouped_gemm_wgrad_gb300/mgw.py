@@ -190,6 +190,9 @@ def diag_timeline_reset() -> None:
 def load() -> ctypes.CDLL:
     """Load libmgw.so (built in-tree by ``moe_grouped_gemm_wgrad_gb300.build``)."""
     global _lib
+    lib = _lib
+    if lib is not None:
+        return lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -206,12 +209,14 @@ def _check(st: int, what: str) -> None:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    """The raw handle of ``stream``, or of the current device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _on_cuda(t: torch.Tensor) -> bool:
@@ -221,7 +226,7 @@ def _on_cuda(t: torch.Tensor) -> bool:
 def _dev_tensor(t: torch.Tensor, dtype, name: str, ndim: int | None = None) -> None:
     if not isinstance(t, torch.Tensor) or not _on_cuda(t):
         raise MgwError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise MgwError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise MgwError(f"{name} must be contiguous")
@@ -253,10 +258,16 @@ def _status(status: torch.Tensor | None) -> None:
 
 
 def _one_device(*ts) -> torch.device:
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) != 1:
-        raise MgwError(f"all tensors must be on one CUDA device, got {sorted(str(d) for d in devs)}")
-    return next(iter(devs))
+    first = None
+    for t in ts:
+        if t is None:
+            continue
+        if first is None:
+            first, dev = t, t.device
+        elif t.device != dev:
+            devs = {str(u.device) for u in ts if u is not None}
+            raise MgwError(f"all tensors must be on one CUDA device, got {sorted(devs)}")
+    return dev
 
 
 def _out(t: torch.Tensor | None, shape, dtype, dev, name: str) -> torch.Tensor:
@@ -271,9 +282,14 @@ def _out(t: torch.Tensor | None, shape, dtype, dev, name: str) -> torch.Tensor:
     return t
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def _device(dev: torch.device):
     """Makes ``dev`` the current CUDA device for the call (the library launches on, and
     sizes its grids for, the current device)."""
+    if torch._C._cuda_getDevice() == dev.index:
+        return _SAME_DEVICE
     return torch.cuda.device(dev)
 
 
