@@ -17,22 +17,45 @@ __host__ __device__ constexpr int act_inner(int act) {
   return act == kActSwiglu ? kActSilu : act == kActGeglu ? kActGelu : act;
 }
 
-__device__ __forceinline__ float normal_cdf(float x) {
-  return 0.5f + 0.5f * erff(x * 0.70710678118654752f);
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// 1 / (1 + e^-x) from e^-|x|, which cannot overflow.  The results are rounded to bf16 by
-// every caller in the GEMM path, so the fast exponential and division (a few fp32 ulp) do.
+// The lower tail h = Phi(-|x|) of the normal distribution and e = exp(-x^2 / 2), by formula
+// 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions: erfc(u) =
+// (a1 t + .. + a5 t^5) exp(-u^2), t = 1 / (1 + 0.3275911 u), with |error| <= 1.5e-7 in erf.
+// Every caller rounds to bf16 (half an ulp is 2e-3 of the value), or sums such values; x Phi(x)
+// is off by at most 1e-7 max(|x|, 1), as it would be through 0.5 + 0.5 erf.
+__device__ __forceinline__ float normal_tail(float x, float& e) {
+  const float t = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.0f));
+  const float y = 0.84932180028801907f * x;  // sqrt(log2(e) / 2)
+  e = ex2_approx(-y * y);
+  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  p = fmaf(p, t, 0.5f * 1.421413741f);
+  p = fmaf(p, t, 0.5f * -0.284496736f);
+  p = fmaf(p, t, 0.5f * 0.254829592f);
+  return p * t * e;
+}
+
+// 1 / (1 + e^-x); e^-x may overflow to infinity, whose reciprocal is 0.
 __device__ __forceinline__ float logistic_fast(float x) {
-  const float q = __expf(-fabsf(x));
-  const float r = __fdividef(1.0f, 1.0f + q);
-  return x >= 0.0f ? r : q * r;
+  return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
   if constexpr (ACT == kActRelu) return fmaxf(x, 0.0f);
-  if constexpr (ACT == kActGelu) return x * normal_cdf(x);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return fmaf(-fabsf(x), normal_tail(x, e), fmaxf(x, 0.0f));  // x Phi(x) = max(x, 0) - |x| h
+  }
   if constexpr (ACT == kActSilu) return x * logistic_fast(x);
   return x;
 }
@@ -44,13 +67,14 @@ __device__ __forceinline__ void act_value_slope(float x, float& value, float& sl
     value = fmaxf(x, 0.0f);
     slope = x > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActGelu) {
-    const float cdf = normal_cdf(x);
-    value = x * cdf;
-    slope = cdf + x * (0.3989422804014327f * __expf(-0.5f * x * x));
+    float e;
+    const float h = normal_tail(x, e);
+    value = fmaf(-fabsf(x), h, fmaxf(x, 0.0f));
+    slope = fmaf(0.3989422804014327f * x, e, x >= 0.0f ? 1.0f - h : h);  // Phi(x) + x phi(x)
   } else if constexpr (ACT == kActSilu) {
     const float s = logistic_fast(x);
     value = x * s;
-    slope = s + value * (1.0f - s);
+    slope = fmaf(value, 1.0f - s, s);
   } else {
     value = x;
     slope = 1.0f;
