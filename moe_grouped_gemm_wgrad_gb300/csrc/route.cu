@@ -8,10 +8,15 @@
 //   expert_idx = the top_k largest v, ties to the lower index; -1 when fewer are left
 //   w_k = scale * s_k, renormalised: scale * s_k / sum_j s_j over the chosen
 //
-// One warp per token: lane l holds the V experts l V .. l V + V - 1 (E <= 32 V), so of equal
-// values the lowest lane's is the lowest index.  Each of the top_k rounds is one warp-wide
-// integer maximum (redux) over order-preserving keys, one ballot, and an update of the winning
-// lane's V keys.  The renormalised softmax needs the chosen logits only; sums are fp32.
+// L lanes of a warp per token, V experts a lane: lane l of the token holds experts l V ..
+// l V + V - 1, so of equal values the lowest lane's is the lowest index.  Up to 256 experts
+// take V = 8 (one or two 16-byte loads) and L = 8, 16 or 32: four, two or one token per warp.
+// A lane sorts its eight keys once; each of the top_k rounds is then a maximum over the token's
+// lanes, one ballot, and a shift of the winning lane's list.  Beyond 256 experts a lane keeps
+// its 16 or 32 keys unsorted and looks through them when it wins.  The work is instruction
+// issue, not bytes: at 65536 x 64 (softmax, top 8) a whole warp per token with two experts a
+// lane took 30 us, this layout 18 us, launch included, against 2 us of reading and writing.  The renormalised
+// softmax needs the chosen logits only; sums are fp32.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -23,12 +28,53 @@ namespace mgw {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8;  // tokens per CTA
+constexpr int kWarps = 8;  // per CTA
+constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// V consecutive elements by 16-byte pieces.
+template <int V>
+__device__ __forceinline__ void load_vec(const float* p, float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p + j);
+    x[j] = f.x, x[j + 1] = f.y, x[j + 2] = f.z, x[j + 3] = f.w;
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p + j);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(h[i]);
+      x[j + 2 * i] = f.x, x[j + 2 * i + 1] = f.y;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 4)
+    *reinterpret_cast<float4*>(p + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+}
+template <int V>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 8) {
+    uint4 u;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[j + 2 * i], x[j + 2 * i + 1]);
+    *reinterpret_cast<uint4*>(p + j) = u;
+  }
+}
 
 // Order-preserving map of a float (not NaN) to an unsigned integer; both zeros map alike.
 // 0 is below every float's key and stands for "not available".
@@ -40,15 +86,32 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Reductions over the token's L lanes.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
   return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 32) return __reduce_max_sync(kAll, v);
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+// The lowest of the token's lanes for which p holds, or -1.
+template <int L>
+__device__ __forceinline__ int lowest_lane(bool p, int lane) {
+  unsigned b = __ballot_sync(kAll, p);
+  if constexpr (L < 32) b &= ((1u << L) - 1u) << (lane & ~(L - 1));
+  return __ffs(b) - 1;
 }
 
 // e^(x - m), exactly 1 at x == m (also when both are infinite)
@@ -57,33 +120,51 @@ __device__ __forceinline__ float exp_from(float x, float m) { return x == m ? 1.
 // The logistic function and its complement from e^-|x|, which cannot overflow.
 __device__ __forceinline__ void logistic(float x, float& s, float& c) {
   const float q = expf(-fabsf(x));
-  const float r = 1.0f / (1.0f + q);
+  const float r = __fdividef(1.0f, 1.0f + q);  // 1 <= 1 + q <= 2
   s = x >= 0.0f ? r : q * r;
   c = x >= 0.0f ? q * r : r;
 }
 
-constexpr float kNegInf = -__builtin_huge_valf();
-
-// Lane `lane`'s V logits, -inf past E; a NaN is reported and counts as -inf.
+// The lane's V logits, -inf past E; a NaN is reported and counts as -inf.
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&x)[V], int* status) {
+__device__ __forceinline__ void load_row(const T* row, int E, int first, bool live, bool vec, float (&x)[V],
+                                         int* status) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = kNegInf;
+  if (live && vec) {
+    if (first < E) load_vec<V>(row + first, x);
+  } else if (live) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (first + j < E) x[j] = load_logit(row + first + j);
+  }
   bool nan = false;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane * V + j;
-    float v = e < E ? load_logit(row + e) : kNegInf;
-    if (v != v) {
-      nan = true;
-      v = kNegInf;
-    }
-    x[j] = v;
+  for (int j = 0; j < V; ++j) nan |= x[j] != x[j];
+  if (nan) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (x[j] != x[j]) x[j] = kNegInf;
+    if (status != nullptr) atomicOr(status, kDevBadLogit);
   }
-  if (nan && status != nullptr) atomicOr(status, kDevBadLogit);
 }
 
-// Scores of the row: softmax over the warp's logits, or the logistic function of each.
-template <int V, bool SIGMOID>
-__device__ __forceinline__ void row_scores(const float (&x)[V], float (&s)[V]) {
+// V values of one lane to a row of fp32 or bf16.
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* row, int E, int first, bool vec, const float (&x)[V]) {
+  if (vec) {
+    if (first < E) store_vec<V>(row + first, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (first + j < E) store_logit(row + first + j, x[j]);
+  }
+}
+
+// Scores of the row: softmax over the token's lanes (max and 1 / sum come back too), or the
+// logistic function of each.
+template <int V, int L, bool SIGMOID>
+__device__ __forceinline__ void row_scores(const float (&x)[V], float (&s)[V], float& m, float& inv) {
   if constexpr (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -91,268 +172,347 @@ __device__ __forceinline__ void row_scores(const float (&x)[V], float (&s)[V]) {
       logistic(x[j], s[j], c);
     }
   } else {
-    float m = kNegInf;
+    m = x[0];
 #pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, x[j]);
-    m = warp_max(m);
+    for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
+    m = lanes_max<L>(m);
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       s[j] = x[j] == kNegInf ? 0.0f : exp_from(x[j], m);
       sum += s[j];
     }
-    sum = warp_sum(sum);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    sum = lanes_sum<L>(sum);
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] *= inv;
   }
 }
 
-template <typename T, int V, bool SIGMOID, bool RENORM>
+// Descending order of the lane's keys, equal ones in index order (a Batcher network for V = 8).
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[V], int (&idx)[V]) {
+  auto swap = [&](int a, int b) {
+    // a stays in front of an equal b unless b's index is lower
+    const bool s = key[b] > key[a] || (key[b] == key[a] && idx[b] < idx[a]);
+    const uint32_t k = key[a];
+    const int i = idx[a];
+    key[a] = s ? key[b] : k;
+    idx[a] = s ? idx[b] : i;
+    key[b] = s ? k : key[b];
+    idx[b] = s ? i : idx[b];
+  };
+  static_assert(V == 8, "the network below is for eight keys");
+  swap(0, 1), swap(2, 3), swap(4, 5), swap(6, 7);
+  swap(0, 2), swap(1, 3), swap(4, 6), swap(5, 7);
+  swap(1, 2), swap(5, 6);
+  swap(0, 4), swap(1, 5), swap(2, 6), swap(3, 7);
+  swap(2, 4), swap(3, 5);
+  swap(1, 2), swap(3, 4), swap(5, 6);
+}
+
+template <typename T, int V, int L, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
-  extern __shared__ float s_vals[];  // with groups: kWarps rows of E values
+  extern __shared__ float s_vals[];  // groups that are not whole lanes: kWarps rows of E values
   const int lane = static_cast<int>(lane_id());
+  const int sub = lane % L;  // lane of the token
   const int warp = threadIdx.x >> 5;
-  const long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  if (t >= a.T) return;
+  const long long t = (static_cast<long long>(blockIdx.x) * kWarps + warp) * (32 / L) + lane / L;
+  const bool live = t < a.T;
   const int E = a.E;
-  float x[V], s[V];
-  load_row<T, V>(static_cast<const T*>(a.logits) + t * E, E, lane, x, a.status);
-  const bool need_scores = SIGMOID || !RENORM || a.scores != nullptr || a.bias != nullptr ||
-                           (a.groups > 1 && a.group_best == 2);
-  if (need_scores) row_scores<V, SIGMOID>(x, s);
-  if (a.scores != nullptr) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = lane * V + j;
-      if (e < E) a.scores[t * E + e] = s[j];
-    }
-  }
+  const int first = sub * V;  // this lane's first expert
+  const bool vec = E % V == 0;
+  const T* row = static_cast<const T*>(a.logits) + t * E;
+  float x[V], s[V], m = 0.0f, inv = 0.0f;
+  load_row<T, V>(row, E, first, live, vec, x, a.status);
+  const bool need_scores = (SIGMOID ? a.bias != nullptr : !RENORM || a.bias != nullptr) ||
+                           a.scores != nullptr || (a.groups > 1 && a.group_best == 2);
+  if (need_scores) row_scores<V, L, SIGMOID>(x, s, m, inv);
+  if (a.scores != nullptr && live) store_row<float, V>(a.scores + t * E, E, first, vec, s);
   uint32_t key[V];
+  if (a.bias != nullptr) {
+    float b[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane * V + j;
-    const float v = a.bias != nullptr && e < E ? s[j] + a.bias[e] : x[j];
-    key[j] = x[j] == kNegInf ? 0u : key_of(v);
+    for (int j = 0; j < V; ++j) b[j] = 0.0f;
+    if (vec) {
+      if (first < E) load_vec<V>(a.bias + first, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (first + j < E) b[j] = a.bias[first + j];
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = x[j] == kNegInf ? 0u : key_of(s[j] + b[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = x[j] == kNegInf ? 0u : key_of(x[j]);
   }
   if (a.groups > 1) {
-    // Group values through shared memory: lane g takes group g.
     const int per = E / a.groups;
-    float* row = s_vals + warp * E;
     const bool sum2 = a.group_best == 2;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = lane * V + j;
-      if (e < E) row[e] = key[j] == 0u ? kNegInf : (sum2 && a.bias == nullptr ? s[j] : value_of(key[j]));
-    }
-    __syncwarp();
-    uint32_t gkey = 0;
-    if (lane < a.groups) {
+    const int lanes = per / V;  // lanes of a group, when groups are whole runs of 2^i lanes
+    if (per % V == 0 && (lanes & (lanes - 1)) == 0) {
       float b1 = kNegInf, b2 = kNegInf;
-      for (int i = 0; i < per; ++i) {
-        const float v = row[lane * per + i];
-        if (v > b1) {
-          b2 = b1;
-          b1 = v;
-        } else if (v > b2) {
-          b2 = v;
-        }
-      }
-      if (b1 != kNegInf) gkey = key_of(sum2 && b2 != kNegInf ? b1 + b2 : b1);
-    }
-    unsigned kept = 0;
-    for (int i = 0; i < a.top_groups; ++i) {
-      const uint32_t m = __reduce_max_sync(kAll, gkey);
-      if (m == 0u) break;
-      const int g = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
-      kept |= 1u << g;
-      if (lane == g) gkey = 0u;
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = lane * V + j;
-      if (e < E && !((kept >> (e / per)) & 1u)) key[j] = 0u;
-    }
-  }
-  // lane k keeps the k-th choice
-  int my_e = -1;
-  uint32_t best = 0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) best = max(best, key[j]);
-  for (int k = 0; k < a.top_k; ++k) {
-    const uint32_t m = __reduce_max_sync(kAll, best);
-    if (m == 0u) break;
-    const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
-    int pick = 0;
-    if (lane == src) {
-      bool found = false;
-      best = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (!found && key[j] == m) {
-          found = true;
-          pick = j;
-          key[j] = 0u;
+        const float v = key[j] == 0u ? kNegInf : (sum2 && a.bias == nullptr ? s[j] : value_of(key[j]));
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
+      }
+      for (int d = lanes / 2; d > 0; d >>= 1) {
+        const float o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+        b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+        b1 = fmaxf(b1, o1);
+      }
+      uint32_t gkey = b1 == kNegInf ? 0u : key_of(sum2 && b2 != kNegInf ? b1 + b2 : b1);
+      bool kept = false;
+      for (int i = 0; i < a.top_groups; ++i) {
+        const uint32_t best = lanes_max<L>(gkey);
+        const int src = lowest_lane<L>(gkey == best && best != 0u, lane);
+        if (src >= 0 && (lane ^ src) < lanes) {  // same run of lanes: only low bits differ
+          kept = true;
+          gkey = 0u;
         }
-        best = max(best, key[j]);
+      }
+      if (!kept) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = 0u;
+      }
+    } else if constexpr (L == 32) {
+      // group values through shared memory: lane g takes group g
+      float* vals = s_vals + warp * E;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (first + j < E)
+          vals[first + j] = key[j] == 0u ? kNegInf : (sum2 && a.bias == nullptr ? s[j] : value_of(key[j]));
+      __syncwarp();
+      uint32_t gkey = 0;
+      if (lane < a.groups) {
+        float b1 = kNegInf, b2 = kNegInf;
+        for (int i = 0; i < per; ++i) {
+          const float v = vals[lane * per + i];
+          b2 = fmaxf(b2, fminf(b1, v));
+          b1 = fmaxf(b1, v);
+        }
+        if (b1 != kNegInf) gkey = key_of(sum2 && b2 != kNegInf ? b1 + b2 : b1);
+      }
+      unsigned kept = 0;
+      for (int i = 0; i < a.top_groups; ++i) {
+        const uint32_t best = lanes_max<32>(gkey);
+        if (best == 0u) break;
+        const int g = lowest_lane<32>(gkey == best, lane);
+        kept |= 1u << g;
+        if (lane == g) gkey = 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (first + j < E && !((kept >> ((first + j) / per)) & 1u)) key[j] = 0u;
+    }
+  }
+  // lane k of the token keeps its k-th choice (top_k <= L)
+  int my_e = -1;
+  if constexpr (V == 8) {
+    int idx[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) idx[j] = j;
+    sort_keys<V>(key, idx);
+    for (int k = 0; k < a.top_k; ++k) {
+      const uint32_t best = lanes_max<L>(key[0]);
+      const int src = lowest_lane<L>(key[0] == best && best != 0u, lane);
+      const int e = __shfl_sync(kAll, first + idx[0], src < 0 ? lane : src);
+      if (sub == k && src >= 0) my_e = e;
+      if (lane == src) {
+#pragma unroll
+        for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1], idx[j] = idx[j + 1];
+        key[V - 1] = 0u;
       }
     }
-    pick = __shfl_sync(kAll, pick, src) + src * V;
-    if (lane == k) my_e = pick;
+  } else {
+    uint32_t head = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) head = max(head, key[j]);
+    for (int k = 0; k < a.top_k; ++k) {
+      const uint32_t best = lanes_max<L>(head);
+      if (best == 0u) break;
+      const int src = lowest_lane<L>(head == best, lane);
+      int pick = 0;
+      if (lane == src) {
+        bool found = false;
+        head = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (!found && key[j] == best) {
+            found = true;
+            pick = j;
+            key[j] = 0u;
+          }
+          head = max(head, key[j]);
+        }
+      }
+      pick = __shfl_sync(kAll, first + pick, src);
+      if (lane == k) my_e = pick;
+    }
   }
-  // weights of the chosen, from their logits or their scores
+  // weights of the chosen, from their logits
   float w = 0.0f, xk = kNegInf;
-  if (my_e >= 0) xk = load_logit(static_cast<const T*>(a.logits) + t * E + my_e);
+  if (my_e >= 0) xk = load_logit(row + my_e);
   if constexpr (SIGMOID) {
     float c;
     if (my_e >= 0) logistic(xk, w, c);
-    if constexpr (RENORM) {
-      const float sum = warp_sum(w);
-      w = sum > 0.0f ? w / sum : 0.0f;
-    }
   } else if constexpr (RENORM) {
-    const float m = warp_max(xk);
-    if (my_e >= 0) w = exp_from(xk, m);
-    const float sum = warp_sum(w);
-    w = sum > 0.0f ? w / sum : 0.0f;
+    const float top = lanes_max<L>(xk);
+    if (my_e >= 0) w = exp_from(xk, top);
   } else {
-    // the score of expert my_e lives in lane my_e / V
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float v = __shfl_sync(kAll, s[j], my_e >= 0 ? my_e / V : 0);
-      if (my_e >= 0 && my_e % V == j) w = v;
-    }
+    if (my_e >= 0) w = exp_from(xk, m) * inv;
   }
-  if (lane < a.top_k) {
-    a.expert_idx[t * a.top_k + lane] = my_e;
-    a.weights[t * a.top_k + lane] = w * a.scale;
+  if constexpr (RENORM) {
+    const float sum = lanes_sum<L>(w);
+    w = sum > 0.0f ? w / sum : 0.0f;
+  }
+  if (live && sub < a.top_k) {
+    a.expert_idx[t * a.top_k + sub] = my_e;
+    a.weights[t * a.top_k + sub] = w * a.scale;
   }
 }
 
-// dlogits of one token per warp.  With G = dL/ds (the scores' own gradient plus the weights'):
-// softmax dx = s (G - sum s G), logistic dx = G s (1 - s).  Renormalised weights w = scale * p
-// depend on the chosen only: their part is p_k (g_k - sum_j p_j g_j), g = scale * dw, times
-// (1 - s_k) for the logistic function.
-template <typename T, int V, bool SIGMOID, bool RENORM>
+// dlogits, with the forward kernel's lanes.  With G = dL/ds (the scores' own gradient plus the
+// weights'): softmax dx = s (G - sum s G), logistic dx = G s (1 - s).  Renormalised weights
+// w = scale * p depend on the chosen only: their part is p_k (g_k - sum_j p_j g_j), g = scale *
+// dw, times (1 - s_k) for the logistic function.  The chosen experts' terms reach the lanes
+// that own them through shared memory.
+template <typename T, int V, int L, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArgs a) {
-  extern __shared__ float s_add[];  // kWarps rows of E: the chosen experts' own terms
+  __shared__ __align__(16) float s_add[kWarps][32 * V];
   const int lane = static_cast<int>(lane_id());
+  const int sub = lane % L;
   const int warp = threadIdx.x >> 5;
-  const long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  if (t >= a.T) return;
+  const long long t = (static_cast<long long>(blockIdx.x) * kWarps + warp) * (32 / L) + lane / L;
+  const bool live = t < a.T;
   const int E = a.E;
-  float* add = s_add + static_cast<size_t>(warp) * E;
-  for (int e = lane; e < E; e += 32) add[e] = 0.0f;
-  __syncwarp();
+  const int first = sub * V;
+  const bool vec = E % V == 0;
   const T* row = static_cast<const T*>(a.logits) + t * E;
-  float x[V], s[V];
-  load_row<T, V>(row, E, lane, x, a.status);
+  float x[V], s[V], add[V], G[V], m = 0.0f, inv = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) add[j] = G[j] = s[j] = 0.0f;
+  load_row<T, V>(row, E, first, live, vec, x, a.status);
+  if (a.dscores != nullptr && live) {
+    if (vec) {
+      if (first < E) load_vec<V>(a.dscores + t * E + first, G);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (first + j < E) G[j] = a.dscores[t * E + first + j];
+    }
+  }
   const bool dense = !SIGMOID && (!RENORM || a.dscores != nullptr);
-  if (dense || a.dscores != nullptr) row_scores<V, SIGMOID>(x, s);
   // the chosen experts' terms: added to G (plain softmax) or straight to dx (the others)
   if (a.dweights != nullptr) {
     int e = -1;
-    float g = 0.0f;
-    if (lane < a.top_k) {
-      e = a.expert_idx[t * a.top_k + lane];
+    float g = 0.0f, xk = kNegInf;
+    if (live && sub < a.top_k) {
+      e = a.expert_idx[t * a.top_k + sub];
       if (e < -1 || e >= E) {
         if (a.status != nullptr) atomicOr(a.status, kDevBadIndex);
         e = -1;
       }
-      if (e >= 0) g = a.dweights[t * a.top_k + lane] * a.scale;
+      if (e >= 0) {
+        g = a.dweights[t * a.top_k + sub] * a.scale;
+        xk = load_logit(row + e);
+        if (!(xk > kNegInf)) e = -1, g = 0.0f, xk = kNegInf;  // masked, or not a number
+      }
     }
-    float xk = e >= 0 ? load_logit(row + e) : kNegInf;
-    if (xk != xk) xk = kNegInf;
-    if (xk == kNegInf) e = -1, g = 0.0f;
     float term = g;
     if constexpr (RENORM) {
       float p = 0.0f, c = 1.0f;
       if constexpr (SIGMOID) {
         if (e >= 0) logistic(xk, p, c);
       } else {
-        const float m = warp_max(xk);
-        if (e >= 0) p = exp_from(xk, m);
+        const float top = lanes_max<L>(xk);
+        if (e >= 0) p = exp_from(xk, top);
       }
-      const float sum = warp_sum(p);
+      const float sum = lanes_sum<L>(p);
       p = sum > 0.0f ? p / sum : 0.0f;
-      term = p * (g - warp_sum(p * g));
+      term = p * (g - lanes_sum<L>(p * g));
       if constexpr (SIGMOID) term *= c;
     } else if constexpr (SIGMOID) {
       float p, c;
       logistic(xk, p, c);
       term = g * p * c;
     }
-    if (e >= 0) atomicAdd(&add[e], term);  // experts of a token differ: one term each
+    float* mine = s_add[warp] + lane * V;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(mine + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
+    if (e >= 0) s_add[warp][(lane - sub) * V + e] = term;  // a token's experts differ
+    __syncwarp();
+    load_vec<V>(mine, add);
   }
-  float G[V];
-  float dot = 0.0f;
+  float dx[V];
+  if constexpr (SIGMOID) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane * V + j;
-    float d = 0.0f;
-    if (e < E && x[j] != kNegInf) {
-      if (a.dscores != nullptr) d = a.dscores[t * E + e];
-      if (!SIGMOID && !RENORM) d += add[e];
+    for (int j = 0; j < V; ++j) {
+      float p = 0.0f, c = 0.0f;
+      if (a.dscores != nullptr && x[j] != kNegInf) logistic(x[j], p, c);
+      dx[j] = (x[j] != kNegInf ? G[j] * p * c : 0.0f) + add[j];
     }
-    G[j] = d;
-    if (dense) dot += s[j] * d;
-  }
-  if (dense) dot = warp_sum(dot);
+  } else {
+    float dot = 0.0f;
+    if (dense) {
+      row_scores<V, L, false>(x, s, m, inv);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane * V + j;
-    if (e >= E) continue;
-    float dx = 0.0f;
-    if constexpr (SIGMOID) {
-      if (a.dscores != nullptr) {
-        float p, c;
-        logistic(x[j], p, c);
-        dx = G[j] * p * c;
+      for (int j = 0; j < V; ++j) {
+        if (x[j] == kNegInf) G[j] = 0.0f;
+        if (!RENORM) G[j] += add[j];
+        dot += s[j] * G[j];
       }
-      dx += add[e];
-    } else {
-      if (dense) dx = s[j] * (G[j] - dot);
-      if (RENORM) dx += add[e];
+      dot = lanes_sum<L>(dot);
     }
-    store_logit(static_cast<T*>(a.dlogits) + t * E + e, dx);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      dx[j] = s[j] * (G[j] - dot);
+      if (RENORM) dx[j] += add[j];
+    }
   }
+  if (live) store_row<T, V>(static_cast<T*>(a.dlogits) + t * E, E, first, vec, dx);
 }
 
-template <typename T, int V, bool SIGMOID, bool RENORM>
-cudaError_t launch_fwd(const RouteArgs& a, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + kWarps - 1) / kWarps);
-  const size_t smem = a.groups > 1 ? sizeof(float) * kWarps * a.E : 0;
-  route_kernel<T, V, SIGMOID, RENORM><<<grid, kWarps * 32, smem, stream>>>(a);
+template <typename T, int V, int L, bool SIGMOID, bool RENORM>
+cudaError_t launch_one(const RouteArgs& a, cudaStream_t stream) {
+  constexpr int kTokens = kWarps * (32 / L);  // per CTA
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + kTokens - 1) / kTokens);
+  const size_t smem = a.groups > 1 && L == 32 ? sizeof(float) * kWarps * a.E : 0;
+  route_kernel<T, V, L, SIGMOID, RENORM><<<grid, kWarps * 32, smem, stream>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int V, bool SIGMOID, bool RENORM>
-cudaError_t launch_bwd(const RouteBwdArgs& a, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + kWarps - 1) / kWarps);
-  route_backward_kernel<T, V, SIGMOID, RENORM>
-      <<<grid, kWarps * 32, sizeof(float) * kWarps * a.E, stream>>>(a);
+template <typename T, int V, int L, bool SIGMOID, bool RENORM>
+cudaError_t launch_one(const RouteBwdArgs& a, cudaStream_t stream) {
+  constexpr int kTokens = kWarps * (32 / L);
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + kTokens - 1) / kTokens);
+  route_backward_kernel<T, V, L, SIGMOID, RENORM><<<grid, kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int V>
-cudaError_t by_mode(const RouteArgs& a, bool sigmoid, bool renorm, cudaStream_t s) {
-  if (sigmoid) return renorm ? launch_fwd<T, V, true, true>(a, s) : launch_fwd<T, V, true, false>(a, s);
-  return renorm ? launch_fwd<T, V, false, true>(a, s) : launch_fwd<T, V, false, false>(a, s);
+template <typename T, int V, int L, typename Args>
+cudaError_t by_mode(const Args& a, bool sigmoid, bool renorm, cudaStream_t s) {
+  if (sigmoid) return renorm ? launch_one<T, V, L, true, true>(a, s) : launch_one<T, V, L, true, false>(a, s);
+  return renorm ? launch_one<T, V, L, false, true>(a, s) : launch_one<T, V, L, false, false>(a, s);
 }
-template <typename T, int V>
-cudaError_t by_mode(const RouteBwdArgs& a, bool sigmoid, bool renorm, cudaStream_t s) {
-  if (sigmoid) return renorm ? launch_bwd<T, V, true, true>(a, s) : launch_bwd<T, V, true, false>(a, s);
-  return renorm ? launch_bwd<T, V, false, true>(a, s) : launch_bwd<T, V, false, false>(a, s);
+
+// Groups that are not runs of whole lanes need a warp per token.
+bool whole_lanes(const RouteBwdArgs&) { return true; }
+bool whole_lanes(const RouteArgs& a) {
+  const int per = a.E / a.groups, lanes = per / 8;
+  return a.groups == 1 || (per % 8 == 0 && (lanes & (lanes - 1)) == 0);
 }
 
 template <typename T, typename Args>
 cudaError_t by_width(const Args& a, bool sigmoid, bool renorm, cudaStream_t s) {
-  if (a.E <= 32) return by_mode<T, 1>(a, sigmoid, renorm, s);
-  if (a.E <= 64) return by_mode<T, 2>(a, sigmoid, renorm, s);
-  if (a.E <= 128) return by_mode<T, 4>(a, sigmoid, renorm, s);
-  if (a.E <= 256) return by_mode<T, 8>(a, sigmoid, renorm, s);
-  if (a.E <= 512) return by_mode<T, 16>(a, sigmoid, renorm, s);
-  return by_mode<T, 32>(a, sigmoid, renorm, s);
+  if (a.E <= 64 && a.top_k <= 8 && whole_lanes(a)) return by_mode<T, 8, 8>(a, sigmoid, renorm, s);
+  if (a.E <= 128 && a.top_k <= 16 && whole_lanes(a)) return by_mode<T, 8, 16>(a, sigmoid, renorm, s);
+  if (a.E <= 256) return by_mode<T, 8, 32>(a, sigmoid, renorm, s);
+  if (a.E <= 512) return by_mode<T, 16, 32>(a, sigmoid, renorm, s);
+  return by_mode<T, 32, 32>(a, sigmoid, renorm, s);
 }
 
 }  // namespace
