@@ -272,6 +272,8 @@ def _tables(rng, T, K, drop):
     (64, 8, 260, "f32", 0, False, False), (65, 32, 72, "bf16", 0.5, True, True),
     (5, 2, 64, "bf16", 1.0, True, True), (5, 2, 64, "bf16", 1.0, False, False),
     (0, 2, 64, "bf16", 0, False, True), (3, 5, 10000, "bf16", 0, True, True),
+    (9, 9, 1002, "bf16", 0.1, True, True), (9, 10, 2052, "bf16", 0.1, False, True), (9, 2, 4102, "f32", 0, True, True),
+    (33, 17, 515, "f32", 0.1, True, True),
 ])
 def test_combine_and_backward(T, K, H, dtype, drop, residual, weighted):
     rng = np.random.default_rng(T + K * 31 + H)
