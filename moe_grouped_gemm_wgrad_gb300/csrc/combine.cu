@@ -104,8 +104,11 @@ struct Piece {
 };
 
 // grid: (tokens, column blocks); a thread owns one piece of the token.
+// Five CTAs of 256 threads per SM: with four (57 registers) 8192 x 8 x 4096 took 121 us instead
+// of 109, with six the eight pieces spill out of flight (120 us); CTAs of 128 or 512 threads 129
+// and 119 us.
 template <typename T, int AB>
-__global__ void __launch_bounds__(kMaxThreads) combine_kernel(CombineArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 5) combine_kernel(CombineArgs a) {
   using P = Piece<T, AB>;
   __shared__ int s_row[kMaxTopK];
   __shared__ float s_w[kMaxTopK];

@@ -4,15 +4,17 @@
 //   row_of[p]      = expert_off[e(p)] + pairs of e(p) before p   (-1 for a dropped pair)
 //   row_index[r]   = p / top_k of the pair p with row_of[p] = r  (-1 past the last row)
 //
-// Every warp owns a contiguous run of pairs.  Pass 1 counts a run's experts in the warp's row
-// of shared memory; a scan over runs and experts turns the counts into every run's first row
-// per expert; pass 2 walks the run again, 32 pairs at a time, a pair's rank among equal
-// experts of the 32 coming from one warp match.  No atomics decide an order: the rows of an
-// expert are its pairs in ascending order, on every run.
+// Every warp owns a contiguous run of pairs and a row of E counters in shared memory.  32 pairs
+// at a time, ballots find the lanes of equal experts, and the last of them adds their
+// number to the counter: the old value plus the lanes before is a pair's rank in the run.  A scan
+// over the runs and over the experts then gives every run's first row per expert.  No atomic
+// decides an order: the rows of an expert are its pairs in ascending order, on every run.
 //
-// Up to kSmallPairs pairs one CTA does it all in one launch (12 bytes a pair: latency bounds
-// it).  More pairs go to `blocks` CTAs in two launches: CTA counts to the workspace, then each
-// CTA sums the counts of the CTAs before it and places its own pairs.
+// Up to four groups of 32 pairs per warp one CTA does it all in one launch.  More pairs
+// go to several CTAs in two launches: CTA counts to the workspace, then each CTA ranks its own
+// pairs, adds up the counts of the CTAs before it and stores.  12 bytes a pair are far from
+// bounding it (1M pairs: 2 us); what does is the chain of phases within a CTA, so a CTA gets few
+// pairs (up to eight groups a warp, whose experts and ranks then stay in registers).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -24,12 +26,13 @@ namespace mgw {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kSmallPairs = 8192;
-constexpr int kPairsPerBlock = 8192;
-constexpr int kMaxBlocks = 128;
+constexpr int kHeld = 8;        // groups of 32 pairs a warp keeps in registers
+constexpr int kMaxBlocks = 1024;
 
 // Warps per CTA: their E counters each share 64 KB.
-constexpr int warps_for(int E) { return E <= 512 ? 32 : 16; }
+__host__ __device__ constexpr int warps_for(int E) { return E <= 512 ? 32 : 16; }
+// Counters of a warp lie this far apart (odd: a column of them falls into different banks).
+__host__ __device__ constexpr int stride_for(int E) { return E | 1; }
 
 // The pair's expert, or -1 for a dropped one; anything else outside the range is reported.
 __device__ __forceinline__ int expert_of(const DispatchArgs& a, int p) {
@@ -41,74 +44,70 @@ __device__ __forceinline__ int expert_of(const DispatchArgs& a, int p) {
   return e;
 }
 
-// This CTA's pairs [lo, hi) and its warp's part of them (whole groups of 32 per warp).
 struct Run {
   int lo, hi;
 };
-__device__ __forceinline__ Run block_run(const DispatchArgs& a, int b, int blocks) {
-  const int per = (a.pairs / 32 + blocks) / blocks * 32;
+// The i-th of n runs of whole groups of 32 pairs within [lo, hi).
+__device__ __forceinline__ Run part(Run all, int i, int n) {
+  const int per = ((all.hi - all.lo + 31) / 32 + n - 1) / n * 32;
+  const long long lo = all.lo + static_cast<long long>(i) * per;
   Run r;
-  const long long lo = static_cast<long long>(b) * per;
-  r.lo = static_cast<int>(lo < a.pairs ? lo : a.pairs);
-  r.hi = static_cast<int>(lo + per < a.pairs ? lo + per : a.pairs);
-  return r;
-}
-__device__ __forceinline__ Run warp_run(Run b, int w, int warps) {
-  const int per = ((b.hi - b.lo + 31) / 32 + warps - 1) / warps * 32;
-  Run r;
-  const long long lo = b.lo + static_cast<long long>(w) * per;
-  r.lo = static_cast<int>(lo < b.hi ? lo : b.hi);
-  r.hi = static_cast<int>(lo + per < b.hi ? lo + per : b.hi);
+  r.lo = static_cast<int>(lo < all.hi ? lo : all.hi);
+  r.hi = static_cast<int>(lo + per < all.hi ? lo + per : all.hi);
   return r;
 }
 
-// Counts the run's experts into cnt[0 .. E), which is zero.
-__device__ __forceinline__ void count_run(const DispatchArgs& a, Run r, int* cnt) {
-  const int lane = static_cast<int>(lane_id());
-  for (int p0 = r.lo; p0 < r.hi; p0 += 32) {
-    const int p = p0 + lane;
-    const int e = p < r.hi ? expert_of(a, p) : -1;
-    if (e >= 0) atomicAdd(&cnt[e], 1);
+// The lanes whose expert equals this lane's (of those with one): a ballot per bit of an expert's
+// number.  The hardware's warp match goes through the distinct values one by one instead: with
+// it a CTA's ranking takes longer the more experts there are (1M pairs of 512: 4 us longer).
+__device__ __forceinline__ unsigned equal_lanes(int e, int bits) {
+  unsigned same = __ballot_sync(kAll, e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (e >> b) & 1;
+    const unsigned with = __ballot_sync(kAll, one);
+    same &= one ? with : ~with;
   }
+  return e >= 0 ? same : 1u << lane_id();
 }
 
-// Places the run's pairs; next[e] is the run's next row of expert e.
-__device__ __forceinline__ void place_run(const DispatchArgs& a, Run r, int* next) {
+// Adds the group's experts to the counters; returns the lane's rank among the run's pairs of its
+// expert (old counter value plus equal lanes before it).
+__device__ __forceinline__ int rank_group(int e, int bits, int* cnt) {
   const int lane = static_cast<int>(lane_id());
-  for (int p0 = r.lo; p0 < r.hi; p0 += 32) {
-    const int p = p0 + lane;
-    const bool in = p < r.hi;
-    int e = in ? a.expert_idx[p] : -1;
-    if (e >= a.E) e = -1;
-    const unsigned same = __match_any_sync(kAll, e);
-    int row = -1;
-    if (e >= 0) row = next[e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == 31 - __clz(same)) next[e] = row + 1;
-    __syncwarp();
-    if (in) a.row_of[p] = row;
-    if (row >= 0) a.row_index[row] = p / a.top_k;
+  const unsigned same = equal_lanes(e, bits);
+  const int last = 31 - __clz(same);
+  int old = 0;
+  if (e >= 0 && lane == last) {
+    old = cnt[e];
+    cnt[e] = old + __popc(same);
   }
+  __syncwarp();
+  old = __shfl_sync(kAll, old, last);
+  return old + __popc(same & ((1u << lane) - 1u));
 }
 
-// Turns per-warp counts [warps][E] into first rows: row of (w, e) = base[e] + counts of e in
-// the warps below w.  Returns e's total over the warps.
-__device__ __forceinline__ int scan_warps(int* cnt, int warps, int E, int e, int base) {
-  int run = base;
-  for (int w = 0; w < warps; ++w) {
-    const int c = cnt[w * E + e];
-    cnt[w * E + e] = run;
-    run += c;
+// Turns column e of the counters [warps][stride] into exclusive sums over the warps, one warp
+// per column, lane w the w-th counter; the total comes back in every lane.
+__device__ __forceinline__ int scan_column(int* cnt, int warps, int stride, int e) {
+  const int lane = static_cast<int>(lane_id());
+  const int c = lane < warps ? cnt[lane * stride + e] : 0;
+  int v = c;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kAll, v, d);
+    if (lane >= d) v += y;
   }
-  return run - base;
+  if (lane < warps) cnt[lane * stride + e] = v - c;
+  return __shfl_sync(kAll, v, 31);
 }
 
-// Exclusive scan of s[0 .. E) in place by one warp, s[E] = the total.
-__device__ __forceinline__ void warp_scan(int* s, int E) {
-  const int lane = static_cast<int>(lane_id());
-  int carry = 0;
-  for (int base = 0; base < E; base += 32) {
-    const int e = base + lane;
+// Exclusive scan of s[0 .. E) in place by the block, s[E] = the total; s_seg holds 32 ints.
+// Ends with a barrier.
+__device__ __forceinline__ void block_scan(int* s, int E, int* s_seg) {
+  const int lane = static_cast<int>(lane_id()), warps = blockDim.x >> 5;
+  const int segs = (E + 31) / 32;  // of 32 experts, at most 32
+  for (int g = threadIdx.x >> 5; g < segs; g += warps) {
+    const int e = 32 * g + lane;
     const int c = e < E ? s[e] : 0;
     int v = c;
 #pragma unroll
@@ -116,115 +115,188 @@ __device__ __forceinline__ void warp_scan(int* s, int E) {
       const int y = __shfl_up_sync(kAll, v, d);
       if (lane >= d) v += y;
     }
-    if (e < E) s[e] = carry + v - c;
-    carry += __shfl_sync(kAll, v, 31);
+    if (e < E) s[e] = v - c;
+    if (lane == 31) s_seg[g] = v;
   }
-  if (lane == 0) s[E] = carry;
+  __syncthreads();
+  for (int g = threadIdx.x >> 5; g < segs; g += warps) {
+    const int before = __reduce_add_sync(kAll, lane < g ? s_seg[lane] : 0);
+    const int e = 32 * g + lane;
+    if (e < E) s[e] += before;
+    if (g == segs - 1 && lane == 0) s[E] = before + s_seg[g];
+  }
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(1024) dispatch_small_kernel(DispatchArgs a) {
-  extern __shared__ int s_cnt[];  // [warps][E], then the E + 1 offsets
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
-  int* s_off = s_cnt + warps * a.E;
-  for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) s_cnt[i] = 0;
-  __syncthreads();
-  const Run b{0, a.pairs};
-  const Run r = warp_run(b, warp, warps);
-  count_run(a, r, s_cnt + warp * a.E);
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_off[e] = scan_warps(s_cnt, warps, a.E, e, 0);
-  __syncthreads();
-  if (warp == 0) warp_scan(s_off, a.E);
-  __syncthreads();
-  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_off[e] = s_off[e];
-  for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) s_cnt[i] += s_off[i % a.E];
-  for (int i = s_off[a.E] + threadIdx.x; i < a.pairs; i += blockDim.x) a.row_index[i] = -1;
-  __syncthreads();
-  place_run(a, r, s_cnt + warp * a.E);
-}
-
+// This CTA's pair counts per expert.
 __global__ void __launch_bounds__(1024) dispatch_count_kernel(DispatchArgs a) {
   extern __shared__ int s_cnt[];  // [E]
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warps = blockDim.x >> 5, lane = static_cast<int>(lane_id());
+  const int bits = 32 - __clz(a.E - 1);
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) s_cnt[i] = 0;
   __syncthreads();
-  count_run(a, warp_run(block_run(a, blockIdx.x, gridDim.x), warp, warps), s_cnt);
+  const Run r = part(part(Run{0, a.pairs}, blockIdx.x, gridDim.x), threadIdx.x >> 5, warps);
+  for (int p0 = r.lo; p0 < r.hi; p0 += 32 * kHeld) {
+    int e[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int p = p0 + 32 * i + lane;
+      e[i] = p < r.hi ? expert_of(a, p) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const unsigned same = equal_lanes(e[i], bits);
+      if (e[i] >= 0 && lane == 31 - __clz(same)) atomicAdd(&s_cnt[e[i]], __popc(same));
+    }
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x)
     a.counts[static_cast<size_t>(blockIdx.x) * a.E + e] = s_cnt[e];
 }
 
+// Ranks and places this CTA's pairs.  ONE: the only CTA, whose counts are the totals.  HELD: a
+// warp's run is at most kHeld groups.
+template <bool ONE, bool HELD>
 __global__ void __launch_bounds__(1024) dispatch_place_kernel(DispatchArgs a) {
-  extern __shared__ int s_cnt[];  // [warps][E], the E + 1 offsets, this CTA's first rows [E]
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
-  int* s_off = s_cnt + warps * a.E;
-  int* s_base = s_off + a.E + 1;
-  for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) s_cnt[i] = 0;
-  // totals over all CTAs, and over the CTAs before this one
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    int before = 0, all = 0;
-    for (unsigned b = 0; b < gridDim.x; ++b) {
-      const int c = a.counts[static_cast<size_t>(b) * a.E + e];
-      all += c;
-      if (b < blockIdx.x) before += c;
+  extern __shared__ int s_cnt[];  // counters [warps][stride], expert offsets [E + 1], first rows [E]
+  __shared__ int s_seg[32];
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id());
+  const int stride = stride_for(a.E), bits = 32 - __clz(a.E - 1);
+  int* s_off = s_cnt + warps * stride;
+  int* s_first = s_off + a.E + 1;
+  int* mine = s_cnt + warp * stride;
+  for (int i = threadIdx.x; i < warps * stride; i += blockDim.x) s_cnt[i] = 0;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_off[e] = s_first[e] = 0;
+  const Run r = part(part(Run{0, a.pairs}, blockIdx.x, gridDim.x), warp, warps);
+  int ex[kHeld], rank[kHeld];
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int p = r.lo + 32 * i + lane;
+      ex[i] = p < r.hi ? expert_of(a, p) : -1;
     }
-    s_off[e] = all;
-    s_base[e] = before;
   }
   __syncthreads();
-  const Run r = warp_run(block_run(a, blockIdx.x, gridDim.x), warp, warps);
-  count_run(a, r, s_cnt + warp * a.E);
-  if (warp == 0) {
-    __syncwarp();
-    warp_scan(s_off, a.E);
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (r.lo + 32 * i < r.hi) rank[i] = rank_group(ex[i], bits, mine);
+  } else {
+    for (int p0 = r.lo; p0 < r.hi; p0 += 32)
+      (void)rank_group(p0 + lane < r.hi ? expert_of(a, p0 + lane) : -1, bits, mine);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-    (void)scan_warps(s_cnt, warps, a.E, e, s_off[e] + s_base[e]);
+  for (int e = warp; e < a.E; e += warps) {
+    const int total = scan_column(s_cnt, warps, stride, e);
+    if (ONE && lane == 0) s_off[e] = total;
+  }
+  if constexpr (!ONE) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the counting launch has finished
+    // Totals over all CTAs, and over the CTAs before this one: every thread adds up a share of
+    // one expert's column (integer sums, whose order does not matter).
+    const int blocks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+    const int parts = max(static_cast<int>(blockDim.x) / a.E, 1);
+    for (int i = threadIdx.x; i < parts * a.E; i += blockDim.x) {
+      const int e = i % a.E;
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int b = i / a.E; b < blocks; b += parts) {
+        const int c = a.counts[static_cast<size_t>(b) * a.E + e];
+        all += c;
+        before += b < me ? c : 0;
+      }
+      atomicAdd(&s_off[e], all);
+      atomicAdd(&s_first[e], before);
+    }
+  }
+  __syncthreads();
+  block_scan(s_off, a.E, s_seg);
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_first[e] += s_off[e];
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_off[e] = s_off[e];
   for (long long i = s_off[a.E] + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.pairs;
        i += static_cast<long long>(gridDim.x) * blockDim.x)
     a.row_index[i] = -1;
   __syncthreads();
-  place_run(a, r, s_cnt + warp * a.E);
+  // the token p / top_k of this lane's pair, carried along from group to group of 32
+  int token = (r.lo + lane) / a.top_k, slot = (r.lo + lane) % a.top_k;
+  const int tokens32 = 32 / a.top_k, slots32 = 32 % a.top_k;
+  auto place = [&](int p, int e, int row) {
+    if (p < r.hi) a.row_of[p] = e >= 0 ? row : -1;
+    if (e >= 0) a.row_index[row] = token;
+    token += tokens32;
+    slot += slots32;
+    if (slot >= a.top_k) slot -= a.top_k, ++token;
+  };
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (r.lo + 32 * i < r.hi) {
+        const int e = ex[i];
+        place(r.lo + 32 * i + lane, e, e >= 0 ? s_first[e] + mine[e] + rank[i] : -1);
+      }
+    }
+  } else {
+    // the counters now hold the run's first rows: ranking again gives the rows
+    for (int p0 = r.lo; p0 < r.hi; p0 += 32) {
+      int e = p0 + lane < r.hi ? a.expert_idx[p0 + lane] : -1;
+      if (e >= a.E || e < 0) e = -1;
+      const int rank = rank_group(e, bits, mine);
+      place(p0 + lane, e, e >= 0 ? s_first[e] + rank : -1);
+    }
+  }
 }
 
 size_t place_smem_bytes(int E) {
-  return sizeof(int) * (static_cast<size_t>(warps_for(E)) * E + 2 * static_cast<size_t>(E) + 1);
+  return sizeof(int) * (static_cast<size_t>(warps_for(E)) * stride_for(E) + 2 * static_cast<size_t>(E) + 1);
+}
+
+template <bool ONE, bool HELD>
+cudaError_t launch_place(const DispatchArgs& a, int blocks, cudaStream_t stream) {
+  static thread_local uint64_t attr_ctx = 0;
+  const size_t max_smem = place_smem_bytes(512) > place_smem_bytes(kMaxExperts) ? place_smem_bytes(512)
+                                                                                : place_smem_bytes(kMaxExperts);
+  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(dispatch_place_kernel<ONE, HELD>),
+                                             max_smem, &attr_ctx);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps_for(a.E)));
+  cfg.dynamicSmemBytes = place_smem_bytes(a.E);
+  cfg.stream = stream;
+  // After a counting launch, the placing one starts while that runs (programmatic dependent
+  // launch): it ranks its own pairs, and waits before it reads the table or writes anything.
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = ONE ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, dispatch_place_kernel<ONE, HELD>, a);
 }
 
 }  // namespace
 
 int dispatch_blocks(long long pairs, int E) {
-  (void)E;
-  if (pairs <= kSmallPairs) return 1;
-  const long long b = (pairs + kPairsPerBlock - 1) / kPairsPerBlock;
+  const long long group = 32 * warps_for(E);  // pairs of one group per warp
+  if (pairs <= 4 * group) return 1;
+  // one, two, four or eight groups a warp while that keeps the CTAs to the device's size
+  for (int g = 1; g < kHeld; g *= 2)
+    if (pairs <= 128 * g * group) return static_cast<int>((pairs + g * group - 1) / (g * group));
+  const long long b = (pairs + kHeld * group - 1) / (kHeld * group);
   return static_cast<int>(b < kMaxBlocks ? b : kMaxBlocks);
 }
 
 cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t stream) {
   const int blocks = dispatch_blocks(a.pairs, a.E);
+  if (blocks == 1) return launch_place<true, true>(a, 1, stream);
   const int threads = 32 * warps_for(a.E);
-  const size_t smem = place_smem_bytes(a.E);
-  static thread_local uint64_t attr_small = 0, attr_place = 0;
-  const size_t max_smem = place_smem_bytes(512) > place_smem_bytes(kMaxExperts) ? place_smem_bytes(512)
-                                                                                : place_smem_bytes(kMaxExperts);
-  if (blocks == 1) {
-    const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(dispatch_small_kernel),
-                                               max_smem, &attr_small);
-    if (err != cudaSuccess) return err;
-    dispatch_small_kernel<<<1, threads, smem, stream>>>(a);
-    return cudaGetLastError();
-  }
-  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(dispatch_place_kernel),
-                                             max_smem, &attr_place);
-  if (err != cudaSuccess) return err;
   dispatch_count_kernel<<<blocks, threads, sizeof(int) * a.E, stream>>>(a);
-  const cudaError_t e1 = cudaGetLastError();
-  if (e1 != cudaSuccess) return e1;
-  dispatch_place_kernel<<<blocks, threads, smem, stream>>>(a);
-  return cudaGetLastError();
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const long long groups = (static_cast<long long>(a.pairs) + 31) / 32;
+  const bool held = (groups + blocks - 1) / blocks <= static_cast<long long>(kHeld) * warps_for(a.E);
+  return held ? launch_place<false, true>(a, blocks, stream) : launch_place<false, false>(a, blocks, stream);
 }
 
 }  // namespace mgw

@@ -226,7 +226,8 @@ def test_route_backward_bad_expert_is_reported():
     (0, 2, 4, 0, 0), (1, 1, 1, 0, 0), (1, 8, 64, 0, 0), (31, 1, 7, 0, 0), (33, 3, 5, 0.2, 0),
     (16, 8, 64, 0, 0), (1000, 2, 1024, 0, 0), (1024, 8, 64, 0, 1), (1025, 8, 64, 0.05, 1),
     (4096, 8, 512, 0, 0), (30000, 7, 600, 0.3, 1), (131071, 8, 64, 0, 1), (50000, 3, 2, 1.0, 0),
-    (200000, 6, 3, 0, 0), (8192, 1, 1, 0, 0), (8193, 1, 1000, 0, 0),
+    (200000, 6, 3, 0, 0), (8192, 1, 1, 0, 0), (8193, 1, 1000, 0, 0), (4096, 1, 512, 0, 0), (4097, 1, 512, 0, 1),
+    (1100000, 4, 40, 0.01, 1), (1100001, 3, 1024, 0, 0),
 ])
 def test_dispatch(T, K, E, drop, skew):
     rng = np.random.default_rng(T + K + E)
@@ -273,7 +274,7 @@ def _tables(rng, T, K, drop):
     (5, 2, 64, "bf16", 1.0, True, True), (5, 2, 64, "bf16", 1.0, False, False),
     (0, 2, 64, "bf16", 0, False, True), (3, 5, 10000, "bf16", 0, True, True),
     (9, 9, 1002, "bf16", 0.1, True, True), (9, 10, 2052, "bf16", 0.1, False, True), (9, 2, 4102, "f32", 0, True, True),
-    (33, 17, 515, "f32", 0.1, True, True),
+    (33, 17, 515, "f32", 0.1, True, True), (5000, 3, 264, "bf16", 0.1, True, True),
 ])
 def test_combine_and_backward(T, K, H, dtype, drop, residual, weighted):
     rng = np.random.default_rng(T + K * 31 + H)
