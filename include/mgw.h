@@ -432,7 +432,7 @@ mgw_status mgw_grouped_fprop_mxfp8_act(const void *xq, const void *xs, const voi
  * dy.)
  * dy_bf16    device, bf16 [M, F].
  * z_bf16     device, bf16 [M, N]; null for MGW_ACT_NONE.
- * N          a positive multiple of 128 (of 256 for the gated activations).
+ * N          a positive multiple of 128 (of 256 for the gated activations), at most 2^20.
  * dz_bf16    device, bf16 [M, N], fully written; null for MGW_ACT_NONE (dz is dy).
  * dbias      device fp32 [E, N], nullable.  The sum's order is fixed by the sizes.
  * workspace  device, 16-byte aligned, mgw_grouped_act_backward_workspace_bytes bytes when dbias

@@ -767,7 +767,7 @@ mgw_status mgw_grouped_act_backward(const void* dy_bf16, const void* z_bf16,
   if (M < 0 || N <= 0 || E < 1 || E > MGW_MAX_EXPERTS) return MGW_ERR_INVALID_ARG;
   if (act < MGW_ACT_NONE || act > MGW_ACT_GEGLU) return MGW_ERR_INVALID_ARG;
   if (M > 0 && act != MGW_ACT_NONE && (!z_bf16 || !dz_bf16)) return MGW_ERR_INVALID_ARG;
-  if (N % (gated(act) ? 256 : 128) != 0 || N > (1 << 23)) return MGW_ERR_UNSUPPORTED;
+  if (N % (gated(act) ? 256 : 128) != 0 || N > (1 << 20)) return MGW_ERR_UNSUPPORTED;
   // rows on the padded axis are counted in 32 bits
   if (mgw_mxfp8_token_capacity(M, E) >= (size_t(1) << 31)) return MGW_ERR_UNSUPPORTED;
   if (!aligned16(dy_bf16) || !aligned16(z_bf16) || !aligned16(dz_bf16) ||

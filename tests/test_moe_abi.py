@@ -84,7 +84,7 @@ def test_act_backward_refusals(lib):
     assert _call(fn, base, N=192) == -2
     assert _call(fn, base, N=128, act=4) == -2
     need = lib.mgw_grouped_act_backward_workspace_bytes(2, 300, 256)
-    assert need == (300 // 128 + 2) * 256 * 4
+    assert need >= (2 + 2) * 256 * 4   # a row of sums per row tile of either expert
     assert _call(fn, base, db=OK, ws=OK, n=need - 1) == -3
     assert lib.mgw_grouped_act_backward_workspace_bytes(0, 300, 256) == 0
 
