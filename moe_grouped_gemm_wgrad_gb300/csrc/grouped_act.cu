@@ -23,10 +23,13 @@
 // Roles (576 threads per CTA):
 //   warp 0       TMA producer (both CTAs): weight rows, half of the routed rows, scale atoms.
 //   warp 1       MMA issuer (even CTA).
-//   warps 2-9    epilogue: two warps per TMEM lane quarter, taking 16-column groups in turn.
-//   warps 10-17  scale writers: warps 10-13 the even stages, 14-17 the odd ones, one TMEM lane
-//                quarter each.  They place the stage's scale words in TMEM, which is what lets
-//                a tile start at any multiple of 16 rows and the gate / up rows interleave.
+//   warps 2-13   epilogue: three warps per TMEM lane quarter, taking 16-column groups in turn.
+//                A group is a chain of waits (TMEM, staging tile, stores), so the number of
+//                warps counts: with two per quarter 32768 rows of SwiGLU with residual and saved
+//                pre-activation took 152 us, with three NN.
+//   warps 14-17  scale writers, one TMEM lane quarter each: they place the stage's scale words
+//                in TMEM, which is what lets a tile start at any multiple of 16 rows and the
+//                gate / up rows interleave.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -52,16 +55,17 @@ constexpr int kOffBar = kOffSf + kStages * kSfStage;
 // full[], empty[], sf_full[], acc_full[2], acc_empty[2], done
 constexpr int kNumBars = 3 * kStages + 5;
 constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) & ~15;
-constexpr int kEpiWarps = 8;
-// Per epilogue warp: 16 rows of y and of z by 32 features in bf16, rows 80 bytes apart so that
-// the 8 rows of a matrix meet 8 different bank groups (gated: three tiles of 16 features, 48
-// bytes apart).
-constexpr int kTurnBytes = 2 * 16 * 80;
-static_assert(3 * 16 * 48 <= kTurnBytes, "gated staging tiles");
+constexpr int kEpiParts = 3;  // epilogue warps per TMEM lane quarter
+constexpr int kEpiWarps = 4 * kEpiParts;
+// Per epilogue warp: a staging tile of 16 rows by 32 features in bf16, rows 80 bytes apart so
+// that the 8 rows of a matrix meet 8 different bank groups (gated: two of 16 features, 48 bytes
+// apart).
+constexpr int kTurnBytes = 2 * 16 * 48;
+static_assert(16 * 80 <= kTurnBytes, "staging tile");
 constexpr int kOffTurn = kOffMisc + 16;
 constexpr int kOffTable = kOffTurn + kEpiWarps * kTurnBytes;
-constexpr int kSfWarp0 = 10;
-constexpr int kThreads = 18 * 32;
+constexpr int kSfWarp0 = 2 + kEpiWarps;
+constexpr int kThreads = (kSfWarp0 + 4) * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 2 * kW;
 static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
@@ -465,7 +469,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // tcgen05.mma reads the scale of operand row j from lane j % 32, column j / 32 of every
     // lane quarter, one byte per 32-element block.
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
-    const uint32_t parity = static_cast<uint32_t>(warp - kSfWarp0) >> 2;  // this warp's stages
     const uint32_t full0_leader = map_to_cta(bar_full(0), 0);
     int stage = 0;
     uint32_t phase = 0;
@@ -480,10 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool by1 = shift & 1u, by2 = shift & 2u, by4 = shift & 4u;
       for (int c = 0; c < nch; ++c) {
         const int st = stage;
-        const uint32_t ph = phase;
-        if (++stage == kStages) stage = 0, phase ^= 1u;
-        if ((st & 1) != static_cast<int>(parity)) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_sf_full(st), ph, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_sf_full(st), phase, abort_flag))) {
           ok = false;
           break;
         }
@@ -517,6 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(full0_leader + 8u * st);
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
     }
     if (!ok && lane == 0) abort_both();
@@ -524,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int ew = warp - 2;
     const int quarter = warp & 3;  // TMEM lanes this warp may access
-    const int part = ew >> 2;      // even or odd 16-column groups
+    const int part = ew >> 2;      // every kEpiParts-th 16-column group
     const uint32_t acc_empty0 = map_to_cta(bar_acc_empty(0), 0);
     const uint32_t tile = sbase + kOffTurn + static_cast<uint32_t>(ew) * kTurnBytes;
     constexpr int kCh = kGated ? 2 : 4;  // 16-byte chunks of y per row and warp
@@ -564,10 +565,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint4 rv[kCh / 2];
       if (res != nullptr && part * 16 < x.nrows)
         Turn<kCh>::load(res, static_cast<size_t>(x.row0) + 16 * part, F, col, x.nrows - 16 * part, rv);
-      for (int g = part; g * 16 < x.nrows; g += 2) {
+      for (int g = part; g * 16 < x.nrows; g += kEpiParts) {
         const int left = x.nrows - 16 * g;  // rows of this group that exist
         const size_t row = static_cast<size_t>(x.row0) + 16 * g;
-        const bool more = (g + 2) * 16 < x.nrows;
+        const bool more = (g + kEpiParts) * 16 < x.nrows;
         tmem_wait_ld_regs(r);
         // z[h][b][j]: lane 16 h + 8 (j / 2) + lane_id / 4, row 8 b + 2 (lane_id % 4) + j % 2
         float z[2][2][4];
@@ -578,14 +579,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[h][b][j] = __uint_as_float(r[8 * h + 4 * b + j]) + bias[h][j >> 1];
         if (more) {
-          tmem_ld_16x256b_x2(ta + 16u * (g + 2), r);
-          tmem_ld_16x256b_x2(ta + (16u << 16) + 16u * (g + 2), r + 8);
+          tmem_ld_16x256b_x2(ta + 16u * (g + kEpiParts), r);
+          tmem_ld_16x256b_x2(ta + (16u << 16) + 16u * (g + kEpiParts), r + 8);
         }
-        uint32_t f[8];
-        __syncwarp();  // the previous group has left the staging tiles
+        uint32_t f[8], rf[8];
+        __syncwarp();  // the previous group has left the staging tile
         if (res != nullptr) {
           Turn<kCh>::fill(tile, rv);
-          if (more) Turn<kCh>::load(res, row + 32, F, col, left - 32, rv);
+          if (more) Turn<kCh>::load(res, row + 16 * kEpiParts, F, col, left - 16 * kEpiParts, rv);
+          __syncwarp();
+          Turn<kCh>::get(tile, rf);
+          __syncwarp();
         }
         if (zout != nullptr) {
           if constexpr (kGated) {
@@ -595,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) f[2 * b + i] = pack_bf16(z[h][b][2 * i], z[h][b][2 * i + 1]);
-              Turn<2>::put(tile + (1 + h) * 768, f);
+              Turn<2>::put(tile + h * 768, f);
             }
           } else {
 #pragma unroll
@@ -603,7 +607,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 f[4 * b + i] = pack_bf16(z[i >> 1][b][2 * (i & 1)], z[i >> 1][b][2 * (i & 1) + 1]);
-            Turn<4>::put(tile + 1280, f);
+            Turn<4>::put(tile, f);
+          }
+          __syncwarp();
+          if constexpr (kGated) {
+            Turn<2>::store(tile, zout, row, N, col, left);
+            Turn<2>::store(tile + 768, zout, row, N, col + F, left);
+          } else {
+            Turn<4>::store(tile, zout, row, N, col, left);
           }
         }
         // y in z's place: [0][b][j] when gated
@@ -617,14 +628,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if constexpr (kGated) z[h][b][j] *= z[1][b][j];
             }
         if (res != nullptr) {
-          __syncwarp();  // the residual is in the tile
-          Turn<kCh>::get(tile, f);
-          __syncwarp();
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < kCh; ++i) {
-              const float2 v = unpack_bf16(f[kCh * b + i]);
+              const float2 v = unpack_bf16(rf[kCh * b + i]);
               z[i >> 1][b][2 * (i & 1)] += v.x;
               z[i >> 1][b][2 * (i & 1) + 1] += v.y;
             }
@@ -634,17 +642,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kCh; ++i)
             f[kCh * b + i] = pack_bf16(z[i >> 1][b][2 * (i & 1)], z[i >> 1][b][2 * (i & 1) + 1]);
+        __syncwarp();  // z has left the tile
         Turn<kCh>::put(tile, f);
         __syncwarp();
         Turn<kCh>::store(tile, y, row, F, col, left);
-        if (zout != nullptr) {
-          if constexpr (kGated) {
-            Turn<2>::store(tile + 768, zout, row, N, col, left);
-            Turn<2>::store(tile + 1536, zout, row, N, col + F, left);
-          } else {
-            Turn<4>::store(tile + 1280, zout, row, N, col, left);
-          }
-        }
       }
       tc_fence_before();
       __syncwarp();
