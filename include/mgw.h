@@ -436,12 +436,12 @@ mgw_status mgw_grouped_fprop_mxfp8_act(const void *xq, const void *xs, const voi
  * dz_bf16    device, bf16 [M, N], fully written; null for MGW_ACT_NONE (dz is dy).
  * dbias      device fp32 [E, N], nullable.  The sum's order is fixed by the sizes.
  * workspace  device, 16-byte aligned, mgw_grouped_act_backward_workspace_bytes bytes when dbias
- *            is given; need not be initialised. */
+ *            is given; need not be initialised, null when that is 0. */
 mgw_status mgw_grouped_act_backward(const void *dy_bf16, const void *z_bf16,
                                     const int32_t *expert_off, int E, int M, int N, int act,
                                     void *dz_bf16, float *dbias, void *workspace,
                                     size_t workspace_bytes, int *status_dev, void *stream);
-/* Host only; 0 for invalid sizes. */
+/* Host only; 0 for small calls and for invalid sizes. */
 size_t mgw_grouped_act_backward_workspace_bytes(int E, int M, int N);
 
 /* mgw_moe_combine -- routed rows back to token order:

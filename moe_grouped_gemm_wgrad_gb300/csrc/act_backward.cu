@@ -9,7 +9,8 @@
 // a time, 104 us so (tiles of 64 or 32 rows: no gain at any size).
 // With dbias the warps' sums meet in shared memory and go to the workspace, one row of sums
 // per tile; a second launch adds every expert's tiles in order, so dbias does not vary between
-// runs.  dbias sums dz before it is rounded to bf16.  HBM bounds it: z, dy and dz once each.
+// runs.  Up to kWholeRows rows in all, a CTA takes a whole expert instead and stores its dbias
+// itself: one launch and no workspace (a launch costs more than the few rows do).  dbias sums dz before it is rounded to bf16.  HBM bounds it: z, dy and dz once each.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -23,6 +24,7 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a tile
 constexpr int kCols = 256;   // columns per CTA: 32 lanes x 8
+constexpr int kWholeRows = 512;
 constexpr int kWarps = 8;
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
@@ -57,7 +59,8 @@ __device__ __forceinline__ int locate(int i, const int* first, int E) {
 
 // Columns are those of dy: F = N, or N / 2 when gated (then each lane has a gate and an up
 // column).  Tiles are counted on the 128-padded row axis.
-template <int ACT>
+// WHOLE: blockIdx.x is an expert, not a row tile.
+template <int ACT, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32) act_backward_kernel(ActBwdArgs a) {
   constexpr bool kGated = act_gated(ACT);
   constexpr int kInner = act_inner(ACT);
@@ -69,10 +72,16 @@ __global__ void __launch_bounds__(kWarps * 32) act_backward_kernel(ActBwdArgs a)
   int* s_pad = s_tab + a.E + 1;
   if (!load_offsets(a.expert_off, a.E, a.M, s_off, s_pad, &s_flag, a.status)) return;
   const int tile = blockIdx.x;
-  if (tile >= s_pad[a.E] / kRows) return;
-  const int e = locate(tile * kRows, s_pad, a.E);
-  const int first = tile * kRows - s_pad[e];
-  const int rows = min(kRows, s_off[e + 1] - s_off[e] - first);
+  int e, first = 0, rows;
+  if constexpr (WHOLE) {
+    e = tile;
+    rows = s_off[e + 1] - s_off[e];
+  } else {
+    if (tile >= s_pad[a.E] / kRows) return;
+    e = locate(tile * kRows, s_pad, a.E);
+    first = tile * kRows - s_pad[e];
+    rows = min(kRows, s_off[e + 1] - s_off[e] - first);
+  }
   const long long row0 = s_off[e] + first;
   const int warp = threadIdx.x >> 5;
   const int F = kGated ? a.N / 2 : a.N;
@@ -143,7 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32) act_backward_kernel(ActBwdArgs a)
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v += s_sum[w][threadIdx.x];
-      a.partial[static_cast<size_t>(tile) * a.N + s * F + col] = v;
+      (WHOLE ? a.dbias + static_cast<size_t>(e) * a.N : a.partial + static_cast<size_t>(tile) * a.N)[s * F + col] = v;
     }
   }
 }
@@ -187,10 +196,15 @@ template <int ACT>
 cudaError_t launch(const ActBwdArgs& a, cudaStream_t stream) {
   const int F = act_gated(ACT) ? a.N / 2 : a.N;
   const size_t smem = sizeof(int) * 2 * (static_cast<size_t>(a.E) + 1);
+  if (a.M <= kWholeRows && a.dbias != nullptr) {
+    const dim3 grid(static_cast<unsigned>(a.E), static_cast<unsigned>((F + kCols - 1) / kCols));
+    act_backward_kernel<ACT, true><<<grid, kWarps * 32, smem, stream>>>(a);
+    return cudaGetLastError();
+  }
   const long long experts = a.M < a.E ? a.M : a.E;
   const long long tiles = a.M / kRows + experts;
   const dim3 grid(static_cast<unsigned>(tiles > 0 ? tiles : 1), static_cast<unsigned>((F + kCols - 1) / kCols));
-  act_backward_kernel<ACT><<<grid, kWarps * 32, smem, stream>>>(a);
+  act_backward_kernel<ACT, false><<<grid, kWarps * 32, smem, stream>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || a.dbias == nullptr) return err;
   cudaLaunchConfig_t cfg = {};
@@ -206,6 +220,13 @@ cudaError_t launch(const ActBwdArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+size_t act_backward_workspace_bytes(int E, int M, int N) {
+  if (M <= kWholeRows) return 0;
+  // one row of sums per 128-row tile of an expert
+  const size_t tiles = static_cast<size_t>(M) / kRows + static_cast<size_t>(M < E ? M : E);
+  return sizeof(float) * tiles * static_cast<size_t>(N);
+}
 
 cudaError_t launch_act_backward(const ActBwdArgs& a, int act, cudaStream_t stream) {
   switch (act) {

@@ -754,9 +754,7 @@ mgw_status mgw_grouped_fprop_mxfp8_act(const void* xq, const void* xs, const voi
 
 size_t mgw_grouped_act_backward_workspace_bytes(int E, int M, int N) {
   if (E < 1 || E > MGW_MAX_EXPERTS || M < 0 || N <= 0) return 0;
-  // one row of sums per 128-row tile of an expert
-  const size_t tiles = static_cast<size_t>(M) / 128 + static_cast<size_t>(M < E ? M : E);
-  return sizeof(float) * tiles * static_cast<size_t>(N);
+  return mgw::act_backward_workspace_bytes(E, M, N);
 }
 
 mgw_status mgw_grouped_act_backward(const void* dy_bf16, const void* z_bf16,

@@ -136,6 +136,7 @@ struct ActBwdArgs {
   int E, M, N;
   int* status;
 };
+size_t act_backward_workspace_bytes(int E, int M, int N);
 cudaError_t launch_act_backward(const ActBwdArgs& a, int act, cudaStream_t stream);
 
 // Router (route.cu).  top_k <= 32 (one selected expert per lane), groups <= 32.

@@ -272,11 +272,11 @@ def _one_device(*ts) -> torch.device:
 
 def _out(t: torch.Tensor | None, shape, dtype, dev, name: str) -> torch.Tensor:
     """The caller's output buffer after checks, or a new one of ``shape``."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     n = 1
     for d in shape:
         n *= int(d)
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
     _dev_tensor(t, dtype, name)
     _need(t, n, name)
     return t
@@ -664,8 +664,8 @@ def grouped_fprop_mxfp8_act(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor
     Mw, K_w = wq.shape
     if K_w != K:
         raise MgwError(f"wq [Mw, {K_w}] and xq [Mcap, {K}] must share the contraction width")
-    _need(xs, scale_bytes(K, Mcap), "xs")
-    _need(ws, scale_bytes(K, Mw), "ws")
+    _need(xs, K * Mcap // 32, "xs")
+    _need(ws, K * Mw // 32, "ws")
     M, N, act = int(M), int(N), int(act)
     F = N // 2 if act in GATED_ACTS else N
     if bias is not None:
@@ -691,7 +691,7 @@ def grouped_act_backward(dy: torch.Tensor, z: torch.Tensor | None, expert_off: t
     """-> (dz bf16 [M, N], dbias fp32 [E, N] or None): the backward pass of
     :func:`grouped_fprop_mxfp8_act`'s epilogue from dy [M, F] bf16 and the saved pre-activation
     z [M, N] bf16.  For ACT_NONE z is None and dz is dy itself.  ``workspace`` (uint8) is
-    allocated when dbias is asked for and none is given."""
+    allocated when a large call with dbias needs one and none is given."""
     act = int(act)
     _dev_tensor(dy, torch.bfloat16, "dy", 2)
     M, F = dy.shape
@@ -712,7 +712,8 @@ def grouped_act_backward(dy: torch.Tensor, z: torch.Tensor | None, expert_off: t
     if with_dbias or dbias is not None:
         dbias = _out(dbias, (E, N), torch.float32, dev, "dbias")
         need = int(lib.mgw_grouped_act_backward_workspace_bytes(E, M, N))
-        workspace = _out(workspace, (need,), torch.uint8, dev, "workspace")
+        if need or workspace is not None:
+            workspace = _out(workspace, (need,), torch.uint8, dev, "workspace")
     with _device(dev):
         st = lib.mgw_grouped_act_backward(_ptr(dy), _ptr(z), _ptr(expert_off), E, M, N, act,
                                           _ptr(dz), _ptr(dbias), _ptr(workspace),

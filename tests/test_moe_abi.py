@@ -74,7 +74,7 @@ def test_fprop_act_refusals(lib):
 
 
 def test_act_backward_refusals(lib):
-    base = dict(dy=OK, z=OK, off=OK, E=2, M=300, N=256, act=2, dz=OK, db=None, ws=None, n=0, status=None,
+    base = dict(dy=OK, z=OK, off=OK, E=2, M=3000, N=256, act=2, dz=OK, db=None, ws=None, n=0, status=None,
                 stream=None)
     fn = lib.mgw_grouped_act_backward
     for bad in (dict(dy=None), dict(z=None), dict(off=None), dict(dz=None), dict(E=0), dict(E=1025),
@@ -83,10 +83,10 @@ def test_act_backward_refusals(lib):
         assert _call(fn, base, **bad) == -1, bad
     assert _call(fn, base, N=192) == -2
     assert _call(fn, base, N=128, act=4) == -2
-    need = lib.mgw_grouped_act_backward_workspace_bytes(2, 300, 256)
-    assert need >= (2 + 2) * 256 * 4   # a row of sums per row tile of either expert
+    need = lib.mgw_grouped_act_backward_workspace_bytes(2, 3000, 256)
+    assert need >= (23 + 2) * 256 * 4   # a row of sums per row tile of either expert
     assert _call(fn, base, db=OK, ws=OK, n=need - 1) == -3
-    assert lib.mgw_grouped_act_backward_workspace_bytes(0, 300, 256) == 0
+    assert lib.mgw_grouped_act_backward_workspace_bytes(0, 3000, 256) == 0
 
 
 def test_combine_refusals(lib):
