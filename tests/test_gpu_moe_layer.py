@@ -1,0 +1,67 @@
+"""The example layer (examples/moe_ffn.py), which runs every routed-layer operator together,
+against autograd on the same parameters in fp32.
+
+Tolerance: e4m3 keeps three mantissa bits, a relative rounding error of about 2.6% rms, so a
+product of two quantized operands is off by 3.7% of its rms, and two chained products with
+what they pass on by 5 to 8%; every tensor is held to 12% of its rms over all elements.  The
+router's choice is compared exactly (both see the same fp32 logits)."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def moe_ffn():
+    spec = importlib.util.spec_from_file_location("moe_ffn", os.path.join(ROOT, "examples", "moe_ffn.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def _rms_error(got, want):
+    return float((got.float() - want).square().mean().sqrt() / want.square().mean().sqrt())
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn,experts,top_k", [(300, 512, 256, 8, 2), (1, 256, 256, 4, 4),
+                                                             (777, 256, 512, 32, 6)])
+def test_layer_matches_autograd(moe_ffn, tokens, hidden, ffn, experts, top_k):
+    layer = moe_ffn.MoeFfn(hidden, ffn, experts, top_k, seed=tokens)
+    layer.b1.normal_(std=0.3)
+    layer.b2.normal_(std=0.3)
+    x = torch.randn(tokens, hidden, device="cuda").bfloat16()
+    dout = torch.randn(tokens, hidden, device="cuda").bfloat16()
+    out = layer.forward(x)
+    dx, grads = layer.backward(dout)
+    assert int(layer.status.item()) == 0
+
+    p = {k: v.clone().requires_grad_() for k, v in layer.parameters().items()}
+    xr = x.float().requires_grad_()
+    logits = xr @ p["router"].t()
+    idx = layer.saved[2].long()
+    assert torch.equal(idx, torch.topk(layer.saved[1], top_k).indices)
+    w = torch.softmax(logits.gather(1, idx), 1)
+    want = xr
+    for e in range(experts):
+        t, k = (idx == e).nonzero(as_tuple=True)
+        if t.numel() == 0:
+            continue
+        z = xr[t] @ p["w1"][e].t() + p["b1"][e]
+        h = torch.nn.functional.silu(z[:, :ffn]) * z[:, ffn:]
+        y = h @ p["w2"][e].t() + p["b2"][e]
+        want = want.index_add(0, t, w[t, k].unsqueeze(1) * y)
+    want.backward(dout.float())
+    assert _rms_error(out, want.detach()) < 0.12
+    assert _rms_error(dx, xr.grad) < 0.12
+    for name, v in p.items():
+        assert _rms_error(grads[name], v.grad) < 0.12, name
+
+
+def test_training_reduces_the_loss(moe_ffn):
+    losses = moe_ffn.train(steps=12, tokens=1024)
+    assert all(b < a for a, b in zip(losses, losses[1:]))
+    assert losses[-1] < 0.9 * losses[0]
