@@ -49,12 +49,17 @@ __device__ __forceinline__ float logistic_fast(float x) {
   return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
 }
 
+// x Phi(x) = max(x, 0) - |x| h, with |x| bounded so that an infinite x meets h = 0 as a number.
+__device__ __forceinline__ float gelu_from_tail(float x, float h) {
+  return fmaf(-fminf(fabsf(x), 1e30f), h, fmaxf(x, 0.0f));
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
-  if constexpr (ACT == kActRelu) return fmaxf(x, 0.0f);
+  if constexpr (ACT == kActRelu) return x <= 0.0f ? 0.0f : x;  // NaN stays NaN
   if constexpr (ACT == kActGelu) {
     float e;
-    return fmaf(-fabsf(x), normal_tail(x, e), fmaxf(x, 0.0f));  // x Phi(x) = max(x, 0) - |x| h
+    return gelu_from_tail(x, normal_tail(x, e));
   }
   if constexpr (ACT == kActSilu) return x * logistic_fast(x);
   return x;
@@ -64,12 +69,12 @@ __device__ __forceinline__ float act_value(float x) {
 template <int ACT>
 __device__ __forceinline__ void act_value_slope(float x, float& value, float& slope) {
   if constexpr (ACT == kActRelu) {
-    value = fmaxf(x, 0.0f);
+    value = x <= 0.0f ? 0.0f : x;
     slope = x > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActGelu) {
     float e;
     const float h = normal_tail(x, e);
-    value = fmaf(-fabsf(x), h, fmaxf(x, 0.0f));
+    value = gelu_from_tail(x, h);
     slope = fmaf(0.3989422804014327f * x, e, x >= 0.0f ? 1.0f - h : h);  // Phi(x) + x phi(x)
   } else if constexpr (ACT == kActSilu) {
     const float s = logistic_fast(x);

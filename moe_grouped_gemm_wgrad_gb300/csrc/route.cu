@@ -101,10 +101,13 @@ __device__ __forceinline__ float lanes_max(float v) {
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  if constexpr (L == 32) return __reduce_max_sync(kAll, v);
+  if constexpr (L == 32) {
+    return __reduce_max_sync(kAll, v);
+  } else {
 #pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+    for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  }
 }
 // The lowest of the token's lanes for which p holds, or -1.
 template <int L>

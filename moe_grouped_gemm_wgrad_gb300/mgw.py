@@ -543,6 +543,15 @@ def _shaped(t: torch.Tensor, shape, dtype, name: str) -> None:
         raise MgwError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _used_on(stream, *ts) -> None:
+    """Tells the allocator that tensors of the current stream's pool are in use on ``stream``,
+    so that their memory is not handed out again before that stream's work on them is done."""
+    if stream is not None:
+        for t in ts:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+
+
 def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None,
               score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,
               group_best: int = 1, renorm: bool = True, scale: float = 1.0,
@@ -577,6 +586,7 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
                                   float(scale), _ptr(expert_idx), _ptr(weights), _ptr(scores),
                                   _ptr(status), _stream(stream))
     _check(st, "mgw_moe_route")
+    _used_on(stream, expert_idx, weights, scores)
     return (expert_idx, weights) if scores is None else (expert_idx, weights, scores)
 
 
@@ -607,6 +617,7 @@ def moe_route_backward(logits: torch.Tensor, expert_idx: torch.Tensor,
                                            _ptr(dweights), _ptr(dscores), _ptr(dlogits),
                                            _ptr(status), _stream(stream))
     _check(st, "mgw_moe_route_backward")
+    _used_on(stream, dlogits)
     return dlogits
 
 
@@ -641,6 +652,7 @@ def moe_dispatch(expert_idx: torch.Tensor, E: int, expert_off: torch.Tensor | No
                                   0 if workspace is None else workspace.numel(), _ptr(status),
                                   _stream(stream))
     _check(st, "mgw_moe_dispatch")
+    _used_on(stream, expert_off, row_index, row_of, workspace)
     return expert_off, row_index, row_of
 
 
@@ -681,6 +693,7 @@ def grouped_fprop_mxfp8_act(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor
             _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(expert_off), E, M, N, K, Mcap, Mw, act,
             _ptr(bias), _ptr(residual), _ptr(out), _ptr(preact), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_fprop_mxfp8_act")
+    _used_on(stream, out, preact)
     return out if preact is None else (out, preact)
 
 
@@ -720,6 +733,7 @@ def grouped_act_backward(dy: torch.Tensor, z: torch.Tensor | None, expert_off: t
                                           0 if workspace is None else workspace.numel(),
                                           _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_act_backward")
+    _used_on(stream, dz, dbias, workspace)
     return (dy if act == ACT_NONE else dz), dbias
 
 
@@ -745,6 +759,7 @@ def moe_combine(y: torch.Tensor, row_of: torch.Tensor, weights: torch.Tensor | N
         st = load().mgw_moe_combine(_ptr(y), dt, M, _ptr(row_of), _ptr(weights), _ptr(residual), T,
                                     top_k, H, _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_moe_combine")
+    _used_on(stream, out)
     return out
 
 
@@ -785,4 +800,5 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: tor
                                              _ptr(weights), T, top_k, H, _ptr(dy), _ptr(dweights),
                                              _ptr(status), _stream(stream))
     _check(st, "mgw_moe_combine_backward")
+    _used_on(stream, dy, dweights)
     return dy, dweights

@@ -518,3 +518,41 @@ def test_operators_can_be_captured_in_a_graph():
     _, _, row2 = mgw.moe_dispatch(idx2, E)
     assert torch.equal(idx, idx2) and torch.equal(row_of, row2)
     assert torch.equal(out, mgw.moe_combine(y, row2, weights=w2))
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu", "swiglu", "geglu"])
+def test_special_values_through_the_epilogue(act):
+    """z = bias alone (x is zero): infinities and NaN come out as the activation defines them."""
+    inf, nan = float("inf"), float("nan")
+    N, F = 256, 128 if act in GATED else 256
+    off = dev_i32([0, 3])
+    ops = (torch.zeros(256, 128, dtype=torch.uint8, device="cuda"),
+           torch.full((1024,), 127, dtype=torch.uint8, device="cuda"),
+           torch.zeros(384, 128, dtype=torch.uint8, device="cuda"),
+           torch.full((1536,), 127, dtype=torch.uint8, device="cuda"), off)
+    bias = torch.ones(1, N, device="cuda")
+    bias[0, :7] = torch.tensor([inf, -1e30, 1e30, nan, 0.0, -0.0, -100.0])
+    y = mgw.grouped_fprop_mxfp8_act(*ops, 3, N, ACT[act], bias=bias).float().cpu()
+    assert (torch.equal(y[0], y[1]) or torch.equal(y[0].isnan(), y[1].isnan())) and y.shape == (3, F)
+    assert y[0, 0] == inf and y[0, 1] == 0 and y[0, 2] > 9e29 and torch.isnan(y[0, 3])
+    assert y[0, 4] == 0 and y[0, 5] == 0 and abs(float(y[0, 6])) < 1e-30
+    assert torch.isfinite(y[:, 7:]).all()
+
+
+def test_side_stream_allocations_are_kept():
+    """Outputs and workspaces allocated by a call on another stream are not reused before that
+    stream is done: many short-lived results while a long queue runs on the side stream."""
+    side = torch.cuda.Stream()
+    idx = torch.randint(0, 32, (20000, 8), device="cuda", dtype=torch.int32)
+    want = mgw.moe_dispatch(idx, 32)
+    torch.cuda.synchronize()
+    busy = torch.randn(4096, 4096, device="cuda")
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = busy @ busy * 1e-2
+    got = [mgw.moe_dispatch(idx, 32, stream=side) for _ in range(4)]
+    for _ in range(8):   # the current stream writes over whatever the allocator hands out
+        torch.full((1 << 18,), -77, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
