@@ -142,6 +142,7 @@ cudaError_t launch_act_backward(const ActBwdArgs& a, int act, cudaStream_t strea
 // Router (route.cu).  top_k <= 32 (one selected expert per lane), groups <= 32.
 constexpr int kMaxTopK = 32;
 constexpr int kMaxGroups = 32;
+constexpr int kDevBadLogit = 16;  // device status bit: a router logit that is not a number
 struct RouteArgs {
   const void* logits;  // [T, E] bf16 or fp32
   const float* bias;   // [E] or null
