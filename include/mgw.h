@@ -1,5 +1,5 @@
 /*
- * mgw -- grouped MoE backward GEMMs for NVIDIA GB300 (sm_103a).
+ * mgw -- grouped MoE GEMMs, and the routed layer around them, for NVIDIA GB300 (sm_103a).
  *
  * C ABI of libmgw.so.  Every entry point takes plain device pointers, sizes and
  * a CUDA stream handle; nothing here depends on PyTorch.  All device work is
