@@ -62,6 +62,10 @@ constexpr int kEpiWarps = 4 * kEpiParts;
 // apart).
 constexpr int kTurnBytes = 2 * 16 * 48;
 static_assert(16 * 80 <= kTurnBytes, "staging tile");
+// Most rows of an item whose contraction is split over the pairs of a cluster, and most pairs.
+constexpr int kSplitRows = 64;
+constexpr int kMaxSplit = 4;
+static_assert((kMaxSplit - 1) * (kSplitRows / 16) * 4 * 2048 <= kStages * kStageBytes, "partial accumulators");
 constexpr int kOffTurn = kOffMisc + 16;
 constexpr int kOffTable = kOffTurn + kEpiWarps * kTurnBytes;
 constexpr int kSfWarp0 = 2 + kEpiWarps;
@@ -142,6 +146,11 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
                : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -247,9 +256,11 @@ __device__ __forceinline__ Item decode(int it, int tiles_f, const int* s_off, co
   return x;
 }
 
-template <int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_act_kernel(const __grid_constant__ ActMmArgs args) {
+// S > 1: few items of few rows.  A cluster of S pairs takes one item, pair j the j-th part of the
+// contraction; the other pairs' accumulators go to the first pair's ring, which is idle by then,
+// and are added there in pair order.
+template <int ACT, int S>
+__global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_constant__ ActMmArgs args) {
   constexpr bool kGated = act_gated(ACT);
   constexpr int kInner = act_inner(ACT);
   extern __shared__ uint8_t smem_raw[];
@@ -267,7 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // their TMA and tcgen05 instructions take.
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t lane = lane_id();
-  const uint32_t rank = cluster_ctarank();  // 0: issues the pair MMAs
+  const uint32_t cta = cluster_ctarank();
+  const uint32_t rank = cta & 1u;   // in the pair; 0 issues the pair MMAs
+  const uint32_t even = cta & ~1u;  // the pair's even CTA
   const bool leader = rank == 0;
 
   if (tid == 0) s_misc[1] = 0;
@@ -320,10 +333,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // both CTAs' barriers are initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(__shfl_sync(0xffffffffu, s_misc[0], 0));
-  const uint32_t peer_abort = map_to_cta(smem_u32(&s_misc[1]), rank ^ 1u);
   auto abort_both = [&]() {
     *abort_flag = 1;
-    st_cluster_u32(peer_abort, 1u);
+    for (uint32_t i = 0; i < 2 * S; ++i)
+      if (i != cta) st_cluster_u32(map_to_cta(smem_u32(&s_misc[1]), i), 1u);
     if (args.status) atomicOr(args.status, kDevTimeout);
   };
 
@@ -332,8 +345,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tiles_f = N / 256;
   const int nch = args.K / BL;
   const int total = __shfl_sync(0xffffffffu, s_tile[E], 0) * tiles_f;  // < 2^31: the C ABI checks the sizes
-  const int npairs = static_cast<int>(gridDim.x >> 1);
-  const int pair = static_cast<int>(blockIdx.x >> 1);
+  // first item and step to the next one; with S > 1 a cluster has one item at most
+  const int pair = static_cast<int>(blockIdx.x) / (2 * S);
+  const int npairs = S > 1 ? 1 << 30 : static_cast<int>(gridDim.x >> 1);
+  // this pair's chunks of the contraction
+  const int split = static_cast<int>(cta >> 1);
+  const int c0 = nch * split / S, c1 = nch * (split + 1) / S;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -344,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     uint32_t chunks = 0;
     bool ok = true;
-    const uint32_t full0_leader = map_to_cta(bar_full(0), 0);
+    const uint32_t full0_leader = map_to_cta(bar_full(0), even);
     const long long a_tiles = args.Mw / 128;   // 128-row tiles of the weights' scale layout
     const long long b_tiles = args.Mcap / 128;
     for (int it = pair; it < total && ok; it += npairs) {
@@ -363,10 +380,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t xbytes = tall ? kBBytes : static_cast<uint32_t>(boxes) * 16 * BL;
       const int xt0 = x.p0 / 128;
       const uint32_t sfb_bytes = static_cast<uint32_t>((x.p0 + x.width - 1) / 128 - xt0 + 1) * 512;
-      const uint8_t* wsf = args.ws + static_cast<size_t>(wrow / 128) * 512;
-      const uint8_t* wsf_up = args.ws + static_cast<size_t>((wrow + F) / 128) * 512;
-      const uint8_t* xsf = args.xs + static_cast<size_t>(xt0) * 512;
-      for (int c = 0; c < nch; ++c) {
+      const uint8_t* wsf = args.ws + (c0 * a_tiles + wrow / 128) * 512;
+      const uint8_t* wsf_up = args.ws + (c0 * a_tiles + (wrow + F) / 128) * 512;
+      const uint8_t* xsf = args.xs + (c0 * b_tiles + xt0) * 512;
+      for (int c = c0; c < c1; ++c) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag))) {
           ok = false;
           break;
@@ -419,7 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true;
-      constexpr uint16_t kBoth = 0x3;
+      const uint16_t both = static_cast<uint16_t>(0x3u << even);
       const uint64_t a_desc0 = sdesc_kmajor_sw128(sbase);
       for (int it = pair; it < total && ok; it += npairs) {
         const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
@@ -432,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++n;
         const uint32_t d = tmem + static_cast<uint32_t>(buf * kW);
         const uint32_t idesc = idesc_mxf8_e4m3(256, x.width, 0, 0);
-        for (int c = 0; c < nch; ++c) {
+        for (int c = c0; c < c1; ++c) {
           // operands in both CTAs' shared memory, scale factors in both CTAs' TMEM
           if (!__all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag))) {
             ok = false;
@@ -446,20 +463,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (uint32_t kb = 0; kb < 4; ++kb)
               mma_mxf8_block32_pair(d, ad + 2 * kb, bd + 2 * kb, idesc | (kb << 4) | (kb << 29), tsf,
-                                    tsf + 8, (c | static_cast<int>(kb)) != 0);
-            mma_commit_pair(bar_empty(stage), kBoth);
+                                    tsf + 8, (c - c0) != 0 || kb != 0);
+            mma_commit_pair(bar_empty(stage), both);
           }
           __syncwarp();
           if (++stage == kStages) stage = 0, phase ^= 1u;
         }
         if (!ok) break;
-        if (issue) mma_commit_pair(bar_acc_full(buf), kBoth);
+        if (issue) mma_commit_pair(bar_acc_full(buf), both);
         __syncwarp();
       }
       if (!ok && lane == 0) abort_both();
       // All MMAs issued by this warp's lane complete before TMEM is released.
       if (issue) {
-        mma_commit_pair(bar_done, 0x1);
+        mma_commit_pair(bar_done, static_cast<uint16_t>(0x1u << even));
         mbar_wait_drain(bar_done, 0);
       }
       __syncwarp();
@@ -469,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // tcgen05.mma reads the scale of operand row j from lane j % 32, column j / 32 of every
     // lane quarter, one byte per 32-element block.
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
-    const uint32_t full0_leader = map_to_cta(bar_full(0), 0);
+    const uint32_t full0_leader = map_to_cta(bar_full(0), even);
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -481,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t start = static_cast<uint32_t>(x.p0 & 127) + lane;
       const uint32_t r0 = start & 31u, shift = start >> 5;
       const bool by1 = shift & 1u, by2 = shift & 2u, by4 = shift & 4u;
-      for (int c = 0; c < nch; ++c) {
+      for (int c = c0; c < c1; ++c) {
         const int st = stage;
         if (!__all_sync(0xffffffffu, mbar_wait(bar_sf_full(st), phase, abort_flag))) {
           ok = false;
@@ -526,14 +543,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int ew = warp - 2;
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     const int part = ew >> 2;      // every kEpiParts-th 16-column group
-    const uint32_t acc_empty0 = map_to_cta(bar_acc_empty(0), 0);
+    const uint32_t acc_empty0 = map_to_cta(bar_acc_empty(0), even);
     const uint32_t tile = sbase + kOffTurn + static_cast<uint32_t>(ew) * kTurnBytes;
     constexpr int kCh = kGated ? 2 : 4;  // 16-byte chunks of y per row and warp
     const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(args.residual);
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(args.y);
     __nv_bfloat16* zout = static_cast<__nv_bfloat16*>(args.z);
+    // Partial accumulators in the ring: 2 KB per (pair, 16-column group, lane quarter).
+    auto partial_at = [&](int j, int g) {
+      return sbase + static_cast<uint32_t>(((j - 1) * (kSplitRows / 16) + g) * 4 + quarter) * 2048u + lane * 16u;
+    };
+    if constexpr (S > 1) {
+      bool send = false;
+      Item x;
+      if (pair < total) {
+        x = decode(pair, tiles_f, s_off, s_pad, s_tile, E);
+        send = x.nrows > 0 && split > 0 &&
+               __all_sync(0xffffffffu, mbar_wait(bar_acc_full(0), 0, abort_flag));
+        if (x.nrows > 0 && split > 0 && !send && lane == 0) abort_both();
+      }
+      tc_fence_after();
+      cluster_sync();  // every pair's MMAs have ended: the first pair's ring is free
+      if (send) {
+        for (int g = part; g * 16 < x.nrows; g += kEpiParts) {
+          uint32_t r[16];
+          tmem_ld_16x256b_x2(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 16u * g, r);
+          tmem_ld_16x256b_x2(tmem + (static_cast<uint32_t>(quarter * 32 + 16) << 16) + 16u * g, r + 8);
+          tmem_wait_ld_regs(r);
+          const uint32_t to = map_to_cta(partial_at(split, g), rank);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_cluster_v4(to + 512u * i, r + 4 * i);
+        }
+      }
+      cluster_sync();  // the partial accumulators are there
+    }
     int n = 0;
-    for (int it = pair; it < total; it += npairs) {
+    for (int it = pair; it < total && split == 0; it += npairs) {
       const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
       if (x.nrows == 0) continue;
       // the warp's first column of y; of z too (gated: gate columns, up columns F further)
@@ -577,7 +622,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[h][b][j] = __uint_as_float(r[8 * h + 4 * b + j]) + bias[h][j >> 1];
+            for (int j = 0; j < 4; ++j) {
+              z[h][b][j] = __uint_as_float(r[8 * h + 4 * b + j]);
+              if constexpr (S == 1) z[h][b][j] += bias[h][j >> 1];
+            }
+        if constexpr (S > 1) {
+#pragma unroll
+          for (int k = 1; k < S; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = ld_shared_v4(partial_at(k, g) + 512u * i);
+              z[i >> 1][i & 1][0] += __uint_as_float(v.x);
+              z[i >> 1][i & 1][1] += __uint_as_float(v.y);
+              z[i >> 1][i & 1][2] += __uint_as_float(v.z);
+              z[i >> 1][i & 1][3] += __uint_as_float(v.w);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[i >> 1][i & 1][j] += bias[i >> 1][j >> 1];
+        }
         if (more) {
           tmem_ld_16x256b_x2(ta + 16u * (g + kEpiParts), r);
           tmem_ld_16x256b_x2(ta + (16u << 16) + 16u * (g + kEpiParts), r + 8);
@@ -653,6 +717,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (S > 1) {
+    if (warp < 2 || warp >= kSfWarp0) {  // the epilogue's two barriers
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no pair MMA reads this CTA's shared memory or writes its TMEM any more
@@ -660,20 +731,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-template <int ACT>
-cudaError_t launch(const ActMmArgs& a, int num_sms, cudaStream_t stream) {
+template <int ACT, int S>
+cudaError_t launch_split(const ActMmArgs& a, long long clusters, cudaStream_t stream) {
   static thread_local uint64_t attr_ctx = 0;
-  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(grouped_act_kernel<ACT>),
+  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(grouped_act_kernel<ACT, S>),
                                              act_smem_bytes(kMaxExperts), &attr_ctx);
   if (err != cudaSuccess) return err;
-  // At most one pair per item; the exact number of row tiles is known on the device only.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = act_smem_bytes(a.E);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2 * S;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, grouped_act_kernel<ACT, S>, a);
+}
+
+template <int ACT>
+cudaError_t launch(const ActMmArgs& a, int num_sms, cudaStream_t stream) {
+  // The exact number of row tiles is known on the device only.
   const long long experts = a.M < a.E ? a.M : a.E;
-  const long long total = (static_cast<long long>(a.M) / kW + experts) * (a.N / 256);
-  long long pairs = num_sms / 2;
-  if (pairs > total) pairs = total;
-  if (pairs < 1) pairs = 1;
-  grouped_act_kernel<ACT><<<static_cast<unsigned>(2 * pairs), kThreads, act_smem_bytes(a.E), stream>>>(a);
-  return cudaGetLastError();
+  long long items = (static_cast<long long>(a.M) / kW + experts) * (a.N / 256);
+  if (items < 1) items = 1;
+  // Few rows and items: split the contraction over clusters of four or two pairs, as long as
+  // these run at once (the device takes 15 clusters of 8 CTAs or 36 of 4; a 16th cluster of 8
+  // waits for a whole one and costs 9 us).  16 rows of one expert, launch included: 1024 x 16384
+  // 36 us with one pair an item, 26 with two, 20 with four; 1024 x 4096 18, 16 and 15 us.
+  const int nch = a.K / BL;
+  if (a.M <= kSplitRows && nch >= 8 && items * 8 <= num_sms * 4 / 5) return launch_split<ACT, 4>(a, items, stream);
+  if (a.M <= kSplitRows && nch >= 4 && items * 4 <= num_sms * 15 / 16) return launch_split<ACT, 2>(a, items, stream);
+  const long long pairs = items < num_sms / 2 ? items : num_sms / 2;  // at most one per item
+  return launch_split<ACT, 1>(a, pairs, stream);
 }
 
 }  // namespace

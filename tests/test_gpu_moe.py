@@ -227,7 +227,7 @@ def test_route_backward_bad_expert_is_reported():
     (16, 8, 64, 0, 0), (1000, 2, 1024, 0, 0), (1024, 8, 64, 0, 1), (1025, 8, 64, 0.05, 1),
     (4096, 8, 512, 0, 0), (30000, 7, 600, 0.3, 1), (131071, 8, 64, 0, 1), (50000, 3, 2, 1.0, 0),
     (200000, 6, 3, 0, 0), (8192, 1, 1, 0, 0), (8193, 1, 1000, 0, 0), (4096, 1, 512, 0, 0), (4097, 1, 512, 0, 1),
-    (1100000, 4, 40, 0.01, 1), (1100001, 3, 1024, 0, 0),
+    (1100000, 4, 40, 0.01, 1), (1100001, 3, 1024, 0, 0), (1100000, 8, 40, 0.01, 1),
 ])
 def test_dispatch(T, K, E, drop, skew):
     rng = np.random.default_rng(T + K + E)
@@ -380,6 +380,16 @@ def _operands(rng, counts, N, K):
     ([5, 300, 0, 0, 64, 111, 2, 1], 512, 128, "gelu", False, False, False),
     ([0, 0], 256, 128, "swiglu", True, False, True),
     ([1, 1, 1, 1] * 10, 256, 256, "geglu", True, False, False),
+    # few rows and items: the contraction is split over a cluster's pairs
+    ([1], 256, 1024, "none", False, False, False),
+    ([64], 512, 1152, "gelu", True, True, True),
+    ([16], 4096, 1024, "swiglu", True, True, True),
+    ([0, 33, 0, 31], 256, 2048, "silu", True, True, True),
+    ([17, 1, 15, 0, 0, 20], 512, 640, "geglu", True, False, True),
+    ([2, 3, 4, 5, 6, 7, 8, 9], 768, 512, "relu", False, True, True),
+    ([48], 1024, 4096, "swiglu", False, False, False),
+    ([65], 256, 1024, "gelu", True, True, True),
+    ([0, 0, 0], 256, 1024, "gelu", True, False, True),
 ])
 def test_fprop_act(counts, N, K, act, bias, residual, save):
     rng = np.random.default_rng(sum(counts) + N + K)
@@ -415,16 +425,25 @@ def test_fprop_act_matches_the_plain_product():
     assert np.all(np.abs(f64(a) - f64(b)) <= 2.0 ** -7 * np.abs(z) + 1e-4)
 
 
-def test_fprop_act_bad_offsets_leave_outputs_alone():
+def test_fprop_act_split_is_repeatable():
+    rng = np.random.default_rng(13)
+    ops, off, _ = _operands(rng, [40], 512, 2048)
+    first = mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), 40, 512, mgw.ACT_SWIGLU)
+    for _ in range(5):
+        assert torch.equal(first, mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), 40, 512, mgw.ACT_SWIGLU))
+
+
+@pytest.mark.parametrize("K", [128, 1024])
+def test_fprop_act_bad_offsets_leave_outputs_alone(K):
     rng = np.random.default_rng(12)
-    ops, off, _ = _operands(rng, [30, 40], 256, 128)
-    for bad in ([0, 50, 40], [1, 30, 70], [0, 30, 69]):
+    ops, off, _ = _operands(rng, [20, 30], 256, K)
+    for bad in ([0, 50, 40], [1, 30, 50], [0, 30, 49]):
         st = status()
-        out = torch.full((70, 256), 5.0, dtype=torch.bfloat16, device="cuda")
-        mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(bad), 70, 256, out=out, status=st)
+        out = torch.full((50, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+        mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(bad), 50, 256, out=out, status=st)
         assert st.item() == mgw.MGW_DEV_BAD_OFFSETS and (out == 5).all()
         st = status()
-        dz = torch.full((70, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+        dz = torch.full((50, 256), 5.0, dtype=torch.bfloat16, device="cuda")
         db = torch.full((2, 256), 5.0, device="cuda")
         mgw.grouped_act_backward(out, out, dev_i32(bad), mgw.ACT_RELU, dz=dz, dbias=db, status=st)
         assert st.item() == mgw.MGW_DEV_BAD_OFFSETS and (dz == 5).all() and (db == 5).all()
