@@ -26,7 +26,7 @@
 //   warps 2-13   epilogue: three warps per TMEM lane quarter, taking 16-column groups in turn.
 //                A group is a chain of waits (TMEM, staging tile, stores), so the number of
 //                warps counts: with two per quarter 32768 rows of SwiGLU with residual and saved
-//                pre-activation took 152 us, with three NN.
+//                pre-activation took 152 us, with three 138, with four no less.
 //   warps 14-17  scale writers, one TMEM lane quarter each: they place the stage's scale words
 //                in TMEM, which is what lets a tile start at any multiple of 16 rows and the
 //                gate / up rows interleave.

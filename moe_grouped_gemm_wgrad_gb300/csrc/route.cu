@@ -12,14 +12,18 @@
 // l V + V - 1, so of equal values the lowest lane's is the lowest index.  Up to 256 experts
 // take V = 8 (one or two 16-byte loads) and L = 8, 16 or 32: four, two or one token per warp.
 // A lane sorts its eight keys once; each of the top_k rounds is then a maximum over the token's
-// lanes, one ballot, and a shift of the winning lane's list.  Beyond 256 experts a lane keeps
-// its 16 or 32 keys unsorted and looks through them when it wins.  The work is instruction
-// issue, not bytes: at 65536 x 64 (softmax, top 8) a whole warp per token with two experts a
-// lane took 30 us, this layout 18 us, launch included, against 2 us of reading and writing.  The renormalised
+// lanes, one ballot, and a shift of the winning lane's list.  Beyond 256 experts a lane keeps its
+// 16 or 32 keys unsorted and looks through them when it wins.  bf16 logits without a bias fit
+// one 32-bit key with their index below them: no ballot, no second list.  The renormalised
 // softmax needs the chosen logits only; sums are fp32.
+//
+// The work is instruction issue and latency, not bytes.  65536 x 64 (softmax, top 8, graph
+// replay with its launch): 30 us with a warp per token and two experts a lane, 17.5 with this
+// layout, 15.5 with one-word keys; reading and writing it takes 2.
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -214,6 +218,53 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[V], int (&idx)[V]) {
   swap(1, 2), swap(3, 4), swap(5, 6);
 }
 
+// The same network for keys that differ, each carrying its index.
+__device__ __forceinline__ void sort_packed(uint32_t (&key)[8]) {
+  auto swap = [&](int a, int b) {
+    const uint32_t hi = max(key[a], key[b]), lo = min(key[a], key[b]);
+    key[a] = hi;
+    key[b] = lo;
+  };
+  swap(0, 1), swap(2, 3), swap(4, 5), swap(6, 7);
+  swap(0, 2), swap(1, 3), swap(4, 6), swap(5, 7);
+  swap(1, 2), swap(5, 6);
+  swap(0, 4), swap(1, 5), swap(2, 6), swap(3, 7);
+  swap(2, 4), swap(3, 5);
+  swap(1, 2), swap(3, 4), swap(5, 6);
+}
+
+// The token's top_k best of keys that each hold a 16-bit value above 65535 - its index; lane k
+// of the token gets the k-th.
+template <int V, int L>
+__device__ __forceinline__ int pick_packed(uint32_t (&key)[V], int top_k, int sub) {
+  int my_e = -1;
+  if constexpr (V == 8) sort_packed(key);
+  uint32_t head = key[0];
+  if constexpr (V != 8) {
+#pragma unroll
+    for (int j = 1; j < V; ++j) head = max(head, key[j]);
+  }
+  for (int k = 0; k < top_k; ++k) {
+    const uint32_t best = lanes_max<L>(head);
+    if (sub == k && best != 0u) my_e = 65535 - static_cast<int>(best & 65535u);
+    const bool won = head == best;
+    if constexpr (V == 8) {
+#pragma unroll
+      for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
+      key[V - 1] = won ? 0u : key[V - 1];
+      head = key[0];
+    } else if (won) {
+      head = 0u;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (key[j] == best) key[j] = 0u;
+        head = max(head, key[j]);
+      }
+    }
+  }
+  return my_e;
+}
+
 template <typename T, int V, int L, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
   extern __shared__ float s_vals[];  // groups that are not whole lanes: kWarps rows of E values
@@ -314,7 +365,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
   }
   // lane k of the token keeps its k-th choice (top_k <= L)
   int my_e = -1;
-  if constexpr (V == 8) {
+  if (std::is_same<T, __nv_bfloat16>::value && a.bias == nullptr) {
+    // a bf16 value is the upper half of its fp32 key
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      key[j] = key[j] == 0u ? 0u : (key[j] & 0xffff0000u) | static_cast<uint32_t>(65535 - (first + j));
+    my_e = pick_packed<V, L>(key, a.top_k, sub);
+  } else if constexpr (V == 8) {
     int idx[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) idx[j] = j;
@@ -395,6 +452,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   const int first = sub * V;
   const bool vec = E % V == 0;
   const T* row = static_cast<const T*>(a.logits) + t * E;
+  // the chosen experts first: their logits' addresses depend on them
+  int e = -1;
+  float g = 0.0f, xk = kNegInf;
+  if (a.dweights != nullptr && live && sub < a.top_k) {
+    e = a.expert_idx[t * a.top_k + sub];
+    g = a.dweights[t * a.top_k + sub] * a.scale;
+  }
   float x[V], s[V], add[V], G[V], m = 0.0f, inv = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) add[j] = G[j] = s[j] = 0.0f;
@@ -411,20 +475,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   const bool dense = !SIGMOID && (!RENORM || a.dscores != nullptr);
   // the chosen experts' terms: added to G (plain softmax) or straight to dx (the others)
   if (a.dweights != nullptr) {
-    int e = -1;
-    float g = 0.0f, xk = kNegInf;
-    if (live && sub < a.top_k) {
-      e = a.expert_idx[t * a.top_k + sub];
-      if (e < -1 || e >= E) {
-        if (a.status != nullptr) atomicOr(a.status, kDevBadIndex);
-        e = -1;
-      }
-      if (e >= 0) {
-        g = a.dweights[t * a.top_k + sub] * a.scale;
-        xk = load_logit(row + e);
-        if (!(xk > kNegInf)) e = -1, g = 0.0f, xk = kNegInf;  // masked, or not a number
-      }
+    if (e < -1 || e >= E) {
+      if (a.status != nullptr) atomicOr(a.status, kDevBadIndex);
+      e = -1;
     }
+    if (e >= 0) xk = load_logit(row + e);
+    if (!(xk > kNegInf)) e = -1, g = 0.0f, xk = kNegInf;  // no expert, masked, or not a number
     float term = g;
     if constexpr (RENORM) {
       float p = 0.0f, c = 1.0f;
