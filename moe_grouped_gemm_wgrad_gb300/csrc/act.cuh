@@ -7,6 +7,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <cstdint>
+
 namespace mgw {
 
 constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4, kActGeglu = 5;
@@ -63,6 +65,54 @@ __device__ __forceinline__ float act_value(float x) {
   }
   if constexpr (ACT == kActSilu) return x * logistic_fast(x);
   return x;
+}
+
+// Two packed fp32 values per instruction (the FMA pipe's packed form).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// act_value of two values in place.  The GELU's polynomial and products run packed: of some 28
+// instructions a pair about 20 are left.
+template <int ACT>
+__device__ __forceinline__ void act_value2(float& x0, float& x1) {
+  if constexpr (ACT == kActGelu) {
+    const float t0 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x0), 1.0f));
+    const float t1 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x1), 1.0f));
+    const F2 x = f2(x0, x1), t = f2(t0, t1);
+    float e0, e1;
+    split(mul2(mul2(x, x), f2(-0.72134752044448170f, -0.72134752044448170f)), e0, e1);  // -log2(e) / 2
+    const F2 e = f2(ex2_approx(e0), ex2_approx(e1));
+    // minus the tail: the polynomial of normal_tail with its signs turned
+    F2 p = fma2(f2(-0.5f * 1.061405429f, -0.5f * 1.061405429f), t, f2(0.5f * 1.453152027f, 0.5f * 1.453152027f));
+    p = fma2(p, t, f2(-0.5f * 1.421413741f, -0.5f * 1.421413741f));
+    p = fma2(p, t, f2(0.5f * 0.284496736f, 0.5f * 0.284496736f));
+    p = fma2(p, t, f2(-0.5f * 0.254829592f, -0.5f * 0.254829592f));
+    p = mul2(mul2(p, t), e);
+    split(fma2(f2(fminf(fabsf(x0), 1e30f), fminf(fabsf(x1), 1e30f)), p, f2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f))),
+          x0, x1);
+  } else {
+    x0 = act_value<ACT>(x0);
+    x1 = act_value<ACT>(x1);
+  }
 }
 
 // Value and slope together (the backward pass of a gated activation needs both).

@@ -57,11 +57,8 @@ constexpr int kNumBars = 3 * kStages + 5;
 constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) & ~15;
 constexpr int kEpiParts = 3;  // epilogue warps per TMEM lane quarter
 constexpr int kEpiWarps = 4 * kEpiParts;
-// Per epilogue warp: a staging tile of 16 rows by 32 features in bf16, rows 80 bytes apart so
-// that the 8 rows of a matrix meet 8 different bank groups (gated: two of 16 features, 48 bytes
-// apart).
-constexpr int kTurnBytes = 2 * 16 * 48;
-static_assert(16 * 80 <= kTurnBytes, "staging tile");
+// Per epilogue warp: a staging tile of 16 rows by 32 features in bf16 (gated: two of 16).
+constexpr int kTurnBytes = 16 * 64;
 // Most rows of an item whose contraction is split over the pairs of a cluster, and most pairs.
 constexpr int kSplitRows = 64;
 constexpr int kMaxSplit = 4;
@@ -161,61 +158,54 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 
-// A warp's staging tile of 16 rows x (8 CH) features, CH 16-byte chunks per row, and the bf16
-// matrix [.., pitch] it is a piece of: rows row0 .. row0 + left - 1 exist, features from col.
+// A warp's staging tile of 16 rows x CH 16-byte chunks of features.  Row r's chunk c lies at chunk
+// c ^ swizzle(r) of its row, so that the 8 rows of a matrix (one chunk each) and the 8 lanes of a
+// 16-byte access (whole rows) both meet the 8 bank groups once.  (With padded rows instead, 80
+// bytes apart, the loads conflicted and kept the LSU's data pipe 62% busy.)
 template <int CH>
 struct Turn {
-  static constexpr int kStride = CH == 4 ? 80 : 48;
+  static constexpr uint32_t kRow = 16 * CH;  // bytes
+  static __device__ __forceinline__ uint32_t at(uint32_t r, uint32_t c) {
+    return r * kRow + ((c ^ (CH == 4 ? (r >> 1) & 3u : (r >> 2) & 1u)) << 4);
+  }
+  // The memory rows' addresses this lane gives for matrices (8 rows, chunk): rows 0-7 of chunks
+  // 0 .. 3 and, 8 rows on, the same again (CH == 4); all four (rows, chunk) at once (CH == 2).
+  static __device__ __forceinline__ uint32_t fragment() {
+    const uint32_t l = lane_id();
+    return CH == 4 ? at(l & 7u, l >> 3) : at((l & 7u) + 8u * (l >> 4), (l >> 3) & 1u);
+  }
   // Fragment f[4 b + i] of rows 8 b .., chunk i (CH == 4), or f[2 b + i] (CH == 2).
-  static __device__ __forceinline__ void put(uint32_t tile, const uint32_t* f) {
-    const uint32_t l = lane_id();
-    if constexpr (CH == 4) {
-      const uint32_t a = tile + (l & 7u) * kStride + (l >> 3) * 16u;
-      stmatrix_x4_trans(a, f);
-      stmatrix_x4_trans(a + 8 * kStride, f + 4);
-    } else {
-      stmatrix_x4_trans(tile + ((l & 7u) + 8u * (l >> 4)) * kStride + ((l >> 3) & 1u) * 16u, f);
-    }
+  static __device__ __forceinline__ void put(uint32_t frag, const uint32_t* f) {
+    stmatrix_x4_trans(frag, f);
+    if constexpr (CH == 4) stmatrix_x4_trans(frag + 8 * kRow, f + 4);  // 8 rows on: same swizzle
   }
-  static __device__ __forceinline__ void get(uint32_t tile, uint32_t* f) {
-    const uint32_t l = lane_id();
-    if constexpr (CH == 4) {
-      const uint32_t a = tile + (l & 7u) * kStride + (l >> 3) * 16u;
-      ldmatrix_x4_trans(a, f);
-      ldmatrix_x4_trans(a + 8 * kStride, f + 4);
-    } else {
-      ldmatrix_x4_trans(tile + ((l & 7u) + 8u * (l >> 4)) * kStride + ((l >> 3) & 1u) * 16u, f);
-    }
+  static __device__ __forceinline__ void get(uint32_t frag, uint32_t* f) {
+    ldmatrix_x4_trans(frag, f);
+    if constexpr (CH == 4) ldmatrix_x4_trans(frag + 8 * kRow, f + 4);
   }
-  static __device__ __forceinline__ int row_of(int p) {
-    return (CH == 4 ? 8 * p : 0) + static_cast<int>(lane_id() / CH);
-  }
-  static __device__ __forceinline__ void store(uint32_t tile, __nv_bfloat16* m, size_t row0, int pitch,
-                                               int col, int left) {
-    const int chunk = static_cast<int>(lane_id() % CH);
+  // This lane's pieces: rows lane / CH (+ 8 with CH == 4), chunk lane % CH.
+  static __device__ __forceinline__ int row() { return static_cast<int>(lane_id() / CH); }
+  static __device__ __forceinline__ int col() { return static_cast<int>(lane_id() % CH) * 8; }
+  static __device__ __forceinline__ uint32_t piece() { return at(lane_id() / CH, lane_id() % CH); }
+  // m: this lane's piece of the group's first row; left: rows of the group that exist.
+  static __device__ __forceinline__ void store(uint32_t piece, __nv_bfloat16* m, size_t pitch, int left) {
 #pragma unroll
     for (int p = 0; p < CH / 2; ++p) {
-      const int r = row_of(p);
-      const uint4 v = ld_shared_v4(tile + r * kStride + chunk * 16);
-      if (r < left)
-        *reinterpret_cast<uint4*>(m + (row0 + r) * static_cast<size_t>(pitch) + col + 8 * chunk) = v;
+      const uint4 v = ld_shared_v4(piece + p * 8 * kRow);
+      if (row() + 8 * p < left) *reinterpret_cast<uint4*>(m + 8 * p * pitch) = v;
     }
   }
-  static __device__ __forceinline__ void load(const __nv_bfloat16* m, size_t row0, int pitch, int col,
-                                              int left, uint4 (&v)[CH / 2]) {
-    const int chunk = static_cast<int>(lane_id() % CH);
+  static __device__ __forceinline__ void load(const __nv_bfloat16* m, size_t pitch, int left,
+                                              uint4 (&v)[CH / 2]) {
 #pragma unroll
     for (int p = 0; p < CH / 2; ++p) {
-      const int r = row_of(p);
       v[p] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < left)
-        v[p] = *reinterpret_cast<const uint4*>(m + (row0 + r) * static_cast<size_t>(pitch) + col + 8 * chunk);
+      if (row() + 8 * p < left) v[p] = *reinterpret_cast<const uint4*>(m + 8 * p * pitch);
     }
   }
-  static __device__ __forceinline__ void fill(uint32_t tile, const uint4 (&v)[CH / 2]) {
+  static __device__ __forceinline__ void fill(uint32_t piece, const uint4 (&v)[CH / 2]) {
 #pragma unroll
-    for (int p = 0; p < CH / 2; ++p)
-      st_shared_v4(tile + row_of(p) * kStride + (lane_id() % CH) * 16u, v[p]);
+    for (int p = 0; p < CH / 2; ++p) st_shared_v4(piece + p * 8 * kRow, v[p]);
   }
 };
 
@@ -546,9 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
     const uint32_t acc_empty0 = map_to_cta(bar_acc_empty(0), even);
     const uint32_t tile = sbase + kOffTurn + static_cast<uint32_t>(ew) * kTurnBytes;
     constexpr int kCh = kGated ? 2 : 4;  // 16-byte chunks of y per row and warp
+    const uint32_t frag = tile + Turn<kCh>::fragment(), piece = tile + Turn<kCh>::piece();
     const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(args.residual);
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(args.y);
-    __nv_bfloat16* zout = static_cast<__nv_bfloat16*>(args.z);
+    const bool save = args.z != nullptr;
     // Partial accumulators in the ring: 2 KB per (pair, 16-column group, lane quarter).
     auto partial_at = [&](int j, int g) {
       return sbase + static_cast<uint32_t>(((j - 1) * (kSplitRows / 16) + g) * 4 + quarter) * 2048u + lane * 16u;
@@ -607,12 +597,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
         tmem_ld_16x256b_x2(ta + 16u * part, r);
         tmem_ld_16x256b_x2(ta + (16u << 16) + 16u * part, r + 8);
       }
+      // this lane's pieces of its first group's rows; a step takes it to the warp's next group
+      const size_t row = static_cast<size_t>(x.row0) + 16 * part + Turn<kCh>::row();
+      const size_t pitch_y = F, pitch_z = N;
+      __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(args.y) + row * pitch_y + col + Turn<kCh>::col();
+      __nv_bfloat16* zp = static_cast<__nv_bfloat16*>(args.z) + row * pitch_z + col + Turn<kCh>::col();
+      const __nv_bfloat16* rp = res + row * pitch_y + col + Turn<kCh>::col();
       uint4 rv[kCh / 2];
-      if (res != nullptr && part * 16 < x.nrows)
-        Turn<kCh>::load(res, static_cast<size_t>(x.row0) + 16 * part, F, col, x.nrows - 16 * part, rv);
+      if (res != nullptr && part * 16 < x.nrows) Turn<kCh>::load(rp, pitch_y, x.nrows - 16 * part, rv);
       for (int g = part; g * 16 < x.nrows; g += kEpiParts) {
         const int left = x.nrows - 16 * g;  // rows of this group that exist
-        const size_t row = static_cast<size_t>(x.row0) + 16 * g;
         const bool more = (g + kEpiParts) * 16 < x.nrows;
         tmem_wait_ld_regs(r);
         // z[h][b][j]: lane 16 h + 8 (j / 2) + lane_id / 4, row 8 b + 2 (lane_id % 4) + j % 2
@@ -649,13 +643,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
         uint32_t f[8], rf[8];
         __syncwarp();  // the previous group has left the staging tile
         if (res != nullptr) {
-          Turn<kCh>::fill(tile, rv);
-          if (more) Turn<kCh>::load(res, row + 16 * kEpiParts, F, col, left - 16 * kEpiParts, rv);
+          Turn<kCh>::fill(piece, rv);
+          rp += 16 * kEpiParts * pitch_y;
+          if (more) Turn<kCh>::load(rp, pitch_y, left - 16 * kEpiParts, rv);
           __syncwarp();
-          Turn<kCh>::get(tile, rf);
+          Turn<kCh>::get(frag, rf);
           __syncwarp();
         }
-        if (zout != nullptr) {
+        if (save) {
           if constexpr (kGated) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -663,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
               for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) f[2 * b + i] = pack_bf16(z[h][b][2 * i], z[h][b][2 * i + 1]);
-              Turn<2>::put(tile + h * 768, f);
+              Turn<2>::put(frag + h * 512, f);
             }
           } else {
 #pragma unroll
@@ -671,15 +666,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 f[4 * b + i] = pack_bf16(z[i >> 1][b][2 * (i & 1)], z[i >> 1][b][2 * (i & 1) + 1]);
-            Turn<4>::put(tile, f);
+            Turn<4>::put(frag, f);
           }
           __syncwarp();
           if constexpr (kGated) {
-            Turn<2>::store(tile, zout, row, N, col, left);
-            Turn<2>::store(tile + 768, zout, row, N, col + F, left);
+            Turn<2>::store(piece, zp, pitch_z, left);
+            Turn<2>::store(piece + 512, zp + F, pitch_z, left);
           } else {
-            Turn<4>::store(tile, zout, row, N, col, left);
+            Turn<4>::store(piece, zp, pitch_z, left);
           }
+          zp += 16 * kEpiParts * pitch_z;
         }
         // y in z's place: [0][b][j] when gated
 #pragma unroll
@@ -687,9 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              z[h][b][j] = act_value<kInner>(z[h][b][j]);
-              if constexpr (kGated) z[h][b][j] *= z[1][b][j];
+            for (int j = 0; j < 4; j += 2) {
+              act_value2<kInner>(z[h][b][j], z[h][b][j + 1]);
+              if constexpr (kGated) {
+                z[h][b][j] *= z[1][b][j];
+                z[h][b][j + 1] *= z[1][b][j + 1];
+              }
             }
         if (res != nullptr) {
 #pragma unroll
@@ -707,9 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
           for (int i = 0; i < kCh; ++i)
             f[kCh * b + i] = pack_bf16(z[i >> 1][b][2 * (i & 1)], z[i >> 1][b][2 * (i & 1) + 1]);
         __syncwarp();  // z has left the tile
-        Turn<kCh>::put(tile, f);
+        Turn<kCh>::put(frag, f);
         __syncwarp();
-        Turn<kCh>::store(tile, y, row, F, col, left);
+        Turn<kCh>::store(piece, yp, pitch_y, left);
+        yp += 16 * kEpiParts * pitch_y;
       }
       tc_fence_before();
       __syncwarp();
