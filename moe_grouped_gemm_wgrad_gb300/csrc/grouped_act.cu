@@ -72,9 +72,10 @@ constexpr uint32_t kSfCol0 = 2 * kW;
 static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
 static_assert(kSfCol0 + 16 * kStages <= kTmemCols, "TMEM budget");
 
-// Tables: expert_off, padded starts and first row tile of every expert, E+1 ints each.
+// Tables: expert_off, padded starts, first row tile and row tile width of every expert, E+1 ints
+// each.
 __host__ __device__ constexpr size_t act_smem_bytes(int E) {
-  return static_cast<size_t>(kOffTable) + sizeof(int) * 3 * (static_cast<size_t>(E) + 1) + 1024;
+  return static_cast<size_t>(kOffTable) + sizeof(int) * 4 * (static_cast<size_t>(E) + 1) + 1024;
 }
 static_assert(act_smem_bytes(kMaxExperts) <= 232448, "shared memory budget");
 
@@ -219,32 +220,44 @@ struct Item {
   int width;  // nrows rounded up to 16: the MMA's N
 };
 
-__device__ __forceinline__ Item decode(int it, int tiles_f, const int* s_off, const int* s_pad,
-                                       const int* s_tile, int E) {
-  const int t = it / tiles_f;
-  int lo = 0, hi = E - 1;  // the largest e with s_tile[e] <= t: an expert with rows
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_tile[mid] <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
+// Walks a pair's items (expert-major, then row tile, then feature tile; items first, first + step,
+// ..).  Every warp of the CTA walks the same sequence, so a step is kept short: no division, and
+// the expert is searched for from the last one on.
+struct Items {
+  const int *s_off, *s_pad, *s_tile, *s_width;
+  int tiles_f, total;        // feature tiles; items in all
+  int step_t, step_f, step;  // the step in row tiles and feature tiles
+  int it, t, ft, e;
+
+  __device__ __forceinline__ Items(const int* off, const int* pad, const int* tile, const int* width,
+                                   int tiles_f_, int total_, int first, int step_)
+      : s_off(off), s_pad(pad), s_tile(tile), s_width(width), tiles_f(tiles_f_), total(total_),
+        step_t(step_ / tiles_f_), step_f(step_ % tiles_f_), step(step_), it(first),
+        t(first / tiles_f_), ft(first % tiles_f_), e(0) {}
+
+  // The next item with rows; false past the last one.  The values are the same in every lane.
+  __device__ __forceinline__ bool next(Item& x) {
+    while (it < total) {
+      while (s_tile[e + 1] <= t) ++e;  // t < s_tile[E]
+      e = __shfl_sync(0xffffffffu, e, 0);
+      const int w = s_width[e];
+      const int r = (t - s_tile[e]) * w;
+      x.e = e;
+      x.ft = ft;
+      x.row0 = __shfl_sync(0xffffffffu, s_off[e] + r, 0);
+      x.p0 = __shfl_sync(0xffffffffu, s_pad[e] + r, 0);
+      // rounding w up can leave a last tile without rows
+      x.nrows = __shfl_sync(0xffffffffu, max(min(w, s_off[e + 1] - s_off[e] - r), 0), 0);
+      x.width = (x.nrows + 15) & ~15;
+      it += step;
+      t += step_t;
+      ft += step_f;
+      if (ft >= tiles_f) ft -= tiles_f, ++t;
+      if (x.nrows > 0) return true;
+    }
+    return false;
   }
-  const int cnt = s_off[lo + 1] - s_off[lo];
-  const int tiles = s_tile[lo + 1] - s_tile[lo];
-  const int w = ((cnt + tiles - 1) / tiles + 15) & ~15;
-  const int r = (t - s_tile[lo]) * w;
-  lo = __shfl_sync(0xffffffffu, lo, 0);
-  Item x;
-  x.e = lo;
-  x.ft = it - t * tiles_f;
-  x.row0 = __shfl_sync(0xffffffffu, s_off[lo] + r, 0);
-  x.p0 = __shfl_sync(0xffffffffu, s_pad[lo] + r, 0);
-  // rounding w up can leave a last tile without rows
-  x.nrows = __shfl_sync(0xffffffffu, max(min(w, cnt - r), 0), 0);
-  x.width = (x.nrows + 15) & ~15;
-  return x;
-}
+};
 
 // S > 1: few items of few rows.  A cluster of S pairs takes one item, pair j the j-th part of the
 // contraction; the other pairs' accumulators go to the first pair's ring, which is idle by then,
@@ -261,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
   int* s_off = reinterpret_cast<int*>(smem + kOffTable);
   int* s_pad = s_off + (E + 1);
   int* s_tile = s_pad + (E + 1);
+  int* s_width = s_tile + (E + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&s_misc[1]);
   const int tid = threadIdx.x;
   // The same value in every lane, in a form the compiler knows to be: the producer and the MMA
@@ -290,7 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
     if (lane == 0) s_tile[0] = 0;
     for (int base = 0; base < E; base += 32) {
       const int e = base + static_cast<int>(lane);
-      int v = e < E ? (s_off[e + 1] - s_off[e] + kW - 1) / kW : 0;
+      const int cnt = e < E ? s_off[e + 1] - s_off[e] : 0;
+      int v = (cnt + kW - 1) / kW;
+      if (e < E) s_width[e] = v > 0 ? ((cnt + v - 1) / v + 15) & ~15 : 16;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, v, d);
@@ -338,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
   // first item and step to the next one; with S > 1 a cluster has one item at most
   const int pair = static_cast<int>(blockIdx.x) / (2 * S);
   const int npairs = S > 1 ? 1 << 30 : static_cast<int>(gridDim.x >> 1);
+  Items items(s_off, s_pad, s_tile, s_width, tiles_f, total, pair, npairs);
   // this pair's chunks of the contraction
   const int split = static_cast<int>(cta >> 1);
   const int c0 = nch * split / S, c1 = nch * (split + 1) / S;
@@ -354,9 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
     const uint32_t full0_leader = map_to_cta(bar_full(0), even);
     const long long a_tiles = args.Mw / 128;   // 128-row tiles of the weights' scale layout
     const long long b_tiles = args.Mcap / 128;
-    for (int it = pair; it < total && ok; it += npairs) {
-      const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
-      if (x.nrows == 0) continue;
+    Item x;
+    while (ok && items.next(x)) {
       // this CTA's weight rows: 128 plain ones, or 64 gate and 64 up rows
       const int f0 = kGated ? x.ft * 128 + 64 * static_cast<int>(rank)
                             : x.ft * 256 + 128 * static_cast<int>(rank);
@@ -428,9 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
       bool ok = true;
       const uint16_t both = static_cast<uint16_t>(0x3u << even);
       const uint64_t a_desc0 = sdesc_kmajor_sw128(sbase);
-      for (int it = pair; it < total && ok; it += npairs) {
-        const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
-        if (x.nrows == 0) continue;
+      Item x;
+      while (ok && items.next(x)) {
         const int buf = n & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(bar_acc_empty(buf), ((n >> 1) & 1) ^ 1u, abort_flag))) {
           ok = false;
@@ -480,9 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int it = pair; it < total && ok; it += npairs) {
-      const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
-      if (x.nrows == 0) continue;
+    Item x;
+    while (ok && items.next(x)) {
       // Row p0 + 32 q + lane of x is word (shift + q) of this lane's row of the atoms: 16 bytes
       // per atom hold the four rows r0, r0 + 32, r0 + 64, r0 + 96.
       const uint32_t start = static_cast<uint32_t>(x.p0 & 127) + lane;
@@ -546,11 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
     if constexpr (S > 1) {
       bool send = false;
       Item x;
-      if (pair < total) {
-        x = decode(pair, tiles_f, s_off, s_pad, s_tile, E);
-        send = x.nrows > 0 && split > 0 &&
-               __all_sync(0xffffffffu, mbar_wait(bar_acc_full(0), 0, abort_flag));
-        if (x.nrows > 0 && split > 0 && !send && lane == 0) abort_both();
+      if (split > 0 && items.next(x)) {
+        send = __all_sync(0xffffffffu, mbar_wait(bar_acc_full(0), 0, abort_flag));
+        if (!send && lane == 0) abort_both();
       }
       tc_fence_after();
       cluster_sync();  // every pair's MMAs have ended: the first pair's ring is free
@@ -568,9 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
       cluster_sync();  // the partial accumulators are there
     }
     int n = 0;
-    for (int it = pair; it < total && split == 0; it += npairs) {
-      const Item x = decode(it, tiles_f, s_off, s_pad, s_tile, E);
-      if (x.nrows == 0) continue;
+    Item x;
+    while (split == 0 && items.next(x)) {
       // the warp's first column of y; of z too (gated: gate columns, up columns F further)
       const int col = kGated ? x.ft * 128 + 64 * static_cast<int>(rank) + 16 * quarter
                              : x.ft * 256 + 128 * static_cast<int>(rank) + 32 * quarter;
