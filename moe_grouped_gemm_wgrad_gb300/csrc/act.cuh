@@ -90,25 +90,34 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
+// normal_tail of two values, packed: minus the tails (the polynomial with its signs turned) and
+// the exponentials.
+__device__ __forceinline__ F2 minus_tail2(float x0, float x1, F2& e) {
+  const float t0 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x0), 1.0f));
+  const float t1 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x1), 1.0f));
+  const F2 x = f2(x0, x1), t = f2(t0, t1);
+  float e0, e1;
+  split(mul2(mul2(x, x), f2(-0.72134752044448170f, -0.72134752044448170f)), e0, e1);  // -log2(e) / 2
+  e = f2(ex2_approx(e0), ex2_approx(e1));
+  F2 p = fma2(f2(-0.5f * 1.061405429f, -0.5f * 1.061405429f), t, f2(0.5f * 1.453152027f, 0.5f * 1.453152027f));
+  p = fma2(p, t, f2(-0.5f * 1.421413741f, -0.5f * 1.421413741f));
+  p = fma2(p, t, f2(0.5f * 0.284496736f, 0.5f * 0.284496736f));
+  p = fma2(p, t, f2(-0.5f * 0.254829592f, -0.5f * 0.254829592f));
+  return mul2(mul2(p, t), e);
+}
+__device__ __forceinline__ F2 gelu2_from_tail(float x0, float x1, F2 minus_h) {
+  return fma2(f2(fminf(fabsf(x0), 1e30f), fminf(fabsf(x1), 1e30f)), minus_h,
+              f2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
+}
+
 // act_value of two values in place.  The GELU's polynomial and products run packed: of some 28
 // instructions a pair about 20 are left.
 template <int ACT>
 __device__ __forceinline__ void act_value2(float& x0, float& x1) {
   if constexpr (ACT == kActGelu) {
-    const float t0 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x0), 1.0f));
-    const float t1 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x1), 1.0f));
-    const F2 x = f2(x0, x1), t = f2(t0, t1);
-    float e0, e1;
-    split(mul2(mul2(x, x), f2(-0.72134752044448170f, -0.72134752044448170f)), e0, e1);  // -log2(e) / 2
-    const F2 e = f2(ex2_approx(e0), ex2_approx(e1));
-    // minus the tail: the polynomial of normal_tail with its signs turned
-    F2 p = fma2(f2(-0.5f * 1.061405429f, -0.5f * 1.061405429f), t, f2(0.5f * 1.453152027f, 0.5f * 1.453152027f));
-    p = fma2(p, t, f2(-0.5f * 1.421413741f, -0.5f * 1.421413741f));
-    p = fma2(p, t, f2(0.5f * 0.284496736f, 0.5f * 0.284496736f));
-    p = fma2(p, t, f2(-0.5f * 0.254829592f, -0.5f * 0.254829592f));
-    p = mul2(mul2(p, t), e);
-    split(fma2(f2(fminf(fabsf(x0), 1e30f), fminf(fabsf(x1), 1e30f)), p, f2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f))),
-          x0, x1);
+    F2 e;
+    const F2 p = minus_tail2(x0, x1, e);
+    split(gelu2_from_tail(x0, x1, p), x0, x1);
   } else {
     x0 = act_value<ACT>(x0);
     x1 = act_value<ACT>(x1);
@@ -133,6 +142,24 @@ __device__ __forceinline__ void act_value_slope(float x, float& value, float& sl
   } else {
     value = x;
     slope = 1.0f;
+  }
+}
+
+// act_value_slope of two values.
+template <int ACT>
+__device__ __forceinline__ void act_value_slope2(float x0, float x1, float (&value)[2], float (&slope)[2]) {
+  if constexpr (ACT == kActGelu) {
+    F2 e;
+    const F2 p = minus_tail2(x0, x1, e);
+    split(gelu2_from_tail(x0, x1, p), value[0], value[1]);
+    float p0, p1;
+    split(p, p0, p1);
+    const F2 cdf = f2(x0 >= 0.0f ? 1.0f + p0 : -p0, x1 >= 0.0f ? 1.0f + p1 : -p1);
+    const F2 phi = mul2(f2(x0, x1), f2(0.3989422804014327f, 0.3989422804014327f));
+    split(fma2(phi, e, cdf), slope[0], slope[1]);  // Phi(x) + x phi(x)
+  } else {
+    act_value_slope<ACT>(x0, value[0], slope[0]);
+    act_value_slope<ACT>(x1, value[1], slope[1]);
   }
 }
 

@@ -122,14 +122,17 @@ __global__ void __launch_bounds__(kWarps * 32) act_backward_kernel(ActBwdArgs a)
           float up[8], du[8];
           if constexpr (kGated) unpack8(ur[i], up);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float v, sl;
-            act_value_slope<kInner>(zv[j], v, sl);
-            d[j] = g[j] * sl;
-            if constexpr (kGated) {
-              d[j] *= up[j];
-              du[j] = g[j] * v;
-              sum[kSums - 1][j] += du[j];
+          for (int j = 0; j < 8; j += 2) {
+            float v[2], sl[2];
+            act_value_slope2<kInner>(zv[j], zv[j + 1], v, sl);
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+              d[j + i2] = g[j + i2] * sl[i2];
+              if constexpr (kGated) {
+                d[j + i2] *= up[j + i2];
+                du[j + i2] = g[j + i2] * v[i2];
+                sum[kSums - 1][j + i2] += du[j + i2];
+              }
             }
           }
           *reinterpret_cast<uint4*>(dz + row * a.N + c) = pack8(d);
@@ -157,13 +160,16 @@ __global__ void __launch_bounds__(kWarps * 32) act_backward_kernel(ActBwdArgs a)
   }
 }
 
-// dbias[e, n]: the sums of the expert's tiles.  32 columns per CTA; warp w adds the tiles w,
-// w + 8, .. and the warps' sums are added in order.
+// dbias[e, n]: the sums of the expert's tiles.  The CTA's 8 warps are 8 / SLICES column blocks
+// of 32 by SLICES slices of the tiles (tiles s, s + SLICES, ..), whose sums are added in order.
+template <int SLICES>
 __global__ void __launch_bounds__(kWarps * 32) act_dbias_kernel(ActBwdArgs a) {
+  constexpr int kBlocks = kWarps / SLICES;
   __shared__ int s_first;
   __shared__ float s_sum[kWarps][32];
   const int e = blockIdx.x, warp = threadIdx.x >> 5;
-  const int n = blockIdx.y * 32 + static_cast<int>(lane_id());  // N is a multiple of 128
+  const int slice = warp / kBlocks;
+  const int n = (blockIdx.y * kBlocks + warp % kBlocks) * 32 + static_cast<int>(lane_id());
   if (threadIdx.x == 0) s_first = 0;
   __syncthreads();
   // the expert's first tile on the padded axis, and the offsets' check, in one pass
@@ -180,16 +186,34 @@ __global__ void __launch_bounds__(kWarps * 32) act_dbias_kernel(ActBwdArgs a) {
   const int t1 = t0 + (a.expert_off[e + 1] - a.expert_off[e] + kRows - 1) / kRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
   float v = 0.0f;
+  if (n < a.N) {
 #pragma unroll 8
-  for (int t = t0 + warp; t < t1; t += kWarps) v += a.partial[static_cast<size_t>(t) * a.N + n];
-  s_sum[warp][lane_id()] = v;
-  __syncthreads();
-  if (warp == 0) {
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s_sum[w][lane_id()];
-    a.dbias[static_cast<size_t>(e) * a.N + n] = v;
+    for (int t = t0 + slice; t < t1; t += SLICES) v += a.partial[static_cast<size_t>(t) * a.N + n];
   }
+  if constexpr (SLICES > 1) {
+    s_sum[warp][lane_id()] = v;
+    __syncthreads();
+    if (slice != 0) return;
+#pragma unroll
+    for (int k = 1; k < SLICES; ++k) v += s_sum[warp + k * kBlocks][lane_id()];
+  }
+  if (n < a.N) a.dbias[static_cast<size_t>(e) * a.N + n] = v;
+}
+
+template <int SLICES>
+cudaError_t launch_dbias(const ActBwdArgs& a, cudaStream_t stream) {
+  constexpr int kBlockCols = kWarps / SLICES * 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.E), static_cast<unsigned>((a.N + kBlockCols - 1) / kBlockCols));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  // starts its own checks while the tiles' launch ends (programmatic dependent launch)
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, act_dbias_kernel<SLICES>, a);
 }
 
 template <int ACT>
@@ -207,16 +231,12 @@ cudaError_t launch(const ActBwdArgs& a, cudaStream_t stream) {
   act_backward_kernel<ACT, false><<<grid, kWarps * 32, smem, stream>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || a.dbias == nullptr) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.E), static_cast<unsigned>(a.N / 32));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, act_dbias_kernel, a);
+  // Slices by the tiles an expert has on average: many CTAs cost more than a few loads in a row
+  // (32768 x 1536 over 64 experts, profiled: 8.3 us with eight slices, 7.6 with one).
+  const long long mean = tiles / a.E;
+  if (mean >= 64) return launch_dbias<8>(a, stream);
+  if (mean >= 16) return launch_dbias<2>(a, stream);
+  return launch_dbias<1>(a, stream);
 }
 
 }  // namespace
