@@ -7,10 +7,15 @@
 // a lane 8 columns (16-byte loads and stores), and keep the columns' sums in fp32 registers.  A
 // warp asks for four rows before it works on the first: 65536 x 1536 took 115 us with one row at
 // a time, 104 us so (tiles of 64 or 32 rows: no gain at any size).
-// With dbias the warps' sums meet in shared memory and go to the workspace, one row of sums
-// per tile; a second launch adds every expert's tiles in order, so dbias does not vary between
-// runs.  Up to kWholeRows rows in all, a CTA takes a whole expert instead and stores its dbias
-// itself: one launch and no workspace (a launch costs more than the few rows do).  dbias sums dz before it is rounded to bf16.  HBM bounds it: z, dy and dz once each.
+//
+// With dbias the warps' sums meet in shared memory and go to the workspace, one row of sums per
+// tile; a second launch adds every expert's tiles in an order that the sizes fix, so dbias does
+// not vary between runs.  It sums dz before dz is rounded to bf16.  Up to kWholeRows rows in all,
+// a CTA takes a whole expert instead and stores its dbias itself: one launch and no workspace (a
+// launch costs more than the few rows do).
+//
+// HBM bounds it: z, dy and dz once each.  65536 x 1536 GELU: 94 us without dbias (6.4 TB/s, 96%
+// of the copy rate), 100 us with it.
 #include <cuda_bf16.h>
 
 #include <cstdint>

@@ -30,6 +30,12 @@
 //   warps 14-17  scale writers, one TMEM lane quarter each: they place the stage's scale words
 //                in TMEM, which is what lets a tile start at any multiple of 16 rows and the
 //                gate / up rows interleave.
+//
+// Measured on a GB300, isolated launches: 65536 x 1536 x 4096 over 64 experts 261 us without an
+// epilogue (3.16 PFLOP/s, tensor pipe 80-87% busy), 280 us with GELU and saved pre-activation;
+// back to back the power cap (SM clock 1.3 GHz) makes that 306 and 330 us.  128 rows over 64
+// experts of 2048 x 4096: 85 us, 6.0 TB/s of weights.  Contractions below about 1500 are bound
+// by the epilogue (65536 x 1024 x 256 GELU, pre-activation saved: 75 us, HBM floor 43).
 #include <cuda_bf16.h>
 
 #include <cstdint>
