@@ -132,19 +132,41 @@ __device__ __forceinline__ void logistic(float x, float& s, float& c) {
   c = x >= 0.0f ? q * r : r;
 }
 
-// The lane's V logits, -inf past E; a NaN is reported and counts as -inf.
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int E, int first, bool live, bool vec, float (&x)[V],
-                                         int* status) {
+// This lane's V elements of its token's row of E: by 16-byte pieces where E is a multiple of V,
+// else one by one.  (Other rows through shared memory, read and written as one run: slower, 36
+// instead of 28 us for 40000 x 61 both ways, the lanes' sectors being in L1 anyway.)
+template <int V, int L>
+struct Row {
+  int E, first;  // first: the lane's first expert
+  bool live, vec;
+
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, float none, float (&x)[V]) const {
 #pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = kNegInf;
-  if (live && vec) {
-    if (first < E) load_vec<V>(row + first, x);
-  } else if (live) {
+    for (int j = 0; j < V; ++j) x[j] = none;
+    if (live && vec) {
+      if (first < E) load_vec<V>(row + first, x);
+    } else if (live) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (first + j < E) x[j] = load_logit(row + first + j);
+      for (int j = 0; j < V; ++j)
+        if (first + j < E) x[j] = load_logit(row + first + j);
+    }
   }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, const float (&x)[V]) const {
+    if (live && vec) {
+      if (first < E) store_vec<V>(row + first, x);
+    } else if (live) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (first + j < E) store_logit(row + first + j, x[j]);
+    }
+  }
+};
+
+// NaN logits are reported and count as masked.
+template <int V>
+__device__ __forceinline__ void mask_nan(float (&x)[V], int* status) {
   bool nan = false;
 #pragma unroll
   for (int j = 0; j < V; ++j) nan |= x[j] != x[j];
@@ -153,18 +175,6 @@ __device__ __forceinline__ void load_row(const T* row, int E, int first, bool li
     for (int j = 0; j < V; ++j)
       if (x[j] != x[j]) x[j] = kNegInf;
     if (status != nullptr) atomicOr(status, kDevBadLogit);
-  }
-}
-
-// V values of one lane to a row of fp32 or bf16.
-template <typename T, int V>
-__device__ __forceinline__ void store_row(T* row, int E, int first, bool vec, const float (&x)[V]) {
-  if (vec) {
-    if (first < E) store_vec<V>(row + first, x);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (first + j < E) store_logit(row + first + j, x[j]);
   }
 }
 
@@ -267,34 +277,26 @@ __device__ __forceinline__ int pick_packed(uint32_t (&key)[V], int top_k, int su
 
 template <typename T, int V, int L, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
-  extern __shared__ float s_vals[];  // groups that are not whole lanes: kWarps rows of E values
+  extern __shared__ float s_vals[];  // groups that are not whole lanes: 32 V values per warp
   const int lane = static_cast<int>(lane_id());
   const int sub = lane % L;  // lane of the token
-  const int warp = threadIdx.x >> 5;
-  const long long t = (static_cast<long long>(blockIdx.x) * kWarps + warp) * (32 / L) + lane / L;
+  const long long t = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * (32 / L) + lane / L;
   const bool live = t < a.T;
   const int E = a.E;
   const int first = sub * V;  // this lane's first expert
-  const bool vec = E % V == 0;
+  const Row<V, L> at{E, first, live, E % V == 0};
   const T* row = static_cast<const T*>(a.logits) + t * E;
   float x[V], s[V], m = 0.0f, inv = 0.0f;
-  load_row<T, V>(row, E, first, live, vec, x, a.status);
+  at.load(row, kNegInf, x);
+  mask_nan(x, a.status);
   const bool need_scores = (SIGMOID ? a.bias != nullptr : !RENORM || a.bias != nullptr) ||
                            a.scores != nullptr || (a.groups > 1 && a.group_best == 2);
   if (need_scores) row_scores<V, L, SIGMOID>(x, s, m, inv);
-  if (a.scores != nullptr && live) store_row<float, V>(a.scores + t * E, E, first, vec, s);
+  if (a.scores != nullptr) at.store(a.scores + t * E, s);
   uint32_t key[V];
   if (a.bias != nullptr) {
     float b[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = 0.0f;
-    if (vec) {
-      if (first < E) load_vec<V>(a.bias + first, b);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (first + j < E) b[j] = a.bias[first + j];
-    }
+    Row<V, L>{E, first, true, at.vec}.load(a.bias, 0.0f, b);
 #pragma unroll
     for (int j = 0; j < V; ++j) key[j] = x[j] == kNegInf ? 0u : key_of(s[j] + b[j]);
   } else {
@@ -332,31 +334,49 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) key[j] = 0u;
       }
-    } else if constexpr (L == 32) {
-      // group values through shared memory: lane g takes group g
-      float* vals = s_vals + warp * E;
+    } else {
+      // group values through shared memory: the token's lane g takes groups g, g + L, ..
+      float* vals = s_vals + (threadIdx.x >> 5) * (32 * V) + lane / L * E;
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (first + j < E)
-          vals[first + j] = key[j] == 0u ? kNegInf : (sum2 && a.bias == nullptr ? s[j] : value_of(key[j]));
+          vals[first + j] =
+              key[j] == 0u ? kNegInf : (sum2 && a.bias == nullptr ? s[j] : value_of(key[j]));
       __syncwarp();
-      uint32_t gkey = 0;
-      if (lane < a.groups) {
+      constexpr int kMine = 32 / L;  // groups of a lane, at most
+      uint32_t gkey[kMine];
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const int g = sub + q * L;
         float b1 = kNegInf, b2 = kNegInf;
-        for (int i = 0; i < per; ++i) {
-          const float v = vals[lane * per + i];
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
+        if (g < a.groups) {
+          for (int i = 0; i < per; ++i) {
+            const float v = vals[g * per + i];
+            b2 = fmaxf(b2, fminf(b1, v));
+            b1 = fmaxf(b1, v);
+          }
         }
-        if (b1 != kNegInf) gkey = key_of(sum2 && b2 != kNegInf ? b1 + b2 : b1);
+        gkey[q] = b1 == kNegInf ? 0u : key_of(sum2 && b2 != kNegInf ? b1 + b2 : b1);
       }
       unsigned kept = 0;
       for (int i = 0; i < a.top_groups; ++i) {
-        const uint32_t best = lanes_max<32>(gkey);
-        if (best == 0u) break;
-        const int g = lowest_lane<32>(gkey == best, lane);
-        kept |= 1u << g;
-        if (lane == g) gkey = 0u;
+        uint32_t mine = gkey[0];
+#pragma unroll
+        for (int q = 1; q < kMine; ++q) mine = max(mine, gkey[q]);
+        const uint32_t best = lanes_max<L>(mine);
+        // the lowest group of that value: the largest 32 - g
+        uint32_t c = 0;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+          if (best != 0u && gkey[q] == best) c = max(c, static_cast<uint32_t>(32 - (sub + q * L)));
+        c = lanes_max<L>(c);
+        if (c != 0u) {
+          const int g = 32 - static_cast<int>(c);
+          kept |= 1u << g;
+#pragma unroll
+          for (int q = 0; q < kMine; ++q)
+            if (g == sub + q * L) gkey[q] = 0u;
+        }
       }
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -449,8 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   const long long t = (static_cast<long long>(blockIdx.x) * kWarps + warp) * (32 / L) + lane / L;
   const bool live = t < a.T;
   const int E = a.E;
-  const int first = sub * V;
-  const bool vec = E % V == 0;
+  const Row<V, L> at{E, sub * V, live, E % V == 0};
   const T* row = static_cast<const T*>(a.logits) + t * E;
   // the chosen experts first: their logits' addresses depend on them
   int e = -1;
@@ -462,16 +481,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   float x[V], s[V], add[V], G[V], m = 0.0f, inv = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) add[j] = G[j] = s[j] = 0.0f;
-  load_row<T, V>(row, E, first, live, vec, x, a.status);
-  if (a.dscores != nullptr && live) {
-    if (vec) {
-      if (first < E) load_vec<V>(a.dscores + t * E + first, G);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (first + j < E) G[j] = a.dscores[t * E + first + j];
-    }
-  }
+  at.load(row, kNegInf, x);
+  mask_nan(x, a.status);
+  if (a.dscores != nullptr) at.load(a.dscores + t * E, 0.0f, G);
   const bool dense = !SIGMOID && (!RENORM || a.dscores != nullptr);
   // the chosen experts' terms: added to G (plain softmax) or straight to dx (the others)
   if (a.dweights != nullptr) {
@@ -533,14 +545,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
       if (RENORM) dx[j] += add[j];
     }
   }
-  if (live) store_row<T, V>(static_cast<T*>(a.dlogits) + t * E, E, first, vec, dx);
+  at.store(static_cast<T*>(a.dlogits) + t * E, dx);
 }
 
 template <typename T, int V, int L, bool SIGMOID, bool RENORM>
 cudaError_t launch_one(const RouteArgs& a, cudaStream_t stream) {
   constexpr int kTokens = kWarps * (32 / L);  // per CTA
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + kTokens - 1) / kTokens);
-  const size_t smem = a.groups > 1 && L == 32 ? sizeof(float) * kWarps * a.E : 0;
+  const size_t smem = a.groups > 1 ? sizeof(float) * kWarps * 32 * V : 0;
   route_kernel<T, V, L, SIGMOID, RENORM><<<grid, kWarps * 32, smem, stream>>>(a);
   return cudaGetLastError();
 }
@@ -558,17 +570,10 @@ cudaError_t by_mode(const Args& a, bool sigmoid, bool renorm, cudaStream_t s) {
   return renorm ? launch_one<T, V, L, false, true>(a, s) : launch_one<T, V, L, false, false>(a, s);
 }
 
-// Groups that are not runs of whole lanes need a warp per token.
-bool whole_lanes(const RouteBwdArgs&) { return true; }
-bool whole_lanes(const RouteArgs& a) {
-  const int per = a.E / a.groups, lanes = per / 8;
-  return a.groups == 1 || (per % 8 == 0 && (lanes & (lanes - 1)) == 0);
-}
-
 template <typename T, typename Args>
 cudaError_t by_width(const Args& a, bool sigmoid, bool renorm, cudaStream_t s) {
-  if (a.E <= 64 && a.top_k <= 8 && whole_lanes(a)) return by_mode<T, 8, 8>(a, sigmoid, renorm, s);
-  if (a.E <= 128 && a.top_k <= 16 && whole_lanes(a)) return by_mode<T, 8, 16>(a, sigmoid, renorm, s);
+  if (a.E <= 64 && a.top_k <= 8) return by_mode<T, 8, 8>(a, sigmoid, renorm, s);
+  if (a.E <= 128 && a.top_k <= 16) return by_mode<T, 8, 16>(a, sigmoid, renorm, s);
   if (a.E <= 256) return by_mode<T, 8, 32>(a, sigmoid, renorm, s);
   if (a.E <= 512) return by_mode<T, 16, 32>(a, sigmoid, renorm, s);
   return by_mode<T, 32, 32>(a, sigmoid, renorm, s);

@@ -74,6 +74,13 @@ ROUTES = [
     (9, 1000, 3, "f32", "softmax", False, 4, 2, 1, True, 1.0, 0),
     (25, 96, 8, "bf16", "softmax", False, 32, 3, 1, True, 1.0, 0),
     (12, 129, 7, "f32", "sigmoid", True, 3, 3, 2, False, 1.0, 0),
+    # groups that cut across a lane's experts, with two and four tokens to a warp
+    (67, 12, 1, "bf16", "softmax", False, 4, 1, 1, True, 2.5, 0),
+    (66, 60, 5, "f32", "sigmoid", True, 20, 7, 2, True, 1.0, 0.2),
+    (35, 96, 12, "bf16", "softmax", False, 32, 9, 1, True, 1.0, 0.3),
+    (35, 126, 3, "f32", "softmax", True, 2, 1, 2, False, 1.0, 0.1),
+    (37, 263, 11, "bf16", "softmax", False, 1, 1, 1, False, 1.0, 0.2),
+    (5, 777, 4, "f32", "sigmoid", True, 7, 2, 2, True, 1.0, 0.1),
 ]
 
 
@@ -174,6 +181,10 @@ def test_route_offsets_past_32_bits():
     (7, 1000, 9, "f32", "softmax", True, 0, True, True),
     (7, 512, 32, "f32", "sigmoid", True, 0.9, True, True),
     (9, 40, 3, "f32", "softmax", True, 0, False, True),
+    (37, 263, 11, "bf16", "softmax", False, 0.2, True, True),
+    (70, 12, 2, "bf16", "sigmoid", True, 0.2, True, True),
+    (33, 101, 9, "f32", "softmax", False, 0.1, True, True),
+    (6, 777, 30, "f32", "sigmoid", False, 0.1, True, True),
     (9, 40, 3, "f32", "sigmoid", True, 0, False, False),
 ])
 def test_route_backward(T, E, K, dtype, score, renorm, masked, dw, ds):
