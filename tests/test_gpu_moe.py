@@ -286,6 +286,12 @@ def _tables(rng, T, K, drop):
     (0, 2, 64, "bf16", 0, False, True), (3, 5, 10000, "bf16", 0, True, True),
     (9, 9, 1002, "bf16", 0.1, True, True), (9, 10, 2052, "bf16", 0.1, False, True), (9, 2, 4102, "f32", 0, True, True),
     (33, 17, 515, "f32", 0.1, True, True), (5000, 3, 264, "bf16", 0.1, True, True),
+    # rows between 16-byte boundaries: shorter than a block, around it, around 31 blocks, longer
+    (5, 3, 1, "bf16", 0, True, True), (6, 2, 2, "bf16", 0.1, True, True), (7, 4, 7, "bf16", 0.2, False, True),
+    (9, 5, 9, "bf16", 0, True, True), (8, 3, 3, "f32", 0.1, True, True), (11, 4, 241, "bf16", 0.1, True, True),
+    (11, 6, 247, "bf16", 0.1, True, True), (10, 9, 249, "bf16", 0, True, True), (12, 2, 1985, "bf16", 0.1, True, True),
+    (12, 2, 1991, "bf16", 0.1, False, True), (13, 3, 125, "f32", 0, True, True), (9, 2, 4001, "bf16", 0.3, True, True),
+    (6, 3, 6, "bf16", 0, True, False), (40, 8, 3311, "bf16", 0.1, True, True),
 ])
 def test_combine_and_backward(T, K, H, dtype, drop, residual, weighted):
     rng = np.random.default_rng(T + K * 31 + H)
@@ -329,6 +335,30 @@ def test_combine_in_place_residual_and_gather_gradient():
     want = mgw.moe_combine(y, dev_i32(row_of), weights=w, residual=res)
     got = mgw.moe_combine(y, dev_i32(row_of), weights=w, residual=res, out=res)
     assert got is res and torch.equal(got, want)
+    for width in (255, 130):   # rows between 16-byte boundaries
+        yo, ro = y[:, :width].contiguous(), torch.randn(50, width, device="cuda")
+        want = mgw.moe_combine(yo, dev_i32(row_of), weights=w, residual=ro)
+        assert torch.equal(mgw.moe_combine(yo, dev_i32(row_of), weights=w, residual=ro, out=ro), want)
+
+
+def test_combine_keeps_neighbouring_rows():
+    """A row of an odd width is stored without touching the rows beside it, and values beside the
+    matrices (NaN here) reach nothing."""
+    H = 333
+    base = torch.full((64 * H,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    y = base[:20 * H].view(20, H)
+    y.copy_(torch.randn(20, H, device="cuda"))
+    row_of = torch.tensor([[19, 0], [3, -1], [7, 11]], dtype=torch.int32, device="cuda")
+    out = torch.full((5, H), 9.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(3, 2, device="cuda")
+    mgw.moe_combine(y, row_of, weights=w, out=out[:3])
+    assert (out[3:] == 9).all() and torch.isfinite(out).all()
+    dy = torch.full((20, H), 9.0, dtype=torch.bfloat16, device="cuda")
+    _, dw = mgw.moe_combine_backward(torch.ones(3, H, dtype=torch.bfloat16, device="cuda"), y, row_of,
+                                     weights=w, dy=dy)
+    named = [0, 3, 7, 11, 19]
+    assert (dy[named] == 1).all() and torch.isfinite(dw).all()
+    assert (dy[[r for r in range(20) if r not in named]] == 9).all()
 
 
 def test_combine_reports_rows_out_of_range():
