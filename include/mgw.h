@@ -352,8 +352,8 @@ mgw_status mgw_grouped_dgrad_mxfp8(const void *dyq, const void *dys, const void 
  *             or with group_best 2 the sum of its two largest (of s + bias; of s without a
  *             bias); only experts of the top_groups best runs can be chosen
  *   expert_idx[t, :] = the top_k largest v in descending order, ties to the lower index
- *   weights[t, k] = scale * s_k, with renorm scale * s_k / sum of the chosen s (0 when that
- *             sum is 0); the bias moves the choice, never the weights
+ *   weights[t, k] = scale * s_k, with renorm scale * s_k / sum of the chosen s (never 0 / 0: the
+ *             scores may all be too small for fp32); the bias moves the choice, never the weights
  * An expert whose logit is -inf is masked for that token: its score is 0 and it is never
  * chosen.  Where fewer than top_k experts are left, the remaining slots are expert -1 with
  * weight 0 (mgw_moe_dispatch drops them).  A logit that is not a number counts as masked and

@@ -132,6 +132,15 @@ __device__ __forceinline__ void logistic(float x, float& s, float& c) {
   c = x >= 0.0f ? q * r : r;
 }
 
+// The same with the score divided by e^base, for base = min(the best chosen logit, 0): scores that
+// are only compared with each other (renormalised weights) then never all underflow.
+__device__ __forceinline__ void logistic_from(float x, float base, float& s, float& c) {
+  const float q = expf(-fabsf(x));
+  const float r = __fdividef(1.0f, 1.0f + q);
+  s = x >= 0.0f ? r : exp_from(x, base) * r;
+  c = x >= 0.0f ? q * r : r;
+}
+
 // This lane's V elements of its token's row of E: by 16-byte pieces where E is a multiple of V,
 // else one by one.  (Other rows through shared memory, read and written as one run: slower, 36
 // instead of 28 us for 40000 x 61 both ways, the lanes' sectors being in L1 anyway.)
@@ -436,7 +445,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
   // weights of the chosen, from their logits
   float w = 0.0f, xk = kNegInf;
   if (my_e >= 0) xk = load_logit(row + my_e);
-  if constexpr (SIGMOID) {
+  if constexpr (SIGMOID && RENORM) {
+    const float base = fminf(lanes_max<L>(xk), 0.0f);
+    float c;
+    if (my_e >= 0) logistic_from(xk, base, w, c);
+  } else if constexpr (SIGMOID) {
     float c;
     if (my_e >= 0) logistic(xk, w, c);
   } else if constexpr (RENORM) {
@@ -496,10 +509,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     float term = g;
     if constexpr (RENORM) {
       float p = 0.0f, c = 1.0f;
+      const float top = lanes_max<L>(xk);
       if constexpr (SIGMOID) {
-        if (e >= 0) logistic(xk, p, c);
+        if (e >= 0) logistic_from(xk, fminf(top, 0.0f), p, c);
       } else {
-        const float top = lanes_max<L>(xk);
         if (e >= 0) p = exp_from(xk, top);
       }
       const float sum = lanes_sum<L>(p);

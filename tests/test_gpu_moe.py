@@ -138,6 +138,29 @@ def test_route_extreme_logits():
             assert idx[6].tolist() == [2, 0, 4]
 
 
+def test_route_renormalised_logistic_scores_that_underflow():
+    """Renormalised logistic weights s_k / sum s where every s is below fp32's (and the last rows
+    below 64 bits') range: s = e^x / (1 + e^x), and e^x may be taken out of the quotient."""
+    rows = [[-89.0, -89.5, -90.25, -300.0], [-100.0, -101.0, -103.5, -120.0], [-150.0, -151.0, -150.5, -400.0],
+            [-1000.0, -1001.0, -1000.25, -2000.0], [-3.0e38, -3.0e38, -3.2e38, -3.3e38], [2.0, -1.0, -90.0, -200.0]]
+    x = np.array(rows)
+    idx, w = mgw.moe_route(dev(x, "f32"), 3, score=SCORE["sigmoid"], scale=2.5)
+    idx, w = idx.cpu().numpy(), f64(w)
+    x = np.float32(x).astype(np.float64)
+    g = np.float32(np.random.default_rng(3).standard_normal((len(x), 3)))
+    d = f64(mgw.moe_route_backward(dev(x, "f32"), dev_i32(idx), dev(g, "f32"), score=SCORE["sigmoid"], scale=2.5))
+    for t in range(len(x)):
+        assert sorted(idx[t]) == [0, 1, 2], t
+        xk = x[t][idx[t]]
+        up = np.exp(np.maximum(xk, -700)) * (xk > -700)
+        p = np.exp(np.maximum(xk - xk.max(), -700)) / (1 + up)
+        p /= p.sum()
+        assert np.all(np.abs(w[t] - 2.5 * p) <= 4e-6 * 2.5 * p + 1e-37), t
+        want = np.zeros(4)
+        want[idx[t]] = 2.5 * p * (g[t] - (p * g[t]).sum()) / (1 + up)
+        assert np.all(np.abs(d[t] - want) <= 1e-5 * 2.5 * np.abs(g[t]).max()), t
+
+
 def test_route_reports_a_logit_that_is_not_a_number():
     x = torch.zeros(3, 16, device="cuda")
     x[1, 5] = float("nan")
