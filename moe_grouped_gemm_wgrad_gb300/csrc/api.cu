@@ -668,8 +668,7 @@ mgw_status mgw_moe_route_backward(const void* logits, int dtype, int T, int E, i
 
 size_t mgw_moe_dispatch_workspace_bytes(int T, int top_k, int E) {
   if (T < 0 || top_k < 1 || top_k > MGW_MAX_TOP_K || E < 1 || E > MGW_MAX_EXPERTS) return 0;
-  const int blocks = mgw::dispatch_blocks(static_cast<long long>(T) * top_k, E);
-  return blocks > 1 ? sizeof(int) * static_cast<size_t>(blocks) * static_cast<size_t>(E) : 0;
+  return mgw::dispatch_workspace_bytes(static_cast<long long>(T) * top_k, E);
 }
 
 mgw_status mgw_moe_dispatch(const int32_t* expert_idx, int T, int top_k, int E, int32_t* expert_off,

@@ -10,12 +10,15 @@
 // over the runs and over the experts then gives every run's first row per expert.  No atomic
 // decides an order: the rows of an expert are its pairs in ascending order, on every run.
 //
-// Up to four groups of 32 pairs per warp one CTA does it all in one launch.  More pairs
-// go to several CTAs in two launches: CTA counts to the workspace, then each CTA ranks its own
-// pairs, adds up the counts of the CTAs before it and stores.  12 bytes a pair are far from
-// bounding it (1M pairs: 2 us); what does is the chain of phases within a CTA, so a CTA gets few
-// pairs (up to eight groups a warp, whose experts and ranks then stay in registers).  128 pairs
-// take 5 us, 65536 11, 1M pairs 19 (of 512 experts 28).
+// Up to two groups of 32 pairs per warp one CTA does it all.  Up to 65536 pairs (32768 of more
+// than 512 experts) a cluster of up to 16 CTAs does, whose CTAs read each other's counts from
+// shared memory: one launch and no workspace.  More pairs go to more CTAs in two launches: CTA
+// counts to the workspace, then each CTA ranks its own pairs, adds up the counts of the CTAs
+// before it and stores.  12 bytes a pair are far from bounding it (1M pairs: 2 us); what does is
+// the chain of phases within a CTA, so a CTA gets few pairs (up to eight groups a warp, whose
+// experts and ranks then stay in registers).  128 pairs take 5 us, 65536 11, 1M pairs 19 (of 512
+// experts 28).  The cluster takes as long as the two launches did (8 CTAs of twice the pairs: 4 us
+// longer), but the call returns 4.5 us sooner: 18 instead of 22.5 us a call at 65536.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -29,6 +32,9 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kHeld = 8;        // groups of 32 pairs a warp keeps in registers
 constexpr int kMaxBlocks = 1024;
+constexpr int kCluster = 16;    // CTAs of the one-launch form, at most
+constexpr int kClusterGroups = 4;  // groups of 32 pairs a warp takes in it, at most
+enum Mode { kOne, kClustered, kMany };
 
 // Warps per CTA: their E counters each share 64 KB.
 __host__ __device__ constexpr int warps_for(int E) { return E <= 512 ? 32 : 16; }
@@ -156,16 +162,25 @@ __global__ void __launch_bounds__(1024) dispatch_count_kernel(DispatchArgs a) {
     a.counts[static_cast<size_t>(blockIdx.x) * a.E + e] = s_cnt[e];
 }
 
-// Ranks and places this CTA's pairs.  ONE: the only CTA, whose counts are the totals.  HELD: a
-// warp's run is at most kHeld groups.
-template <bool ONE, bool HELD>
+__device__ __forceinline__ int ld_cluster(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// Ranks and places this CTA's pairs.  kOne: the only CTA, whose counts are the totals.
+// kClustered: the grid is one cluster, whose CTAs read each other's counts from shared memory.
+// kMany: all CTAs' counts are in the workspace.  HELD: a warp's run is at most kHeld groups.
+template <Mode MODE, bool HELD>
 __global__ void __launch_bounds__(1024) dispatch_place_kernel(DispatchArgs a) {
-  extern __shared__ int s_cnt[];  // counters [warps][stride], expert offsets [E + 1], first rows [E]
+  // counters [warps][stride], expert offsets [E + 1], first rows [E], this CTA's counts [E]
+  extern __shared__ int s_cnt[];
   __shared__ int s_seg[32];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id());
   const int stride = stride_for(a.E), bits = 32 - __clz(a.E - 1);
   int* s_off = s_cnt + warps * stride;
   int* s_first = s_off + a.E + 1;
+  int* s_mine = s_first + a.E;
   int* mine = s_cnt + warp * stride;
   for (int i = threadIdx.x; i < warps * stride; i += blockDim.x) s_cnt[i] = 0;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_off[e] = s_first[e] = 0;
@@ -190,9 +205,29 @@ __global__ void __launch_bounds__(1024) dispatch_place_kernel(DispatchArgs a) {
   __syncthreads();
   for (int e = warp; e < a.E; e += warps) {
     const int total = scan_column(s_cnt, warps, stride, e);
-    if (ONE && lane == 0) s_off[e] = total;
+    if (MODE == kOne && lane == 0) s_off[e] = total;
+    if (MODE == kClustered && lane == 0) s_mine[e] = total;
   }
-  if constexpr (!ONE) {
+  if constexpr (MODE == kClustered) {
+    cluster_sync();  // every CTA's counts are there
+    const int blocks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+      int c[kCluster], all = 0, before = 0;
+#pragma unroll
+      for (int b = 0; b < kCluster; ++b)
+        c[b] = b < blocks ? ld_cluster(map_to_cta(smem_u32(s_mine + e), static_cast<uint32_t>(b))) : 0;
+#pragma unroll
+      for (int b = 0; b < kCluster; ++b) {
+        all += c[b];
+        before += b < me ? c[b] : 0;
+      }
+      s_off[e] = all;
+      s_first[e] = before;
+    }
+    // read; waited for before the CTA ends
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  if constexpr (MODE == kMany) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the counting launch has finished
     // Totals over all CTAs, and over the CTAs before this one: every thread adds up a share of
     // one expert's column (integer sums, whose order does not matter).
@@ -247,40 +282,61 @@ __global__ void __launch_bounds__(1024) dispatch_place_kernel(DispatchArgs a) {
       place(p0 + lane, e, e >= 0 ? s_first[e] + rank : -1);
     }
   }
+  if constexpr (MODE == kClustered) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 size_t place_smem_bytes(int E) {
-  return sizeof(int) * (static_cast<size_t>(warps_for(E)) * stride_for(E) + 2 * static_cast<size_t>(E) + 1);
+  return sizeof(int) * (static_cast<size_t>(warps_for(E)) * stride_for(E) + 3 * static_cast<size_t>(E) + 1);
 }
 
-template <bool ONE, bool HELD>
+template <Mode MODE, bool HELD>
 cudaError_t launch_place(const DispatchArgs& a, int blocks, cudaStream_t stream) {
   static thread_local uint64_t attr_ctx = 0;
   const size_t max_smem = place_smem_bytes(512) > place_smem_bytes(kMaxExperts) ? place_smem_bytes(512)
                                                                                 : place_smem_bytes(kMaxExperts);
-  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(dispatch_place_kernel<ONE, HELD>),
-                                             max_smem, &attr_ctx);
+  const void* kernel = reinterpret_cast<const void*>(dispatch_place_kernel<MODE, HELD>);
+  if (MODE == kClustered && (attr_ctx == 0 || attr_ctx != current_context_id())) {
+    // clusters of more than eight CTAs have to be asked for, once per context as well
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
+  }
+  const cudaError_t err = set_smem_attr_once(kernel, max_smem, &attr_ctx);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(32 * warps_for(a.E)));
   cfg.dynamicSmemBytes = place_smem_bytes(a.E);
   cfg.stream = stream;
-  // After a counting launch, the placing one starts while that runs (programmatic dependent
-  // launch): it ranks its own pairs, and waits before it reads the table or writes anything.
   cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  if (MODE == kClustered) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(blocks);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+  } else {
+    // After a counting launch, the placing one starts while that runs (programmatic dependent
+    // launch): it ranks its own pairs, and waits before it reads the table or writes anything.
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = &attr;
-  cfg.numAttrs = ONE ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, dispatch_place_kernel<ONE, HELD>, a);
+  cfg.numAttrs = MODE == kOne ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, dispatch_place_kernel<MODE, HELD>, a);
 }
 
-}  // namespace
-
-int dispatch_blocks(long long pairs, int E) {
+// CTAs of a call that one launch does: one, or a cluster; 0 for calls that take two launches.
+int one_launch_blocks(long long pairs, int E) {
   const long long group = 32 * warps_for(E);  // pairs of one group per warp
-  if (pairs <= 4 * group) return 1;
+  if (pairs <= 2 * group) return 1;
+  // one, two or four groups a warp
+  for (int g = 1; g <= kClusterGroups; g *= 2)
+    if (pairs <= kCluster * g * group) return static_cast<int>((pairs + g * group - 1) / (g * group));
+  return 0;
+}
+
+// CTAs of the two launches.
+int many_blocks(long long pairs, int E) {
+  const long long group = 32 * warps_for(E);
   // one, two, four or eight groups a warp while that keeps the CTAs to the device's size
   for (int g = 1; g < kHeld; g *= 2)
     if (pairs <= 128 * g * group) return static_cast<int>((pairs + g * group - 1) / (g * group));
@@ -288,16 +344,25 @@ int dispatch_blocks(long long pairs, int E) {
   return static_cast<int>(b < kMaxBlocks ? b : kMaxBlocks);
 }
 
+}  // namespace
+
+size_t dispatch_workspace_bytes(long long pairs, int E) {
+  if (one_launch_blocks(pairs, E) > 0) return 0;
+  return sizeof(int) * static_cast<size_t>(many_blocks(pairs, E)) * static_cast<size_t>(E);
+}
+
 cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t stream) {
-  const int blocks = dispatch_blocks(a.pairs, a.E);
-  if (blocks == 1) return launch_place<true, true>(a, 1, stream);
+  const int few = one_launch_blocks(a.pairs, a.E);
+  if (few == 1) return launch_place<kOne, true>(a, 1, stream);
+  if (few > 1) return launch_place<kClustered, true>(a, few, stream);
+  const int blocks = many_blocks(a.pairs, a.E);
   const int threads = 32 * warps_for(a.E);
   dispatch_count_kernel<<<blocks, threads, sizeof(int) * a.E, stream>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   const long long groups = (static_cast<long long>(a.pairs) + 31) / 32;
   const bool held = (groups + blocks - 1) / blocks <= static_cast<long long>(kHeld) * warps_for(a.E);
-  return held ? launch_place<false, true>(a, blocks, stream) : launch_place<false, false>(a, blocks, stream);
+  return held ? launch_place<kMany, true>(a, blocks, stream) : launch_place<kMany, false>(a, blocks, stream);
 }
 
 }  // namespace mgw

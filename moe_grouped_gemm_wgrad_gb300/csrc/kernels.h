@@ -177,7 +177,7 @@ struct DispatchArgs {
   int pairs, top_k, E;
   int* status;
 };
-int dispatch_blocks(long long pairs, int E);
+size_t dispatch_workspace_bytes(long long pairs, int E);
 cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t stream);
 
 // Combine (combine.cu).

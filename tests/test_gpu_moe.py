@@ -262,6 +262,10 @@ def test_route_backward_bad_expert_is_reported():
     (4096, 8, 512, 0, 0), (30000, 7, 600, 0.3, 1), (131071, 8, 64, 0, 1), (50000, 3, 2, 1.0, 0),
     (200000, 6, 3, 0, 0), (8192, 1, 1, 0, 0), (8193, 1, 1000, 0, 0), (4096, 1, 512, 0, 0), (4097, 1, 512, 0, 1),
     (1100000, 4, 40, 0.01, 1), (1100001, 3, 1024, 0, 0), (1100000, 8, 40, 0.01, 1),
+    # around one CTA, clusters of 2 to 16 CTAs, and two launches; the last runs of CTAs empty
+    (2048, 1, 64, 0, 0), (2049, 1, 64, 0, 1), (683, 3, 64, 0.2, 0), (16384, 1, 64, 0, 0), (5462, 3, 64, 0, 1),
+    (4097, 8, 512, 0.1, 0), (8192, 8, 64, 0, 1), (8193, 8, 64, 0, 0), (512, 2, 513, 0, 0), (1025, 1, 1024, 0, 0),
+    (8193, 1, 600, 0.1, 1), (4096, 8, 1024, 0, 0), (32769, 1, 1024, 0, 0), (32769, 1, 1, 0, 0),
 ])
 def test_dispatch(T, K, E, drop, skew):
     rng = np.random.default_rng(T + K + E)
@@ -359,7 +363,7 @@ def test_combine_in_place_residual_and_gather_gradient():
     got = mgw.moe_combine(y, dev_i32(row_of), weights=w, residual=res, out=res)
     assert got is res and torch.equal(got, want)
     for width in (255, 130):   # rows between 16-byte boundaries
-        yo, ro = y[:, :width].contiguous(), torch.randn(50, width, device="cuda")
+        yo, ro = y[:, :width].contiguous(), dev(rng.standard_normal((50, width)), "f32")
         want = mgw.moe_combine(yo, dev_i32(row_of), weights=w, residual=ro)
         assert torch.equal(mgw.moe_combine(yo, dev_i32(row_of), weights=w, residual=ro, out=ro), want)
 
@@ -370,7 +374,7 @@ def test_combine_keeps_neighbouring_rows():
     H = 333
     base = torch.full((64 * H,), float("nan"), dtype=torch.bfloat16, device="cuda")
     y = base[:20 * H].view(20, H)
-    y.copy_(torch.randn(20, H, device="cuda"))
+    y.copy_(dev(np.random.default_rng(9).standard_normal((20, H)), "bf16"))
     row_of = torch.tensor([[19, 0], [3, -1], [7, 11]], dtype=torch.int32, device="cuda")
     out = torch.full((5, H), 9.0, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(3, 2, device="cuda")

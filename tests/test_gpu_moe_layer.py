@@ -61,6 +61,32 @@ def test_layer_matches_autograd(moe_ffn, tokens, hidden, ffn, experts, top_k):
         assert _rms_error(grads[name], v.grad) < 0.12, name
 
 
+@pytest.mark.parametrize("tokens,experts,top_k", [(1, 4, 4), (3, 8, 2), (65, 16, 5)])
+def test_router_gradient_of_the_layer_from_its_own_rows(moe_ffn, tokens, experts, top_k):
+    """The router's gradient against 64 bits on the expert outputs that the layer itself kept: of few
+    tokens it is a difference of nearly equal numbers, in which the quantization of those outputs
+    weighs more than in the other gradients.  Held to fp32's rounding of the terms before they
+    cancel: 256-term dot products (2^-24 * (256 / 8 + 16), as combine's), and a few roundings."""
+    layer = moe_ffn.MoeFfn(256, 256, experts, top_k, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    x, dout = (torch.randn(tokens, 256, generator=g, device="cuda").bfloat16() for _ in range(2))
+    layer.forward(x)
+    _, grads = layer.backward(dout)
+    _, logits, idx, _, _, _, row_of, _, _, y = layer.saved
+    dw = (y.double()[row_of.long()] * dout.double().unsqueeze(1)).sum(2)
+    mag = (y.double()[row_of.long()] * dout.double().unsqueeze(1)).abs().sum(2)
+    p = torch.softmax(logits.double().gather(1, idx.long()), 1)
+
+    def to_experts(d):
+        return torch.zeros(tokens, experts, dtype=torch.float64, device="cuda").scatter_(1, idx.long(), d)
+
+    want = to_experts(p * (dw - (p * dw).sum(1, keepdim=True))).t() @ x.double()
+    room = to_experts(p * (mag + (p * mag).sum(1, keepdim=True))).t() @ x.double().abs()
+    # the fp32 library product that sums over the tokens rounds at most once per term
+    tol = (2.0 ** -24 * (256 / 8 + 16) + 2.0 ** -24 * (tokens + 64)) * room
+    assert ((grads["router"].double() - want).abs() <= tol).all()
+
+
 def test_training_reduces_the_loss(moe_ffn):
     losses = moe_ffn.train(steps=12, tokens=1024)
     assert all(b < a for a, b in zip(losses, losses[1:]))
