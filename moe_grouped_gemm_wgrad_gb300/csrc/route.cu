@@ -10,7 +10,9 @@
 //
 // L lanes of a warp per token, V experts a lane: lane l of the token holds experts l V ..
 // l V + V - 1, so of equal values the lowest lane's is the lowest index.  Up to 256 experts
-// take V = 8 (one or two 16-byte loads) and L = 8, 16 or 32: four, two or one token per warp.
+// take V = 8 (one or two 16-byte loads) and L = 4, 8, 16 or 32: eight, four, two or one token per
+// warp, as few lanes as hold the experts, with up to two choices a lane (both ways, bf16 softmax:
+// 65536 x 8 top 2 30 -> 22 us against eight lanes, 40000 x 64 top 12 40 -> 26 against sixteen).
 // A lane sorts its eight keys once; each of the top_k rounds is then a maximum over the token's
 // lanes, one ballot, and a shift of the winning lane's list.  Beyond 256 experts a lane keeps its
 // 16 or 32 keys unsorted and looks through them when it wins.  bf16 logits without a bias fit
@@ -252,20 +254,23 @@ __device__ __forceinline__ void sort_packed(uint32_t (&key)[8]) {
   swap(1, 2), swap(3, 4), swap(5, 6);
 }
 
-// The token's top_k best of keys that each hold a 16-bit value above 65535 - its index; lane k
-// of the token gets the k-th.
+// Choices that a lane keeps: lane l of the token has the l-th, and with fewer than 32 lanes to a
+// token the (L + l)-th.
+template <int L>
+constexpr int kChoices = L < 32 ? 2 : 1;
+
+// The token's top_k best of keys that each hold a 16-bit value above 65535 - its index.
 template <int V, int L>
-__device__ __forceinline__ int pick_packed(uint32_t (&key)[V], int top_k, int sub) {
-  int my_e = -1;
+__device__ __forceinline__ void pick_packed(uint32_t (&key)[V], int top_k, int sub, int (&my_e)[kChoices<L>]) {
   if constexpr (V == 8) sort_packed(key);
   uint32_t head = key[0];
   if constexpr (V != 8) {
 #pragma unroll
     for (int j = 1; j < V; ++j) head = max(head, key[j]);
   }
-  for (int k = 0; k < top_k; ++k) {
+  auto round = [&](int k, int& mine) {
     const uint32_t best = lanes_max<L>(head);
-    if (sub == k && best != 0u) my_e = 65535 - static_cast<int>(best & 65535u);
+    if (sub == k && best != 0u) mine = 65535 - static_cast<int>(best & 65535u);
     const bool won = head == best;
     if constexpr (V == 8) {
 #pragma unroll
@@ -280,8 +285,10 @@ __device__ __forceinline__ int pick_packed(uint32_t (&key)[V], int top_k, int su
         head = max(head, key[j]);
       }
     }
-  }
-  return my_e;
+  };
+#pragma unroll
+  for (int r = 0; r < kChoices<L>; ++r)
+    for (int k = 0; k < min(top_k - r * L, L); ++k) round(k, my_e[r]);
 }
 
 template <typename T, int V, int L, bool SIGMOID, bool RENORM>
@@ -392,30 +399,35 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
         if (first + j < E && !((kept >> ((first + j) / per)) & 1u)) key[j] = 0u;
     }
   }
-  // lane k of the token keeps its k-th choice (top_k <= L)
-  int my_e = -1;
+  constexpr int R = kChoices<L>;
+  int my_e[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) my_e[r] = -1;
   if (std::is_same<T, __nv_bfloat16>::value && a.bias == nullptr) {
     // a bf16 value is the upper half of its fp32 key
 #pragma unroll
     for (int j = 0; j < V; ++j)
       key[j] = key[j] == 0u ? 0u : (key[j] & 0xffff0000u) | static_cast<uint32_t>(65535 - (first + j));
-    my_e = pick_packed<V, L>(key, a.top_k, sub);
+    pick_packed<V, L>(key, a.top_k, sub, my_e);
   } else if constexpr (V == 8) {
     int idx[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) idx[j] = j;
     sort_keys<V>(key, idx);
-    for (int k = 0; k < a.top_k; ++k) {
+    auto round = [&](int k, int& mine) {
       const uint32_t best = lanes_max<L>(key[0]);
       const int src = lowest_lane<L>(key[0] == best && best != 0u, lane);
       const int e = __shfl_sync(kAll, first + idx[0], src < 0 ? lane : src);
-      if (sub == k && src >= 0) my_e = e;
+      if (sub == k && src >= 0) mine = e;
       if (lane == src) {
 #pragma unroll
         for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1], idx[j] = idx[j + 1];
         key[V - 1] = 0u;
       }
-    }
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      for (int k = 0; k < min(a.top_k - r * L, L); ++k) round(k, my_e[r]);
   } else {
     uint32_t head = 0;
 #pragma unroll
@@ -439,32 +451,43 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
         }
       }
       pick = __shfl_sync(kAll, first + pick, src);
-      if (lane == k) my_e = pick;
+      if (lane == k) my_e[0] = pick;
     }
   }
   // weights of the chosen, from their logits
-  float w = 0.0f, xk = kNegInf;
-  if (my_e >= 0) xk = load_logit(row + my_e);
-  if constexpr (SIGMOID && RENORM) {
-    const float base = fminf(lanes_max<L>(xk), 0.0f);
+  const bool more = R > 1 && a.top_k > L;  // a lane's second choice counts
+  float w[R], xk[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    w[r] = 0.0f;
+    xk[r] = my_e[r] >= 0 ? load_logit(row + my_e[r]) : kNegInf;
+  }
+  float top = kNegInf;
+  if constexpr (RENORM) top = lanes_max<L>(R > 1 ? fmaxf(xk[0], xk[R - 1]) : xk[0]);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if ((r > 0 && !more) || my_e[r] < 0) continue;
     float c;
-    if (my_e >= 0) logistic_from(xk, base, w, c);
-  } else if constexpr (SIGMOID) {
-    float c;
-    if (my_e >= 0) logistic(xk, w, c);
-  } else if constexpr (RENORM) {
-    const float top = lanes_max<L>(xk);
-    if (my_e >= 0) w = exp_from(xk, top);
-  } else {
-    if (my_e >= 0) w = exp_from(xk, m) * inv;
+    if constexpr (SIGMOID && RENORM)
+      logistic_from(xk[r], fminf(top, 0.0f), w[r], c);
+    else if constexpr (SIGMOID)
+      logistic(xk[r], w[r], c);
+    else if constexpr (RENORM)
+      w[r] = exp_from(xk[r], top);
+    else
+      w[r] = exp_from(xk[r], m) * inv;
   }
   if constexpr (RENORM) {
-    const float sum = lanes_sum<L>(w);
-    w = sum > 0.0f ? w / sum : 0.0f;
+    const float sum = lanes_sum<L>(R > 1 ? w[0] + w[R - 1] : w[0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = sum > 0.0f ? w[r] / sum : 0.0f;
   }
-  if (live && sub < a.top_k) {
-    a.expert_idx[t * a.top_k + sub] = my_e;
-    a.weights[t * a.top_k + sub] = w * a.scale;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (live && sub + r * L < a.top_k) {
+      a.expert_idx[t * a.top_k + sub + r * L] = my_e[r];
+      a.weights[t * a.top_k + sub + r * L] = w[r] * a.scale;
+    }
   }
 }
 
@@ -485,11 +508,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   const Row<V, L> at{E, sub * V, live, E % V == 0};
   const T* row = static_cast<const T*>(a.logits) + t * E;
   // the chosen experts first: their logits' addresses depend on them
-  int e = -1;
-  float g = 0.0f, xk = kNegInf;
-  if (a.dweights != nullptr && live && sub < a.top_k) {
-    e = a.expert_idx[t * a.top_k + sub];
-    g = a.dweights[t * a.top_k + sub] * a.scale;
+  constexpr int R = kChoices<L>;
+  int e[R];
+  float g[R], xk[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    e[r] = -1, g[r] = 0.0f, xk[r] = kNegInf;
+    if (a.dweights != nullptr && live && sub + r * L < a.top_k) {
+      e[r] = a.expert_idx[t * a.top_k + sub + r * L];
+      g[r] = a.dweights[t * a.top_k + sub + r * L] * a.scale;
+    }
   }
   float x[V], s[V], add[V], G[V], m = 0.0f, inv = 0.0f;
 #pragma unroll
@@ -500,35 +528,47 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   const bool dense = !SIGMOID && (!RENORM || a.dscores != nullptr);
   // the chosen experts' terms: added to G (plain softmax) or straight to dx (the others)
   if (a.dweights != nullptr) {
-    if (e < -1 || e >= E) {
-      if (a.status != nullptr) atomicOr(a.status, kDevBadIndex);
-      e = -1;
-    }
-    if (e >= 0) xk = load_logit(row + e);
-    if (!(xk > kNegInf)) e = -1, g = 0.0f, xk = kNegInf;  // no expert, masked, or not a number
-    float term = g;
-    if constexpr (RENORM) {
-      float p = 0.0f, c = 1.0f;
-      const float top = lanes_max<L>(xk);
-      if constexpr (SIGMOID) {
-        if (e >= 0) logistic_from(xk, fminf(top, 0.0f), p, c);
-      } else {
-        if (e >= 0) p = exp_from(xk, top);
+    const bool more = R > 1 && a.top_k > L;
+    float term[R], p[R], c[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (e[r] < -1 || e[r] >= E) {
+        if (a.status != nullptr) atomicOr(a.status, kDevBadIndex);
+        e[r] = -1;
       }
-      const float sum = lanes_sum<L>(p);
-      p = sum > 0.0f ? p / sum : 0.0f;
-      term = p * (g - lanes_sum<L>(p * g));
-      if constexpr (SIGMOID) term *= c;
-    } else if constexpr (SIGMOID) {
-      float p, c;
-      logistic(xk, p, c);
-      term = g * p * c;
+      if (e[r] >= 0) xk[r] = load_logit(row + e[r]);
+      if (!(xk[r] > kNegInf)) e[r] = -1, g[r] = 0.0f, xk[r] = kNegInf;  // no expert, masked, or not a number
+      p[r] = 0.0f, c[r] = 1.0f;
+    }
+    float top = kNegInf;
+    if constexpr (RENORM) top = lanes_max<L>(R > 1 ? fmaxf(xk[0], xk[R - 1]) : xk[0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      term[r] = g[r];
+      if ((r > 0 && !more) || e[r] < 0) continue;
+      if constexpr (SIGMOID && RENORM)
+        logistic_from(xk[r], fminf(top, 0.0f), p[r], c[r]);
+      else if constexpr (SIGMOID)
+        logistic(xk[r], p[r], c[r]);
+      else if constexpr (RENORM)
+        p[r] = exp_from(xk[r], top);
+      if constexpr (SIGMOID && !RENORM) term[r] = g[r] * p[r] * c[r];
+    }
+    if constexpr (RENORM) {
+      const float sum = lanes_sum<L>(R > 1 ? p[0] + p[R - 1] : p[0]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) p[r] = sum > 0.0f ? p[r] / sum : 0.0f;
+      const float dot = lanes_sum<L>(R > 1 ? p[0] * g[0] + p[R - 1] * g[R - 1] : p[0] * g[0]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) term[r] = p[r] * (g[r] - dot) * c[r];
     }
     float* mine = s_add[warp] + lane * V;
 #pragma unroll
     for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(mine + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
-    if (e >= 0) s_add[warp][(lane - sub) * V + e] = term;  // a token's experts differ
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (e[r] >= 0) s_add[warp][(lane - sub) * V + e[r]] = term[r];  // a token's experts differ
     __syncwarp();
     load_vec<V>(mine, add);
   }
@@ -585,8 +625,9 @@ cudaError_t by_mode(const Args& a, bool sigmoid, bool renorm, cudaStream_t s) {
 
 template <typename T, typename Args>
 cudaError_t by_width(const Args& a, bool sigmoid, bool renorm, cudaStream_t s) {
-  if (a.E <= 64 && a.top_k <= 8) return by_mode<T, 8, 8>(a, sigmoid, renorm, s);
-  if (a.E <= 128 && a.top_k <= 16) return by_mode<T, 8, 16>(a, sigmoid, renorm, s);
+  if (a.E <= 32 && a.top_k <= 8) return by_mode<T, 8, 4>(a, sigmoid, renorm, s);
+  if (a.E <= 64 && a.top_k <= 16) return by_mode<T, 8, 8>(a, sigmoid, renorm, s);
+  if (a.E <= 128) return by_mode<T, 8, 16>(a, sigmoid, renorm, s);
   if (a.E <= 256) return by_mode<T, 8, 32>(a, sigmoid, renorm, s);
   if (a.E <= 512) return by_mode<T, 16, 32>(a, sigmoid, renorm, s);
   return by_mode<T, 32, 32>(a, sigmoid, renorm, s);

@@ -81,6 +81,19 @@ ROUTES = [
     (35, 126, 3, "f32", "softmax", True, 2, 1, 2, False, 1.0, 0.1),
     (37, 263, 11, "bf16", "softmax", False, 1, 1, 1, False, 1.0, 0.2),
     (5, 777, 4, "f32", "sigmoid", True, 7, 2, 2, True, 1.0, 0.1),
+    # four, eight and sixteen lanes to a token, with one choice a lane and with two
+    (41, 8, 2, "bf16", "softmax", False, 1, 1, 1, True, 1.0, 0.1),
+    (70, 32, 8, "f32", "sigmoid", True, 1, 1, 1, True, 2.5, 0.2),
+    (39, 31, 5, "bf16", "softmax", False, 1, 1, 1, False, 1.0, 0.1),
+    (63, 32, 6, "f32", "softmax", True, 4, 2, 2, True, 1.0, 0.2),
+    (63, 32, 3, "bf16", "sigmoid", False, 2, 1, 1, False, 1.0, 0.1),
+    (50, 24, 7, "bf16", "sigmoid", True, 8, 5, 2, True, 1.0, 0.2),
+    (44, 28, 10, "bf16", "sigmoid", True, 2, 2, 1, True, 1.0, 0.1),
+    (37, 64, 16, "f32", "softmax", False, 8, 4, 1, True, 1.0, 0.1),
+    (37, 61, 9, "bf16", "softmax", False, 1, 1, 1, False, 2.5, 0.9),
+    (21, 128, 32, "bf16", "softmax", False, 1, 1, 1, True, 1.0, 0.1),
+    (21, 100, 17, "f32", "sigmoid", False, 4, 3, 1, True, 1.0, 0.5),
+    (19, 9, 9, "f32", "softmax", True, 1, 1, 1, False, 1.0, 0.3),
 ]
 
 
@@ -209,6 +222,9 @@ def test_route_offsets_past_32_bits():
     (33, 101, 9, "f32", "softmax", False, 0.1, True, True),
     (6, 777, 30, "f32", "sigmoid", False, 0.1, True, True),
     (9, 40, 3, "f32", "sigmoid", True, 0, False, False),
+    (45, 28, 10, "bf16", "sigmoid", True, 0.1, True, True), (37, 20, 8, "f32", "softmax", True, 0.2, True, True),
+    (19, 128, 32, "f32", "softmax", True, 0, True, False), (23, 64, 13, "f32", "sigmoid", False, 0, True, False),
+    (66, 8, 5, "bf16", "softmax", False, 0.1, True, True), (17, 100, 17, "f32", "sigmoid", True, 0, True, True),
 ])
 def test_route_backward(T, E, K, dtype, score, renorm, masked, dw, ds):
     rng = np.random.default_rng(T + E * 7)
