@@ -270,28 +270,10 @@ def _one_device(*ts) -> torch.device:
     return dev
 
 
-# torch's allocation of a CUDA tensor without its general argument parsing and dispatch (what the
-# code that torch generates calls): 0.9 instead of 1.5 us by itself, and with the code that is not
-# run 1.2 to 1.5 us a tensor less of a call (router of 4 tokens: 15.8 -> 12.9 us).
-_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
-                      "_empty_strided_cuda", None)
-
-
-def _empty(shape, dtype, dev: torch.device) -> torch.Tensor:
-    """A new contiguous tensor on ``dev``."""
-    if (_empty_cuda is not None and dev.index is not None and len(shape) <= 2
-            and torch._C._cuda_getDevice() == dev.index):
-        try:
-            return _empty_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
-        except RuntimeError:
-            pass  # a size that torch.empty refuses in clearer words, or no memory
-    return torch.empty(shape, dtype=dtype, device=dev)
-
-
 def _out(t: torch.Tensor | None, shape, dtype, dev, name: str) -> torch.Tensor:
     """The caller's output buffer after checks, or a new one of ``shape``."""
     if t is None:
-        return _empty(shape, dtype, dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
     n = 1
     for d in shape:
         n *= int(d)
