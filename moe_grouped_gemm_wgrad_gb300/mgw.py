@@ -10,6 +10,11 @@ library cannot: dtype, contiguity, one device for all operands, and that every
 caller-supplied buffer holds at least the elements the call reads or writes.  A
 failed check raises :class:`MgwError` before anything is launched.  Each call runs
 with the operands' device current.
+
+A call runs on the current stream, or on ``stream`` where that is given.  What it allocates
+then belongs to ``stream``'s pool, and its tensors are recorded as in use on both streams,
+so they may be dropped at any time.  Order between the streams is the caller's: ``stream``
+has to wait for whoever writes the operands, and whoever reads the results for ``stream``.
 """
 from __future__ import annotations
 
@@ -277,10 +282,15 @@ def _one_device(*ts) -> torch.device:
     return dev
 
 
-def _out(t: torch.Tensor | None, shape, dtype, dev, name: str) -> torch.Tensor:
-    """The caller's output buffer after checks, or a new one of ``shape``."""
+def _out(t: torch.Tensor | None, shape, dtype, dev, name: str, side=None) -> torch.Tensor:
+    """The caller's output or workspace buffer after checks, or a new one of ``shape``: from the pool
+    of the stream ``side`` that the call runs on, if that is not the current one.  Memory of the
+    current stream's pool may still be in use by work queued there, for which ``side`` does not wait."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        if side is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(side):
+            return torch.empty(shape, dtype=dtype, device=dev)
     n = 1
     for d in shape:
         n *= int(d)
@@ -289,15 +299,34 @@ def _out(t: torch.Tensor | None, shape, dtype, dev, name: str) -> torch.Tensor:
     return t
 
 
-_SAME_DEVICE = contextlib.nullcontext()
+_AS_IT_IS = contextlib.nullcontext()
 
 
 def _device(dev: torch.device):
     """Makes ``dev`` the current CUDA device for the call (the library launches on, and
     sizes its grids for, the current device)."""
     if torch.cuda.current_device() == dev.index:
-        return _SAME_DEVICE
+        return _AS_IT_IS
     return torch.cuda.device(dev)
+
+
+def _side(stream, dev: torch.device):
+    """``stream`` as a torch stream where it is not ``dev``'s current one, else None."""
+    handle = stream.cuda_stream
+    here = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev.index)
+    if handle == here:
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+
+
+def _used_on(side, *ts) -> None:
+    """Tells the allocator that the tensors of a call on ``side`` are in use there and on the current
+    stream, so that memory that the host frees meanwhile is handed out again only when both streams
+    are past this point."""
+    for t in ts:
+        if t is not None:
+            t.record_stream(side)
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def token_capacity(M: int, E: int) -> int:
@@ -319,12 +348,15 @@ def mxfp8_quantize(src: torch.Tensor, expert_off: torch.Tensor, Mcap: int | None
     M, C = src.shape
     Mcap = token_capacity(M, E) if Mcap is None else int(Mcap)
     dev = _one_device(src, expert_off, q, scales, status)
-    q = _out(q, (C, Mcap), torch.uint8, dev, "q")
-    scales = _out(scales, (scale_bytes(C, Mcap),), torch.uint8, dev, "scales")
+    side = None if stream is None else _side(stream, dev)
+    q = _out(q, (C, Mcap), torch.uint8, dev, "q", side)
+    scales = _out(scales, (scale_bytes(C, Mcap),), torch.uint8, dev, "scales", side)
     with _device(dev):
         st = load().mgw_mxfp8_quantize(_ptr(src), M, C, _ptr(expert_off), E, _ptr(q), _ptr(scales),
                                        Mcap, int(scale_rule), _ptr(status), _stream(stream))
     _check(st, "mgw_mxfp8_quantize")
+    if side is not None:
+        _used_on(side, src, expert_off, q, scales, status)
     return q, scales
 
 
@@ -342,13 +374,16 @@ def mxfp8_quantize_gather(src: torch.Tensor, row_index: torch.Tensor, expert_off
     M = row_index.numel()
     Mcap = token_capacity(M, E) if Mcap is None else int(Mcap)
     dev = _one_device(src, row_index, expert_off, q, scales, status)
-    q = _out(q, (C, Mcap), torch.uint8, dev, "q")
-    scales = _out(scales, (scale_bytes(C, Mcap),), torch.uint8, dev, "scales")
+    side = None if stream is None else _side(stream, dev)
+    q = _out(q, (C, Mcap), torch.uint8, dev, "q", side)
+    scales = _out(scales, (scale_bytes(C, Mcap),), torch.uint8, dev, "scales", side)
     with _device(dev):
         st = load().mgw_mxfp8_quantize_gather(_ptr(src), src_rows, _ptr(row_index), M, C,
                                               _ptr(expert_off), E, _ptr(q), _ptr(scales), Mcap,
                                               int(scale_rule), _ptr(status), _stream(stream))
     _check(st, "mgw_mxfp8_quantize_gather")
+    if side is not None:
+        _used_on(side, src, row_index, expert_off, q, scales, status)
     return q, scales
 
 
@@ -375,12 +410,15 @@ def grouped_wgrad_mxfp8(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor, xs
                         status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """grad_w [E*N, K] bf16 from quantized g^T (N rows) and x^T (K rows)."""
     E, N, K, Mcap, dev = _wgrad_operands(gq, gs, xq, xs, expert_off, status, out)
-    out = _out(out, (E * N, K), torch.bfloat16, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (E * N, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_wgrad_mxfp8(_ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs),
                                             _ptr(expert_off), E, int(M), N, K, Mcap, _ptr(out),
                                             _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_wgrad_mxfp8")
+    if side is not None:
+        _used_on(side, gq, gs, xq, xs, expert_off, out, status)
     return out
 
 
@@ -403,12 +441,15 @@ def grouped_wgrad_mxfp8_balanced(gq: torch.Tensor, gs: torch.Tensor, xq: torch.T
     (see :func:`wgrad_workspace`); calls sharing it must not overlap."""
     _dev_tensor(workspace, torch.uint8, "workspace")
     E, N, K, Mcap, dev = _wgrad_operands(gq, gs, xq, xs, expert_off, status, out, workspace)
-    out = _out(out, (E * N, K), torch.bfloat16, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (E * N, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_wgrad_mxfp8_balanced(
             _ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs), _ptr(expert_off), E, int(M), N, K, Mcap,
             _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_wgrad_mxfp8_balanced")
+    if side is not None:
+        _used_on(side, gq, gs, xq, xs, expert_off, workspace, out, status)
     return out
 
 
@@ -420,12 +461,15 @@ def grouped_wgrad_mxfp8_balanced_noalloc(gq: torch.Tensor, gs: torch.Tensor, xq:
     """As :func:`grouped_wgrad_mxfp8_balanced` on the library's own workspace (a device array
     in the library; nothing is allocated, calls must not overlap)."""
     E, N, K, Mcap, dev = _wgrad_operands(gq, gs, xq, xs, expert_off, status, out)
-    out = _out(out, (E * N, K), torch.bfloat16, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (E * N, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_wgrad_mxfp8_balanced_noalloc(
             _ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs), _ptr(expert_off), E, int(M), N, K, Mcap,
             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_wgrad_mxfp8_balanced_noalloc")
+    if side is not None:
+        _used_on(side, gq, gs, xq, xs, expert_off, out, status)
     return out
 
 
@@ -442,11 +486,14 @@ def grouped_dgrad_f32(dy: torch.Tensor, W: torch.Tensor, expert_off: torch.Tenso
     _offsets(expert_off, E)
     _status(status)
     dev = _one_device(dy, W, expert_off, out, status)
-    out = _out(out, (rows, in_f), torch.float32, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (rows, in_f), torch.float32, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_dgrad_f32(_ptr(dy), _ptr(W), _ptr(expert_off), E, rows, out_f,
                                           in_f, _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_dgrad_f32")
+    if side is not None:
+        _used_on(side, dy, W, expert_off, out, status)
     return out
 
 
@@ -468,13 +515,16 @@ def mxfp8_quantize_rows(src: torch.Tensor, expert_off: torch.Tensor, Mcap: int |
         M = src_rows
     Mcap = token_capacity(M, E) if Mcap is None else int(Mcap)
     dev = _one_device(src, expert_off, row_index, q, scales, status)
-    q = _out(q, (Mcap, C), torch.uint8, dev, "q")
-    scales = _out(scales, (scale_bytes(C, Mcap),), torch.uint8, dev, "scales")
+    side = None if stream is None else _side(stream, dev)
+    q = _out(q, (Mcap, C), torch.uint8, dev, "q", side)
+    scales = _out(scales, (scale_bytes(C, Mcap),), torch.uint8, dev, "scales", side)
     with _device(dev):
         st = load().mgw_mxfp8_quantize_rows(_ptr(src), src_rows, _ptr(row_index), M, C,
                                             _ptr(expert_off), E, _ptr(q), _ptr(scales), Mcap,
                                             int(scale_rule), _ptr(status), _stream(stream))
     _check(st, "mgw_mxfp8_quantize_rows")
+    if side is not None:
+        _used_on(side, src, expert_off, row_index, q, scales, status)
     return q, scales
 
 
@@ -496,12 +546,15 @@ def grouped_fprop_mxfp8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws
     _need(xs, scale_bytes(K, Mcap), "xs")
     _need(ws, scale_bytes(K, Mw), "ws")
     dev = _one_device(xq, xs, wq, ws, expert_off, out, status)
-    out = _out(out, (int(M), int(N)), torch.bfloat16, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (int(M), int(N)), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_fprop_mxfp8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws),
                                             _ptr(expert_off), E, int(M), int(N), K, Mcap, Mw,
                                             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_fprop_mxfp8")
+    if side is not None:
+        _used_on(side, xq, xs, wq, ws, expert_off, out, status)
     return out
 
 
@@ -522,12 +575,15 @@ def grouped_dgrad_mxfp8(dyq: torch.Tensor, dys: torch.Tensor, wtq: torch.Tensor,
     _need(dys, scale_bytes(N, Mcap), "dys")
     _need(wts, scale_bytes(K, Mw), "wts")
     dev = _one_device(dyq, dys, wtq, wts, expert_off, out, status)
-    out = _out(out, (int(M), K), torch.bfloat16, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (int(M), K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_dgrad_mxfp8(_ptr(dyq), _ptr(dys), _ptr(wtq), _ptr(wts),
                                             _ptr(expert_off), E, int(M), N, K, Mcap, Mw,
                                             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_dgrad_mxfp8")
+    if side is not None:
+        _used_on(side, dyq, dys, wtq, wts, expert_off, out, status)
     return out
 
 
@@ -548,15 +604,6 @@ def _shaped(t: torch.Tensor, shape, dtype, name: str) -> None:
     _dev_tensor(t, dtype, name, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise MgwError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _used_on(stream, *ts) -> None:
-    """Tells the allocator that tensors of the current stream's pool are in use on ``stream``,
-    so that their memory is not handed out again before that stream's work on them is done."""
-    if stream is not None:
-        for t in ts:
-            if t is not None and t.is_cuda:
-                t.record_stream(stream)
 
 
 def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None,
@@ -583,17 +630,19 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
         _shaped(bias, (E,), torch.float32, "bias")
     _status(status)
     dev = _one_device(logits, bias, expert_idx, weights, scores, status)
-    expert_idx = _out(expert_idx, (T, top_k), torch.int32, dev, "expert_idx")
-    weights = _out(weights, (T, top_k), torch.float32, dev, "weights")
+    side = None if stream is None else _side(stream, dev)
+    expert_idx = _out(expert_idx, (T, top_k), torch.int32, dev, "expert_idx", side)
+    weights = _out(weights, (T, top_k), torch.float32, dev, "weights", side)
     if with_scores or scores is not None:
-        scores = _out(scores, (T, E), torch.float32, dev, "scores")
+        scores = _out(scores, (T, E), torch.float32, dev, "scores", side)
     with _device(dev):
         st = load().mgw_moe_route(_ptr(logits), dt, T, E, _ptr(bias), top_k, int(score),
                                   int(groups), int(top_groups), int(group_best), int(bool(renorm)),
                                   float(scale), _ptr(expert_idx), _ptr(weights), _ptr(scores),
                                   _ptr(status), _stream(stream))
     _check(st, "mgw_moe_route")
-    _used_on(stream, expert_idx, weights, scores)
+    if side is not None:
+        _used_on(side, logits, bias, expert_idx, weights, scores, status)
     return (expert_idx, weights) if scores is None else (expert_idx, weights, scores)
 
 
@@ -617,14 +666,16 @@ def moe_route_backward(logits: torch.Tensor, expert_idx: torch.Tensor,
         _shaped(dscores, (T, E), torch.float32, "dscores")
     _status(status)
     dev = _one_device(logits, expert_idx, dweights, dscores, dlogits, status)
-    dlogits = _out(dlogits, (T, E), logits.dtype, dev, "dlogits")
+    side = None if stream is None else _side(stream, dev)
+    dlogits = _out(dlogits, (T, E), logits.dtype, dev, "dlogits", side)
     with _device(dev):
         st = load().mgw_moe_route_backward(_ptr(logits), dt, T, E, top_k, int(score),
                                            int(bool(renorm)), float(scale), _ptr(expert_idx),
                                            _ptr(dweights), _ptr(dscores), _ptr(dlogits),
                                            _ptr(status), _stream(stream))
     _check(st, "mgw_moe_route_backward")
-    _used_on(stream, dlogits)
+    if side is not None:
+        _used_on(side, logits, expert_idx, dweights, dscores, dlogits, status)
     return dlogits
 
 
@@ -648,18 +699,20 @@ def moe_dispatch(expert_idx: torch.Tensor, E: int, expert_off: torch.Tensor | No
     dev = _one_device(expert_idx, expert_off, row_index, row_of, workspace, status)
     lib = load()
     need = int(lib.mgw_moe_dispatch_workspace_bytes(T, top_k, E))
-    workspace = _out(workspace, (need,), torch.uint8, dev, "workspace") \
+    side = None if stream is None else _side(stream, dev)
+    workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side) \
         if need or workspace is not None else None
-    expert_off = _out(expert_off, (E + 1,), torch.int32, dev, "expert_off")
-    row_index = _out(row_index, (T * top_k,), torch.int32, dev, "row_index")
-    row_of = _out(row_of, (T, top_k), torch.int32, dev, "row_of")
+    expert_off = _out(expert_off, (E + 1,), torch.int32, dev, "expert_off", side)
+    row_index = _out(row_index, (T * top_k,), torch.int32, dev, "row_index", side)
+    row_of = _out(row_of, (T, top_k), torch.int32, dev, "row_of", side)
     with _device(dev):
         st = lib.mgw_moe_dispatch(_ptr(expert_idx), T, top_k, E, _ptr(expert_off), _ptr(row_index),
                                   _ptr(row_of), _ptr(workspace),
                                   0 if workspace is None else workspace.numel(), _ptr(status),
                                   _stream(stream))
     _check(st, "mgw_moe_dispatch")
-    _used_on(stream, expert_off, row_index, row_of, workspace)
+    if side is not None:
+        _used_on(side, expert_idx, expert_off, row_index, row_of, workspace, status)
     return expert_off, row_index, row_of
 
 
@@ -692,15 +745,17 @@ def grouped_fprop_mxfp8_act(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor
     if residual is not None:
         _shaped(residual, (M, F), torch.bfloat16, "residual")
     dev = _one_device(xq, xs, wq, ws, expert_off, bias, residual, out, preact, status)
-    out = _out(out, (M, F), torch.bfloat16, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (M, F), torch.bfloat16, dev, "out", side)
     if save_preact or preact is not None:
-        preact = _out(preact, (M, N), torch.bfloat16, dev, "preact")
+        preact = _out(preact, (M, N), torch.bfloat16, dev, "preact", side)
     with _device(dev):
         st = load().mgw_grouped_fprop_mxfp8_act(
             _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(expert_off), E, M, N, K, Mcap, Mw, act,
             _ptr(bias), _ptr(residual), _ptr(out), _ptr(preact), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_fprop_mxfp8_act")
-    _used_on(stream, out, preact)
+    if side is not None:
+        _used_on(side, xq, xs, wq, ws, expert_off, bias, residual, out, preact, status)
     return out if preact is None else (out, preact)
 
 
@@ -726,21 +781,23 @@ def grouped_act_backward(dy: torch.Tensor, z: torch.Tensor | None, expert_off: t
     E = _offsets(expert_off)
     _status(status)
     dev = _one_device(dy, z, expert_off, dz, dbias, workspace, status)
+    side = None if stream is None else _side(stream, dev)
     if act != ACT_NONE:
-        dz = _out(dz, (M, N), torch.bfloat16, dev, "dz")
+        dz = _out(dz, (M, N), torch.bfloat16, dev, "dz", side)
     lib = load()
     if with_dbias or dbias is not None:
-        dbias = _out(dbias, (E, N), torch.float32, dev, "dbias")
+        dbias = _out(dbias, (E, N), torch.float32, dev, "dbias", side)
         need = int(lib.mgw_grouped_act_backward_workspace_bytes(E, M, N))
         if need or workspace is not None:
-            workspace = _out(workspace, (need,), torch.uint8, dev, "workspace")
+            workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side)
     with _device(dev):
         st = lib.mgw_grouped_act_backward(_ptr(dy), _ptr(z), _ptr(expert_off), E, M, N, act,
                                           _ptr(dz), _ptr(dbias), _ptr(workspace),
                                           0 if workspace is None else workspace.numel(),
                                           _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_act_backward")
-    _used_on(stream, dz, dbias, workspace)
+    if side is not None:
+        _used_on(side, dy, z, expert_off, dz, dbias, workspace, status)
     return (dy if act == ACT_NONE else dz), dbias
 
 
@@ -761,12 +818,14 @@ def moe_combine(y: torch.Tensor, row_of: torch.Tensor, weights: torch.Tensor | N
         _shaped(residual, (T, H), y.dtype, "residual")
     _status(status)
     dev = _one_device(y, row_of, weights, residual, out, status)
-    out = _out(out, (T, H), y.dtype, dev, "out")
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (T, H), y.dtype, dev, "out", side)
     with _device(dev):
         st = load().mgw_moe_combine(_ptr(y), dt, M, _ptr(row_of), _ptr(weights), _ptr(residual), T,
                                     top_k, H, _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_moe_combine")
-    _used_on(stream, out)
+    if side is not None:
+        _used_on(side, y, row_of, weights, residual, out, status)
     return out
 
 
@@ -799,13 +858,15 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: tor
     M = int(M)
     _status(status)
     dev = _one_device(dout, y, row_of, weights, dy, dweights, status)
-    dy = _out(dy, (M, H), dout.dtype, dev, "dy")
+    side = None if stream is None else _side(stream, dev)
+    dy = _out(dy, (M, H), dout.dtype, dev, "dy", side)
     if weights is not None:
-        dweights = _out(dweights, (T, top_k), torch.float32, dev, "dweights")
+        dweights = _out(dweights, (T, top_k), torch.float32, dev, "dweights", side)
     with _device(dev):
         st = load().mgw_moe_combine_backward(_ptr(dout), _ptr(y), dt, M, _ptr(row_of),
                                              _ptr(weights), T, top_k, H, _ptr(dy), _ptr(dweights),
                                              _ptr(status), _stream(stream))
     _check(st, "mgw_moe_combine_backward")
-    _used_on(stream, dy, dweights)
+    if side is not None:
+        _used_on(side, dout, y, row_of, weights, dy, dweights, status)
     return dy, dweights
