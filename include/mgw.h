@@ -430,6 +430,9 @@ mgw_status mgw_grouped_fprop_mxfp8_act(const void *xq, const void *xs, const voi
  *              0 for an expert without rows)
  * (dz then goes to the quantizers of the data and weight gradients; the residual's gradient is
  * dy.)
+ * A z that is not a number makes its dz, and that expert's dbias of the column, none either,
+ * whatever the activation.  An infinite z has relu's slopes, 1 and 0; gelu's and silu's formulas
+ * multiply infinity by 0 there: not a number.
  * dy_bf16    device, bf16 [M, F].
  * z_bf16     device, bf16 [M, N]; null for MGW_ACT_NONE.
  * N          a positive multiple of 128 (of 256 for the gated activations), at most 2^20.

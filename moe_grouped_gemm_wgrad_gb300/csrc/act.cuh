@@ -1,5 +1,5 @@
 // Activations of the expert products and their slopes, in fp32.
-//   relu(x) = max(x, 0), slope 0 at 0
+//   relu(x) = max(x, 0), slope 0 at 0; NaN has neither a value nor a slope
 //   gelu(x) = x Phi(x), Phi the normal distribution function; slope Phi(x) + x phi(x)
 //   silu(x) = x s(x), s the logistic function; slope s(x) (1 + x (1 - s(x)))
 //   swiglu, geglu: silu or gelu of the gate times the up value (two halves of the product's
@@ -129,7 +129,7 @@ template <int ACT>
 __device__ __forceinline__ void act_value_slope(float x, float& value, float& slope) {
   if constexpr (ACT == kActRelu) {
     value = x <= 0.0f ? 0.0f : x;
-    slope = x > 0.0f ? 1.0f : 0.0f;
+    slope = x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;  // NaN stays NaN
   } else if constexpr (ACT == kActGelu) {
     float e;
     const float h = normal_tail(x, e);
