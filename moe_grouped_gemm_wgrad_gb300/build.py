@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmgw.so")
 # Test build: the same objects, except the C ABI compiled with MGW_TEST_HOOKS, which lets
-# the device time-limit test make a pipeline stage that never fills (MGW_TEST_DROP_LOAD=1).
+# the device time-limit test make a pipeline stage that never fills (MGW_TEST_DROP_LOAD=1),
+# and a test of contexts with few SMs limit the clusters in use (MGW_TEST_MAX_CLUSTER).
 # libmgw.so itself has no such switch.
 LIB_TESTHOOKS = os.path.join(HERE, "libmgw_testhooks.so")
 # Diagnostic build (include/mgw_diag.h): the wgrad and fp32 dgrad kernels and the C ABI

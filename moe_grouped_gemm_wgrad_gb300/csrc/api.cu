@@ -697,6 +697,14 @@ mgw_status mgw_moe_dispatch(const int32_t* expert_idx, int T, int top_k, int E, 
   a.pairs = static_cast<int>(pairs);
   a.top_k = top_k;
   a.E = E;
+  a.max_cluster = 0;
+#ifdef MGW_TEST_HOOKS
+  {
+    // Only in the test build of the library (libmgw_testhooks.so), see kernels.h.
+    const char* v = std::getenv("MGW_TEST_MAX_CLUSTER");
+    a.max_cluster = v != nullptr ? std::atoi(v) : 0;
+  }
+#endif
   a.status = status_dev;
   const cudaError_t err = mgw::launch_dispatch(a, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;

@@ -17,8 +17,10 @@
 // before it and stores.  12 bytes a pair are far from bounding it (1M pairs: 2 us); what does is
 // the chain of phases within a CTA, so a CTA gets few pairs (up to eight groups a warp, whose
 // experts and ranks then stay in registers).  128 pairs take 5 us, 65536 11, 1M pairs 19 (of 512
-// experts 28).  The cluster takes as long as the two launches did (8 CTAs of twice the pairs: 4 us
-// longer), but the call returns 4.5 us sooner: 18 instead of 22.5 us a call at 65536.
+// experts 28).  The cluster takes as long as the two launches did, but the call returns 4.5 us
+// sooner: 18 instead of 22.5 us a call at 65536.  Where a context cannot run 16 CTAs as a cluster
+// (a share of the SMs), eight take the same calls with up to eight groups a warp, or one CTA does
+// in two passes: 65536 pairs of 64 experts 9, 13 and 82 us, 16384 pairs 6, 7 and 23.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -289,18 +291,49 @@ size_t place_smem_bytes(int E) {
   return sizeof(int) * (static_cast<size_t>(warps_for(E)) * stride_for(E) + 3 * static_cast<size_t>(E) + 1);
 }
 
+size_t max_place_smem() {
+  return place_smem_bytes(512) > place_smem_bytes(kMaxExperts) ? place_smem_bytes(512)
+                                                               : place_smem_bytes(kMaxExperts);
+}
+
+// The largest cluster, of 16 or 8 CTAs, that the current context can run; 1 when it can run
+// neither (a process may have a share of the SMs only).  Asked once per context and thread.
+int largest_cluster() {
+  static thread_local uint64_t attr_ctx = 0;
+  static thread_local int largest = 0;
+  if (attr_ctx != 0 && attr_ctx == current_context_id()) return largest;
+  const void* kernel = reinterpret_cast<const void*>(dispatch_place_kernel<kClustered, true>);
+  largest = 1;
+  // clusters of more than eight CTAs have to be asked for, once per context as well
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      set_smem_attr_once(kernel, max_place_smem(), &attr_ctx) == cudaSuccess) {
+    for (int size = kCluster; size >= 8 && largest == 1; size /= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(size));
+      cfg.blockDim = dim3(1024);
+      cfg.dynamicSmemBytes = max_place_smem();
+      cudaLaunchAttribute attr = {};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = static_cast<unsigned>(size);
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int active = 0;
+      if (cudaOccupancyMaxActiveClusters(&active, kernel, &cfg) != cudaSuccess)
+        (void)cudaGetLastError();  // a size that does not fit is no error of the call
+      else if (active > 0)
+        largest = size;
+    }
+  }
+  return largest;
+}
+
 template <Mode MODE, bool HELD>
 cudaError_t launch_place(const DispatchArgs& a, int blocks, cudaStream_t stream) {
   static thread_local uint64_t attr_ctx = 0;
-  const size_t max_smem = place_smem_bytes(512) > place_smem_bytes(kMaxExperts) ? place_smem_bytes(512)
-                                                                                : place_smem_bytes(kMaxExperts);
   const void* kernel = reinterpret_cast<const void*>(dispatch_place_kernel<MODE, HELD>);
-  if (MODE == kClustered && (attr_ctx == 0 || attr_ctx != current_context_id())) {
-    // clusters of more than eight CTAs have to be asked for, once per context as well
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (err != cudaSuccess) return err;
-  }
-  const cudaError_t err = set_smem_attr_once(kernel, max_smem, &attr_ctx);
+  const cudaError_t err = set_smem_attr_once(kernel, max_place_smem(), &attr_ctx);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -324,14 +357,19 @@ cudaError_t launch_place(const DispatchArgs& a, int blocks, cudaStream_t stream)
   return cudaLaunchKernelEx(&cfg, dispatch_place_kernel<MODE, HELD>, a);
 }
 
+// CTAs of a cluster of at most `most` CTAs that take up to `groups` groups a warp (one, two, four ..);
+// 0 for more pairs than that.
+int cluster_blocks(long long pairs, int E, int most, int groups) {
+  const long long group = 32 * warps_for(E);  // pairs of one group per warp
+  for (int g = 1; g <= groups; g *= 2)
+    if (pairs <= most * g * group) return static_cast<int>((pairs + g * group - 1) / (g * group));
+  return 0;
+}
+
 // CTAs of a call that one launch does: one, or a cluster; 0 for calls that take two launches.
 int one_launch_blocks(long long pairs, int E) {
-  const long long group = 32 * warps_for(E);  // pairs of one group per warp
-  if (pairs <= 2 * group) return 1;
-  // one, two or four groups a warp
-  for (int g = 1; g <= kClusterGroups; g *= 2)
-    if (pairs <= kCluster * g * group) return static_cast<int>((pairs + g * group - 1) / (g * group));
-  return 0;
+  if (pairs <= 2 * 32 * warps_for(E)) return 1;
+  return cluster_blocks(pairs, E, kCluster, kClusterGroups);
 }
 
 // CTAs of the two launches.
@@ -354,7 +392,15 @@ size_t dispatch_workspace_bytes(long long pairs, int E) {
 cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t stream) {
   const int few = one_launch_blocks(a.pairs, a.E);
   if (few == 1) return launch_place<kOne, true>(a, 1, stream);
-  if (few > 1) return launch_place<kClustered, true>(a, few, stream);
+  if (few > 1) {
+    int most = largest_cluster();
+    if (a.max_cluster > 0 && a.max_cluster < most) most = a.max_cluster;
+    if (few <= most) return launch_place<kClustered, true>(a, few, stream);
+    // Clusters of eight take the same calls with twice the groups a warp.  Without clusters one
+    // CTA takes them all: these calls have no workspace for the two launches.
+    const int blocks = cluster_blocks(a.pairs, a.E, most, kHeld);
+    return blocks > 1 ? launch_place<kClustered, true>(a, blocks, stream) : launch_place<kOne, false>(a, 1, stream);
+  }
   const int blocks = many_blocks(a.pairs, a.E);
   const int threads = 32 * warps_for(a.E);
   dispatch_count_kernel<<<blocks, threads, sizeof(int) * a.E, stream>>>(a);

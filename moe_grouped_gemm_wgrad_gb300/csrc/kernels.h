@@ -167,14 +167,18 @@ struct RouteBwdArgs {
 cudaError_t launch_route_backward(const RouteBwdArgs& a, bool f32, bool sigmoid, bool renorm,
                                   cudaStream_t stream);
 
-// Row tables (dispatch.cu).  `blocks` CTAs; more than one needs blocks * E ints of workspace.
+// Row tables (dispatch.cu): one launch of one CTA or of a cluster, or two launches, whose CTAs
+// meet in a workspace of a row of E counts for each.
 struct DispatchArgs {
   const int32_t* expert_idx;  // [pairs]
   int32_t* expert_off;        // [E + 1]
   int32_t* row_index;         // [pairs]
   int32_t* row_of;            // [pairs]
-  int32_t* counts;            // workspace [blocks, E]
+  int32_t* counts;            // workspace [CTAs, E] of the two launches
   int pairs, top_k, E;
+  // Test hook: the largest cluster to use, as where a context cannot run larger ones.  Always zero
+  // (no limit) in libmgw.so; libmgw_testhooks.so sets it, from MGW_TEST_MAX_CLUSTER.
+  int max_cluster;
   int* status;
 };
 size_t dispatch_workspace_bytes(long long pairs, int E);

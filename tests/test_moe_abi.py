@@ -236,3 +236,11 @@ def test_binding_combine(fake):
     _rejects(fake, mgw.moe_combine_backward, bf(5, 64), f32(10, 64), ro, weights=w)
     _rejects(fake, mgw.moe_combine_backward, bf(5, 64), y, ro, M=11, weights=w)
     _rejects(fake, mgw.moe_combine_backward, bf(5, 64), y, ro, dweights=w)
+
+
+def test_cluster_limit_only_in_the_test_build():
+    build.build()
+    with open(build.LIB, "rb") as f:
+        assert b"MGW_TEST_MAX_CLUSTER" not in f.read()
+    with open(build.LIB_TESTHOOKS, "rb") as f:
+        assert b"MGW_TEST_MAX_CLUSTER" in f.read()
