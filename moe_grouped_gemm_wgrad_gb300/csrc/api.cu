@@ -577,6 +577,15 @@ mgw_status mgw_grouped_dgrad_mxfp8(const void* dyq, const void* dys, const void*
 namespace {
 
 bool element_type(int dtype) { return dtype == MGW_TYPE_BF16 || dtype == MGW_TYPE_F32; }
+// Only the test build of the library (libmgw_testhooks.so) has a limit, see kernels.h.
+int test_max_cluster() {
+#ifdef MGW_TEST_HOOKS
+  const char* v = std::getenv("MGW_TEST_MAX_CLUSTER");
+  return v != nullptr ? std::atoi(v) : 0;
+#else
+  return 0;
+#endif
+}
 bool gated(int act) { return act == MGW_ACT_SWIGLU || act == MGW_ACT_GEGLU; }
 
 mgw_status route_check(const void* logits, int dtype, int T, int E, int top_k, int score,
@@ -697,14 +706,7 @@ mgw_status mgw_moe_dispatch(const int32_t* expert_idx, int T, int top_k, int E, 
   a.pairs = static_cast<int>(pairs);
   a.top_k = top_k;
   a.E = E;
-  a.max_cluster = 0;
-#ifdef MGW_TEST_HOOKS
-  {
-    // Only in the test build of the library (libmgw_testhooks.so), see kernels.h.
-    const char* v = std::getenv("MGW_TEST_MAX_CLUSTER");
-    a.max_cluster = v != nullptr ? std::atoi(v) : 0;
-  }
-#endif
+  a.max_cluster = test_max_cluster();
   a.status = status_dev;
   const cudaError_t err = mgw::launch_dispatch(a, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
@@ -754,6 +756,7 @@ mgw_status mgw_grouped_fprop_mxfp8_act(const void* xq, const void* xs, const voi
   a.K = K;
   a.Mcap = static_cast<long long>(Mcap);
   a.Mw = static_cast<long long>(Mw);
+  a.max_cluster = test_max_cluster();
   a.status = status_dev;
   const cudaError_t err = mgw::launch_grouped_act(a, act, dev.sms, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;

@@ -753,23 +753,52 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_act_kernel(const __grid_c
 }
 
 template <int ACT, int S>
-cudaError_t launch_split(const ActMmArgs& a, long long clusters, cudaStream_t stream) {
-  static thread_local uint64_t attr_ctx = 0;
-  const cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(grouped_act_kernel<ACT, S>),
-                                             act_smem_bytes(kMaxExperts), &attr_ctx);
-  if (err != cudaSuccess) return err;
+cudaLaunchConfig_t split_config(size_t smem, long long clusters, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * S));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = act_smem_bytes(a.E);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2 * S;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
+  cfg.dynamicSmemBytes = smem;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = 2 * S;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int ACT, int S>
+cudaError_t set_smem() {
+  static thread_local uint64_t attr_ctx = 0;
+  return set_smem_attr_once(reinterpret_cast<const void*>(grouped_act_kernel<ACT, S>),
+                            act_smem_bytes(kMaxExperts), &attr_ctx);
+}
+
+// Clusters of S pairs that the current context runs at once: none where a process has a share of
+// the SMs that is too small.  Asked once per context and thread.
+template <int ACT, int S>
+int clusters_at_once() {
+  static thread_local uint64_t asked_ctx = 0;
+  static thread_local int active = 0;
+  if (asked_ctx != 0 && asked_ctx == current_context_id()) return active;
+  if (set_smem<ACT, S>() != cudaSuccess) return 0;
+  cudaLaunchAttribute attr = {};
+  const cudaLaunchConfig_t cfg = split_config<ACT, S>(act_smem_bytes(kMaxExperts), 1, &attr);
+  if (cudaOccupancyMaxActiveClusters(&active, grouped_act_kernel<ACT, S>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();  // a size that does not fit is no error of the call
+    active = 0;
+  }
+  asked_ctx = current_context_id();
+  return active;
+}
+
+template <int ACT, int S>
+cudaError_t launch_split(const ActMmArgs& a, long long clusters, cudaStream_t stream) {
+  const cudaError_t err = set_smem<ACT, S>();
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr = {};
+  cudaLaunchConfig_t cfg = split_config<ACT, S>(act_smem_bytes(a.E), clusters, &attr);
+  cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, grouped_act_kernel<ACT, S>, a);
 }
 
@@ -784,8 +813,13 @@ cudaError_t launch(const ActMmArgs& a, int num_sms, cudaStream_t stream) {
   // waits for a whole one and costs 9 us).  16 rows of one expert, launch included: 1024 x 16384
   // 36 us with one pair an item, 26 with two, 20 with four; 1024 x 4096 18, 16 and 15 us.
   const int nch = a.K / BL;
-  if (a.M <= kSplitRows && nch >= 8 && items * 8 <= num_sms * 4 / 5) return launch_split<ACT, 4>(a, items, stream);
-  if (a.M <= kSplitRows && nch >= 4 && items * 4 <= num_sms * 15 / 16) return launch_split<ACT, 2>(a, items, stream);
+  const int most = a.max_cluster > 0 ? a.max_cluster : 8;
+  if (a.M <= kSplitRows && nch >= 8 && items * 8 <= num_sms * 4 / 5 && most >= 8 &&
+      items <= clusters_at_once<ACT, 4>())
+    return launch_split<ACT, 4>(a, items, stream);
+  if (a.M <= kSplitRows && nch >= 4 && items * 4 <= num_sms * 15 / 16 && most >= 4 &&
+      items <= clusters_at_once<ACT, 2>())
+    return launch_split<ACT, 2>(a, items, stream);
   const long long pairs = items < num_sms / 2 ? items : num_sms / 2;  // at most one per item
   return launch_split<ACT, 1>(a, pairs, stream);
 }

@@ -119,6 +119,7 @@ struct ActMmArgs {
   void* z;                // bf16 [M, N] or null
   int E, M, N, K;
   long long Mcap, Mw;
+  int max_cluster;        // test hook, as DispatchArgs::max_cluster
   int* status;
 };
 int act_row_box();

@@ -10,6 +10,7 @@ import torch
 import moe_reference as ref
 from moe_grouped_gemm_wgrad_gb300 import build, mgw
 from helpers import dev_i32
+from test_gpu_moe import ACT, GATED, _operands, dev, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,21 @@ def test_dispatch_with_smaller_clusters(limited, most, T, K, E, drop):
     assert np.array_equal(off.cpu().numpy(), woff)
     assert np.array_equal(row_index.cpu().numpy(), wri)
     assert np.array_equal(row_of.cpu().numpy(), wro)
+
+
+@pytest.mark.parametrize("most", [8, 4, 2])
+@pytest.mark.parametrize("counts,N,K,act", [([16], 1024, 2048, "swiglu"), ([0, 33, 0, 31], 256, 1024, "gelu"),
+                                            ([5, 7], 512, 640, "none"), ([1], 256, 512, "silu")])
+def test_product_with_smaller_clusters(limited, most, counts, N, K, act):
+    """Contractions split over clusters of four pairs, of two, and not at all: the tolerance is that of
+    test_fprop_act."""
+    rng = np.random.default_rng(sum(counts) + N + K)
+    ops, off, z = _operands(rng, counts, N, K)
+    M, F = sum(counts), N // 2 if act in GATED else N
+    b = np.float32(rng.standard_normal((len(counts), N)))
+    want = ref.act(act, z + np.repeat(b.astype(np.float64), counts, axis=0))
+    limited.setenv("MGW_TEST_MAX_CLUSTER", str(most))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), M, N, ACT[act], bias=dev(b, "f32"), status=st)
+    assert st.item() == 0 and got.shape == (M, F)
+    assert np.all(np.abs(f64(got) - want) <= 4e-3 * np.abs(want) + 1e-3 * np.sqrt(np.mean(want ** 2)))
