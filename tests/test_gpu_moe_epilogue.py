@@ -11,9 +11,10 @@ import pytest
 import torch
 
 import moe_reference as ref
+import oracle
 from moe_grouped_gemm_wgrad_gb300 import mgw, synth
-from helpers import dev_i32
-from test_gpu_moe import ACT, GATED, _operands, dev, f64, status
+from helpers import dev_bf16, dev_i32, oracle_quantize_by_expert
+from test_gpu_moe import ACT, GATED, dev, f64, status
 
 pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
@@ -63,3 +64,65 @@ def test_an_up_value_that_is_not_a_number_reaches_the_gate_only():
                                      mgw.ACT_SWIGLU)
     bad = torch.isnan(dz).nonzero().tolist()
     assert bad == [[1, 7]]
+
+
+# ------------------------------------------------------------- many work items a CTA pair
+MIXED = [33, 209, 1, 417, 150, 16, 0, 40]     # 1 to 3 row tiles of 1 to 13 groups of 16 rows
+
+
+def _large_operands(rng, counts, N, K, product=True):
+    """_operands for larger sizes: experts quantized on threads, z by matrix products in float64."""
+    E, M = len(counts), sum(counts)
+    off = synth.offsets_from_counts(np.asarray(counts))
+    w_off = np.arange(E + 1, dtype=np.int32) * N
+    xb = synth.bf16_bits_from_f32(rng.standard_normal((M, K)).astype(np.float32))
+    wb = synth.bf16_bits_from_f32((rng.standard_normal((E * N, K)) * K ** -0.5).astype(np.float32))
+    ops = (*mgw.mxfp8_quantize_rows(dev_bf16(xb), dev_i32(off)), *mgw.mxfp8_quantize_rows(dev_bf16(wb), dev_i32(w_off)))
+    if not product:
+        return ops, off, None
+    oxq, oxs = oracle_quantize_by_expert(xb, off, oracle.token_capacity(M, E), rows=True)
+    owq, ows = oracle_quantize_by_expert(wb, w_off, oracle.token_capacity(E * N, E), rows=True)
+    z = np.empty((M, N))
+    for _, r0, r1, v in oracle.grouped_fprop_mx_by_expert(oxq, oxs, owq, ows, off, w_off):
+        z[r0:r1] = v
+    return ops, off, z
+
+
+def _items(counts, N):
+    return sum((c + 207) // 208 for c in counts) * (N // 256)
+
+
+@pytest.mark.parametrize("counts,N,K,act,bias,residual,save", [
+    (MIXED, 8192, 128, "gelu", True, True, True),
+    (MIXED, 8192, 896, "swiglu", True, True, True),
+    ([33] * 70 + [209, 417, 300], 1024, 128, "swiglu", True, False, True),
+    ([33] * 70 + [209, 417, 300], 1024, 896, "silu", False, True, False),
+    ([1, 16, 17, 208] * 20, 1024, 256, "geglu", True, True, True),
+])
+def test_fprop_act_of_many_items_a_pair(counts, N, K, act, bias, residual, save):
+    """At least four items for each pair of a 152-SM device, one after the other: both accumulators,
+    their reuse, the ring and its phases across items, and epilogue warps whose first group moves on
+    from item to item, also where an item has fewer groups than warps."""
+    assert _items(counts, N) >= 4 * 76
+    rng = np.random.default_rng(N + K)
+    E, M, F = len(counts), sum(counts), N // 2 if act in GATED else N
+    ops, off, z = _large_operands(rng, counts, N, K)
+    b = np.float32(rng.standard_normal((E, N))) if bias else None
+    res = ref.bf16(rng.standard_normal((M, F))) if residual else None
+    if bias:
+        z = z + np.repeat(b.astype(np.float64), counts, axis=0)
+    want = ref.act(act, z) + (res if residual else 0.0)
+    kw = dict(bias=None if b is None else dev(b, "f32"), residual=None if res is None else dev(res, "bf16"),
+              save_preact=save)
+    runs = []
+    for _ in range(2):
+        st = status()
+        out = torch.full((M + 3, F), 77.0, dtype=torch.bfloat16, device="cuda")
+        got = mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), M, N, ACT[act], out=out, status=st, **kw)
+        assert st.item() == 0 and (out[M:] == 77).all()
+        runs.append(got if save else (got, got))
+    (y, zg), (y2, z2) = runs
+    assert torch.equal(y, y2) and torch.equal(zg, z2)
+    if save:
+        assert np.all(np.abs(f64(zg) - z) <= 4e-3 * np.abs(z) + 1e-3 * np.sqrt(np.mean(z ** 2)))
+    assert np.all(np.abs(f64(y[:M]) - want) <= 4e-3 * np.abs(want) + 1e-3 * np.sqrt(np.mean(want ** 2)))
