@@ -126,3 +126,18 @@ def test_fprop_act_of_many_items_a_pair(counts, N, K, act, bias, residual, save)
     if save:
         assert np.all(np.abs(f64(zg) - z) <= 4e-3 * np.abs(z) + 1e-3 * np.sqrt(np.mean(z ** 2)))
     assert np.all(np.abs(f64(y[:M]) - want) <= 4e-3 * np.abs(want) + 1e-3 * np.sqrt(np.mean(want ** 2)))
+
+
+@pytest.mark.parametrize("counts,N,K,act", [
+    (MIXED, 8192, 128, "gelu"), (MIXED, 8192, 128, "swiglu"), ([300, 0, 129], 512, 384, "none"),
+    ([40], 512, 2048, "silu"), ([16, 3], 1024, 1024, "swiglu"),    # contraction split over pairs
+])
+def test_the_products_residual_may_be_its_output(counts, N, K, act):
+    rng = np.random.default_rng(N + K)
+    M, F = sum(counts), N // 2 if act in GATED else N
+    ops, off, _ = _large_operands(rng, counts, N, K, product=False)
+    res = dev(rng.standard_normal((M, F)), "bf16")
+    want = mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), M, N, ACT[act], residual=res)
+    buf = res.clone()
+    got = mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), M, N, ACT[act], residual=buf, out=buf)
+    assert got is buf and torch.equal(got, want) and not torch.equal(got, res)
