@@ -141,3 +141,33 @@ def test_the_products_residual_may_be_its_output(counts, N, K, act):
     buf = res.clone()
     got = mgw.grouped_fprop_mxfp8_act(*ops, dev_i32(off), M, N, ACT[act], residual=buf, out=buf)
     assert got is buf and torch.equal(got, want) and not torch.equal(got, res)
+
+
+# ------------------------------------------------------ bias sums over long and skewed experts
+@pytest.mark.parametrize("counts,N,act", [
+    ([8300], 128, "none"), ([8300], 256, "swiglu"), ([0, 33000, 3], 128, "gelu"), ([0, 33000, 3], 256, "geglu"),
+    ([8192 * 2, 8192], 384, "relu"),                  # eight slices
+    ([2100, 0, 5000], 256, "silu"),                   # two
+    ([9000] + [40] * 31, 256, "gelu"),                # one, an expert far above the mean
+])
+def test_bias_gradient_of_long_experts(counts, N, act):
+    rng = np.random.default_rng(sum(counts) + N)
+    M, F = sum(counts), N // 2 if act in GATED else N
+    off = synth.offsets_from_counts(np.asarray(counts))
+    dy = ref.bf16(rng.standard_normal((M, F)))
+    z = ref.bf16(rng.standard_normal((M, N)))
+    zt = None if act == "none" else dev(z, "bf16")
+    runs = []
+    for _ in range(2):
+        st = status()
+        dz, db = mgw.grouped_act_backward(dev(dy, "bf16"), zt, dev_i32(off), ACT[act], with_dbias=True, status=st)
+        assert st.item() == 0
+        runs.append((dz, db))
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+    want = ref.act_backward(act, dy, z)
+    grad = np.abs(dy) if act not in GATED else \
+        np.concatenate([np.abs(dy * z[:, F:]), np.abs(dy) * np.maximum(np.abs(z[:, :F]), 1)], axis=1)
+    for e, n in enumerate(counts):
+        rows = slice(off[e], off[e + 1])
+        tol = 2.0 ** -24 * (n / 8 + 16) * np.abs(want[rows]).sum(axis=0) + 2e-6 * grad[rows].sum(axis=0)
+        assert np.all(np.abs(f64(db)[e] - want[rows].sum(axis=0)) <= tol)
