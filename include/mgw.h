@@ -393,7 +393,10 @@ mgw_status mgw_moe_route_backward(const void *logits, int dtype, int T, int E, i
  *            MGW_DEV_BAD_INDEX and drops the pair too.
  * expert_off device int32 [E+1]: rows of expert e are expert_off[e] .. expert_off[e+1]-1.
  *            expert_off[E] = T * top_k less the dropped pairs: the M (rows) of the calls
- *            above.  With nothing dropped the caller knows it without reading it back.
+ *            above, which they take from the host.  With nothing dropped the caller knows it;
+ *            where pairs may be dropped (masked experts) the caller reads expert_off[E] back
+ *            first, and row_index's first expert_off[E] entries are the quantizers' row_index.
+ *            Any other M makes those calls report MGW_DEV_BAD_OFFSETS and write nothing.
  * row_index  device int32 [T * top_k]: the token of every row, ascending within an expert;
  *            -1 past expert_off[E].  The row_index of the gathering quantizers.
  * row_of     device int32 [T, top_k]: the row of every pair, -1 for a dropped one.

@@ -687,8 +687,9 @@ def moe_dispatch(expert_idx: torch.Tensor, E: int, expert_off: torch.Tensor | No
     -> (expert_off int32 [E+1], row_index int32 [T*top_k], row_of int32 [T, top_k]).
 
     ``expert_off`` and ``row_index`` are what the quantizers and grouped products take, with
-    M = expert_off[E] rows (T * top_k when nothing is dropped); ``row_of`` is what
-    :func:`moe_combine` takes.  ``workspace`` (uint8) is allocated when a large call needs one
+    M = expert_off[E] rows: T * top_k when nothing is dropped.  Where pairs may be dropped, read
+    ``M = int(expert_off[-1])`` back (these calls take M from the host) and pass
+    ``row_index[:M]``.  ``row_of`` is what :func:`moe_combine` takes.  ``workspace`` (uint8) is allocated when a large call needs one
     and none is given."""
     _dev_tensor(expert_idx, torch.int32, "expert_idx", 2)
     T, top_k = expert_idx.shape

@@ -171,3 +171,77 @@ def test_bias_gradient_of_long_experts(counts, N, act):
         rows = slice(off[e], off[e + 1])
         tol = 2.0 ** -24 * (n / 8 + 16) * np.abs(want[rows]).sum(axis=0) + 2e-6 * grad[rows].sum(axis=0)
         assert np.all(np.abs(f64(db)[e] - want[rows].sum(axis=0)) <= tol)
+
+
+# ------------------------------------------------------------- dropped pairs through a layer
+def _masked_layer():
+    """A routing with masked experts: some tokens have fewer than top_k experts, some none."""
+    T, E, K, H, N = 203, 12, 4, 256, 512
+    rng = np.random.default_rng(17)
+    x = np.float32(rng.standard_normal((T, E)))
+    x[rng.random((T, E)) < 0.75] = -np.inf
+    x[5], x[77] = -np.inf, -np.inf
+    hidden = synth.bf16_bits_from_f32(rng.standard_normal((T, H)).astype(np.float32))
+    wb = synth.bf16_bits_from_f32((rng.standard_normal((E * N, H)) / 16).astype(np.float32))
+    return T, E, K, H, N, rng, x, hidden, wb
+
+
+def test_dropped_pairs_through_a_layer():
+    """The caller reads expert_off[E] back once: M, and the length of row_index that the calls take."""
+    T, E, K, H, N, rng, x, hidden, wb = _masked_layer()
+    st = status()
+    idx, w = mgw.moe_route(dev(x, "f32"), K, status=st)
+    off, row_index, row_of = mgw.moe_dispatch(idx, E, status=st)
+    M = int(off[-1])
+    assert 0 < M < T * K and (idx == -1).sum().item() == T * K - M
+    assert (row_index[M:] == -1).all() and (row_index[:M] >= 0).all()
+    row_index = row_index[:M]
+    w_off = np.arange(E + 1, dtype=np.int32) * N
+    xd = dev_bf16(hidden)
+    xq, xs = mgw.mxfp8_quantize_rows(xd, off, row_index=row_index, status=st)
+    wq, ws = mgw.mxfp8_quantize_rows(dev_bf16(wb), dev_i32(w_off), status=st)
+    y, z = mgw.grouped_fprop_mxfp8_act(xq, xs, wq, ws, off, M, N, mgw.ACT_SWIGLU, save_preact=True, status=st)
+    res = ref.bf16(rng.standard_normal((T, N // 2)))
+    out = mgw.moe_combine(y, row_of, weights=w, residual=dev(res, "bf16"), status=st)
+    # the same in 64 bits, from the router's choice on
+    ri, ro, o = row_index.cpu().numpy(), row_of.cpu().numpy(), off.cpu().numpy()
+    oxq, oxs = oracle.mxfp8_quantize_rows(np.ascontiguousarray(hidden[ri]), o)
+    owq, ows = oracle.mxfp8_quantize_rows(wb, w_off)
+    h = ref.act("swiglu", oracle.grouped_fprop_mx(oxq, oxs, owq, ows, o, w_off, M))
+    rms = np.sqrt(np.mean(h ** 2))
+    wf = f64(w)
+    want = ref.combine(h, ro, wf, res)
+    tol = ref.combine(4e-3 * np.abs(h) + 1e-3 * rms, ro, wf, None) + 2.0 ** -8 * np.abs(want) + 1e-6 * (np.abs(want) + rms)
+    assert np.all(np.abs(f64(out) - want) <= tol)
+    assert np.array_equal(f64(out)[[5, 77]], res[[5, 77]])      # no expert: the residual
+    # and back: every gradient's call takes the same M
+    dout = dev(rng.standard_normal((T, N // 2)), "bf16")
+    dy, dw = mgw.moe_combine_backward(dout, y, row_of, weights=w, status=st)
+    dz, db = mgw.grouped_act_backward(dy, z, off, mgw.ACT_SWIGLU, with_dbias=True, status=st)
+    gq, gs = mgw.mxfp8_quantize(dz, off, status=st)
+    xtq, xts = mgw.mxfp8_quantize_gather(xd, row_index, off, status=st)
+    dW = mgw.grouped_wgrad_mxfp8(gq, gs, xtq, xts, off, M, status=st)
+    dzq, dzs = mgw.mxfp8_quantize_rows(dz, off, status=st)
+    wtq, wts = mgw.mxfp8_quantize(dev_bf16(wb), dev_i32(w_off), status=st)
+    dxr = mgw.grouped_dgrad_mxfp8(dzq, dzs, wtq, wts, off, M, status=st)
+    dx = mgw.moe_combine(dxr, row_of, status=st)
+    dl = mgw.moe_route_backward(dev(x, "f32"), idx, dw, status=st)
+    assert st.item() == 0
+    for t in (dy, dz, db, dW, dx, dl):
+        assert torch.isfinite(t).all()
+    assert (dx[[5, 77]] == 0).all() and (dl[[5, 77]] == 0).all() and (dw[idx == -1] == 0).all()
+    assert (f64(dl)[np.isinf(x)] == 0).all()
+    wdz = ref.act_backward("swiglu", f64(dy), f64(z))
+    assert np.all(np.abs(f64(db) - np.stack([wdz[o[e]:o[e + 1]].sum(0) for e in range(E)])) <= 1e-4)
+
+
+def test_the_tables_of_all_pairs_are_refused_where_some_are_dropped():
+    """Without the read: M = T * top_k is not expert_off[E], and every call says so and writes nothing."""
+    T, E, K, H, N, _, x, hidden, wb = _masked_layer()
+    idx, _ = mgw.moe_route(dev(x, "f32"), K)
+    off, row_index, _ = mgw.moe_dispatch(idx, E)
+    cap = mgw.token_capacity(T * K, E)
+    st = status()
+    q = torch.full((cap, H), 9, dtype=torch.uint8, device="cuda")
+    mgw.mxfp8_quantize_rows(dev_bf16(hidden), off, row_index=row_index, q=q, status=st)
+    assert st.item() == mgw.MGW_DEV_BAD_OFFSETS and (q == 9).all()
