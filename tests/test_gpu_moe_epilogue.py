@@ -66,6 +66,30 @@ def test_an_up_value_that_is_not_a_number_reaches_the_gate_only():
     assert bad == [[1, 7]]
 
 
+def test_gelu_and_its_slope_before_any_rounding_to_bf16():
+    """One row an expert and dy = 1: dbias is the slope itself in fp32, and the up columns' dbias of the
+    gated form the GELU's value.  Over every bf16 z up to 14.
+
+    The tail's formula is good to 1.5e-7 / 2; its factors t and e to about 2^-22 of themselves with the
+    approximate reciprocal and exponential, of a tail of at most 1/2 whose derivative by them is below
+    1 (2.4e-7); e counts once more in x phi(x), of at most 0.25, where its argument's rounding adds
+    x^2 2^-24 (0.6e-7): 5e-7 for the slope, 4e-7 max(|x|, 1) for the value."""
+    from scipy.special import erfc
+
+    bits = np.arange(0x4160 + 1, dtype=np.uint16)          # 0 .. 14
+    every = np.concatenate([bits, bits | 0x8000]).view(np.int16)
+    E, N = 1024, 128
+    z = torch.from_numpy(np.resize(every, E * N)).view(torch.bfloat16).view(E, N).cuda()
+    off, x = dev_i32(np.arange(E + 1)), f64(z)
+    phi = 0.5 * erfc(-x / np.sqrt(2.0))
+    one = torch.ones(E, N, dtype=torch.bfloat16, device="cuda")
+    _, db = mgw.grouped_act_backward(one, z, off, mgw.ACT_GELU, with_dbias=True)
+    assert np.abs(f64(db) - (phi + x * np.exp(-x * x / 2) / np.sqrt(2 * np.pi))).max() <= 5e-7
+    both = torch.cat([z, torch.ones_like(z)], dim=1)
+    _, db = mgw.grouped_act_backward(one, both, off, mgw.ACT_GEGLU, with_dbias=True)
+    assert (np.abs(f64(db)[:, N:] - x * phi) / np.maximum(np.abs(x), 1)).max() <= 4e-7
+
+
 # ------------------------------------------------------------- many work items a CTA pair
 MIXED = [33, 209, 1, 417, 150, 16, 0, 40]     # 1 to 3 row tiles of 1 to 13 groups of 16 rows
 
