@@ -30,41 +30,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The lower tail h = Phi(-|x|) of the normal distribution and e = exp(-x^2 / 2), by formula
-// 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions: erfc(u) =
-// (a1 t + .. + a5 t^5) exp(-u^2), t = 1 / (1 + 0.3275911 u), with |error| <= 1.5e-7 in erf.
-// In fp32 x Phi(x) is off by up to 1.6e-7 max(|x|, 1), where x (0.5 + 0.5 erf) is by 1.1e-7, and
-// the slope by 6.6e-8 rms over normal x, where that is by 2.7e-8.  Next to bf16 (half an ulp is up to
-// 2^-8 of a value) that is nothing, and far below x = 0 the tail is the better of the two; the one
-// fp32 output that has it in is the bias gradient, a sum of slopes.
-__device__ __forceinline__ float normal_tail(float x, float& e) {
-  const float t = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.0f));
-  const float y = 0.84932180028801907f * x;  // sqrt(log2(e) / 2)
-  e = ex2_approx(-y * y);
-  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-  p = fmaf(p, t, 0.5f * 1.421413741f);
-  p = fmaf(p, t, 0.5f * -0.284496736f);
-  p = fmaf(p, t, 0.5f * 0.254829592f);
-  return p * t * e;
-}
-
 // 1 / (1 + e^-x); e^-x may overflow to infinity, whose reciprocal is 0.
 __device__ __forceinline__ float logistic_fast(float x) {
   return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
 }
 
-// x Phi(x) = max(x, 0) - |x| h, with |x| bounded so that an infinite x meets h = 0 as a number.
-__device__ __forceinline__ float gelu_from_tail(float x, float h) {
-  return fmaf(-fminf(fabsf(x), 1e30f), h, fmaxf(x, 0.0f));
-}
-
+// Activations other than the GELU, which comes in pairs only (act_value2).
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
+  static_assert(ACT != kActGelu, "act_value2");
   if constexpr (ACT == kActRelu) return x <= 0.0f ? 0.0f : x;  // NaN stays NaN
-  if constexpr (ACT == kActGelu) {
-    float e;
-    return gelu_from_tail(x, normal_tail(x, e));
-  }
   if constexpr (ACT == kActSilu) return x * logistic_fast(x);
   return x;
 }
@@ -92,8 +67,13 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// normal_tail of two values, packed: minus the tails (the polynomial with its signs turned) and
-// the exponentials.
+// Of two values: minus the lower tail h = Phi(-|x|) of the normal distribution, and e = exp(-x^2 / 2),
+// by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions: erfc(u) =
+// (a1 t + .. + a5 t^5) exp(-u^2), t = 1 / (1 + 0.3275911 u), with |error| <= 1.5e-7 in erf (the
+// polynomial has its signs turned).  In fp32 x Phi(x) is off by up to 1.6e-7 max(|x|, 1), where
+// x (0.5 + 0.5 erf) is by 1.1e-7, and the slope by 6.6e-8 rms over normal x, where that is by 2.7e-8.
+// Next to bf16 (half an ulp is up to 2^-8 of a value) that is nothing, and far below x = 0 the tail
+// is the better of the two; the one fp32 output that has it in is the bias gradient, a sum of slopes.
 __device__ __forceinline__ F2 minus_tail2(float x0, float x1, F2& e) {
   const float t0 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x0), 1.0f));
   const float t1 = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(x1), 1.0f));
@@ -107,6 +87,7 @@ __device__ __forceinline__ F2 minus_tail2(float x0, float x1, F2& e) {
   p = fma2(p, t, f2(-0.5f * 0.254829592f, -0.5f * 0.254829592f));
   return mul2(mul2(p, t), e);
 }
+// x Phi(x) = max(x, 0) - |x| h, with |x| bounded so that an infinite x meets h = 0 as a number.
 __device__ __forceinline__ F2 gelu2_from_tail(float x0, float x1, F2 minus_h) {
   return fma2(f2(fminf(fabsf(x0), 1e30f), fminf(fabsf(x1), 1e30f)), minus_h,
               f2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
@@ -129,14 +110,10 @@ __device__ __forceinline__ void act_value2(float& x0, float& x1) {
 // Value and slope together (the backward pass of a gated activation needs both).
 template <int ACT>
 __device__ __forceinline__ void act_value_slope(float x, float& value, float& slope) {
+  static_assert(ACT != kActGelu, "act_value_slope2");
   if constexpr (ACT == kActRelu) {
     value = x <= 0.0f ? 0.0f : x;
     slope = x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;  // NaN stays NaN
-  } else if constexpr (ACT == kActGelu) {
-    float e;
-    const float h = normal_tail(x, e);
-    value = gelu_from_tail(x, h);
-    slope = fmaf(0.3989422804014327f * x, e, x >= 0.0f ? 1.0f - h : h);  // Phi(x) + x phi(x)
   } else if constexpr (ACT == kActSilu) {
     const float s = logistic_fast(x);
     value = x * s;

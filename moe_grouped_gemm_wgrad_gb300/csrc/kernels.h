@@ -126,7 +126,8 @@ int act_row_box();
 cudaError_t launch_grouped_act(const ActMmArgs& a, int act, int num_sms, cudaStream_t stream);
 
 // Backward pass of the epilogue (act_backward.cu).  Partial bias sums of every 128-row tile of
-// an expert go to `partial` [tiles, N] (null without dbias) and are summed in tile order.
+// an expert go to `partial` [tiles, N] (null without dbias); one, two or eight slices of an expert's
+// tiles are summed each in tile order, then in the order of the slices.
 struct ActBwdArgs {
   const void* dy;      // bf16 [M, F]
   const void* z;       // bf16 [M, N]; null for the identity
@@ -140,9 +141,8 @@ struct ActBwdArgs {
 size_t act_backward_workspace_bytes(int E, int M, int N);
 cudaError_t launch_act_backward(const ActBwdArgs& a, int act, cudaStream_t stream);
 
-// Router (route.cu).  top_k <= 32 (one selected expert per lane), groups <= 32.
+// Router (route.cu).  top_k <= 32 (the token's lanes hold one or two choices each), groups <= 32.
 constexpr int kMaxTopK = 32;
-constexpr int kMaxGroups = 32;
 constexpr int kDevBadLogit = 16;  // device status bit: a router logit that is not a number
 struct RouteArgs {
   const void* logits;  // [T, E] bf16 or fp32
