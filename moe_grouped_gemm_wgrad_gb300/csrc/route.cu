@@ -596,6 +596,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     for (int j = 0; j < V; ++j) {
       dx[j] = s[j] * (G[j] - dot);
       if (RENORM) dx[j] += add[j];
+      if (x[j] == kNegInf) dx[j] = 0.0f;  // whatever dot is
     }
   }
   at.store(static_cast<T*>(a.dlogits) + t * E, dx);
