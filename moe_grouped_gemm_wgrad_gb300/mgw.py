@@ -53,6 +53,7 @@ ACT_SWIGLU = 4       # silu(gate) * up, the product's columns being gate then up
 ACT_GEGLU = 5        # gelu(gate) * up
 GATED_ACTS = (ACT_SWIGLU, ACT_GEGLU)
 MAX_TOP_K = 32
+MAX_SIZE = 2 ** 31 - 1   # of every size and count in the C ABI
 
 EXPORTS = (
     "mgw_status_string", "mgw_version", "mgw_mxfp8_token_capacity", "mgw_mxfp8_scale_bytes",
@@ -244,6 +245,16 @@ def _dev_tensor(t: torch.Tensor, dtype, name: str, ndim: int | None = None) -> N
         raise MgwError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
         raise MgwError(f"{name} must be {ndim}-D, got shape {tuple(t.shape)}")
+    if t.numel() > MAX_SIZE and max(t.shape) > MAX_SIZE:
+        raise MgwError(f"a dimension of {name} {tuple(t.shape)} exceeds the C ABI's 32-bit sizes")
+
+
+def _size(n, name: str) -> int:
+    """``n`` as a size that the C ABI's 32-bit arguments hold (ctypes would cut it down silently)."""
+    n = int(n)
+    if n > MAX_SIZE or n < -MAX_SIZE:
+        raise MgwError(f"{name} = {n} exceeds the C ABI's 32-bit sizes")
+    return n
 
 
 def _need(t: torch.Tensor, n: int, name: str) -> None:
@@ -331,7 +342,7 @@ def _used_on(side, *ts) -> None:
 
 def token_capacity(M: int, E: int) -> int:
     """Padded token axis length that fits any split of M tokens over E experts."""
-    return int(load().mgw_mxfp8_token_capacity(int(M), int(E)))
+    return int(load().mgw_mxfp8_token_capacity(_size(M, "M"), _size(E, "E")))
 
 
 def scale_bytes(C: int, Mcap: int) -> int:
@@ -411,10 +422,11 @@ def grouped_wgrad_mxfp8(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor, xs
     """grad_w [E*N, K] bf16 from quantized g^T (N rows) and x^T (K rows)."""
     E, N, K, Mcap, dev = _wgrad_operands(gq, gs, xq, xs, expert_off, status, out)
     side = None if stream is None else _side(stream, dev)
+    M = _size(M, "M")
     out = _out(out, (E * N, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_wgrad_mxfp8(_ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs),
-                                            _ptr(expert_off), E, int(M), N, K, Mcap, _ptr(out),
+                                            _ptr(expert_off), E, M, N, K, Mcap, _ptr(out),
                                             _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_wgrad_mxfp8")
     if side is not None:
@@ -426,7 +438,7 @@ def wgrad_workspace(E: int, N: int, K: int, device=None) -> torch.Tensor:
     """A zero-filled workspace for :func:`grouped_wgrad_mxfp8_balanced` on ``device``."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
-        nbytes = int(load().mgw_grouped_wgrad_workspace_bytes(int(E), int(N), int(K)))
+        nbytes = int(load().mgw_grouped_wgrad_workspace_bytes(_size(E, "E"), _size(N, "N"), _size(K, "K")))
     if nbytes == 0:
         raise MgwError("mgw_grouped_wgrad_workspace_bytes: no usable device")
     return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
@@ -442,10 +454,11 @@ def grouped_wgrad_mxfp8_balanced(gq: torch.Tensor, gs: torch.Tensor, xq: torch.T
     _dev_tensor(workspace, torch.uint8, "workspace")
     E, N, K, Mcap, dev = _wgrad_operands(gq, gs, xq, xs, expert_off, status, out, workspace)
     side = None if stream is None else _side(stream, dev)
+    M = _size(M, "M")
     out = _out(out, (E * N, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_wgrad_mxfp8_balanced(
-            _ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs), _ptr(expert_off), E, int(M), N, K, Mcap,
+            _ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs), _ptr(expert_off), E, M, N, K, Mcap,
             _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_wgrad_mxfp8_balanced")
     if side is not None:
@@ -462,10 +475,11 @@ def grouped_wgrad_mxfp8_balanced_noalloc(gq: torch.Tensor, gs: torch.Tensor, xq:
     in the library; nothing is allocated, calls must not overlap)."""
     E, N, K, Mcap, dev = _wgrad_operands(gq, gs, xq, xs, expert_off, status, out)
     side = None if stream is None else _side(stream, dev)
+    M = _size(M, "M")
     out = _out(out, (E * N, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_wgrad_mxfp8_balanced_noalloc(
-            _ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs), _ptr(expert_off), E, int(M), N, K, Mcap,
+            _ptr(gq), _ptr(gs), _ptr(xq), _ptr(xs), _ptr(expert_off), E, M, N, K, Mcap,
             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_wgrad_mxfp8_balanced_noalloc")
     if side is not None:
@@ -547,10 +561,11 @@ def grouped_fprop_mxfp8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws
     _need(ws, scale_bytes(K, Mw), "ws")
     dev = _one_device(xq, xs, wq, ws, expert_off, out, status)
     side = None if stream is None else _side(stream, dev)
-    out = _out(out, (int(M), int(N)), torch.bfloat16, dev, "out", side)
+    M, N = _size(M, "M"), _size(N, "N")
+    out = _out(out, (M, N), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_fprop_mxfp8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws),
-                                            _ptr(expert_off), E, int(M), int(N), K, Mcap, Mw,
+                                            _ptr(expert_off), E, M, N, K, Mcap, Mw,
                                             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_fprop_mxfp8")
     if side is not None:
@@ -576,10 +591,11 @@ def grouped_dgrad_mxfp8(dyq: torch.Tensor, dys: torch.Tensor, wtq: torch.Tensor,
     _need(wts, scale_bytes(K, Mw), "wts")
     dev = _one_device(dyq, dys, wtq, wts, expert_off, out, status)
     side = None if stream is None else _side(stream, dev)
-    out = _out(out, (int(M), K), torch.bfloat16, dev, "out", side)
+    M = _size(M, "M")
+    out = _out(out, (M, K), torch.bfloat16, dev, "out", side)
     with _device(dev):
         st = load().mgw_grouped_dgrad_mxfp8(_ptr(dyq), _ptr(dys), _ptr(wtq), _ptr(wts),
-                                            _ptr(expert_off), E, int(M), N, K, Mcap, Mw,
+                                            _ptr(expert_off), E, M, N, K, Mcap, Mw,
                                             _ptr(out), _ptr(status), _stream(stream))
     _check(st, "mgw_grouped_dgrad_mxfp8")
     if side is not None:
@@ -623,7 +639,7 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
     dt = _element_type(logits, "logits")
     _dev_tensor(logits, logits.dtype, "logits", 2)
     T, E = logits.shape
-    top_k = int(top_k)
+    top_k = _size(top_k, "top_k")
     if top_k < 1 or top_k > min(MAX_TOP_K, E):
         raise MgwError(f"top_k must be 1 .. {min(MAX_TOP_K, E)}, got {top_k}")
     if bias is not None:
@@ -693,7 +709,7 @@ def moe_dispatch(expert_idx: torch.Tensor, E: int, expert_off: torch.Tensor | No
     and none is given."""
     _dev_tensor(expert_idx, torch.int32, "expert_idx", 2)
     T, top_k = expert_idx.shape
-    E = int(E)
+    E = _size(E, "E")
     if E < 1:
         raise MgwError(f"E must be at least 1, got {E}")
     _status(status)
@@ -739,7 +755,7 @@ def grouped_fprop_mxfp8_act(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor
         raise MgwError(f"wq [Mw, {K_w}] and xq [Mcap, {K}] must share the contraction width")
     _need(xs, K * Mcap // 32, "xs")
     _need(ws, K * Mw // 32, "ws")
-    M, N, act = int(M), int(N), int(act)
+    M, N, act = _size(M, "M"), _size(N, "N"), int(act)
     F = N // 2 if act in GATED_ACTS else N
     if bias is not None:
         _shaped(bias, (E, N), torch.float32, "bias")
@@ -856,7 +872,7 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: tor
         M = y.shape[0]
     elif M is None:
         raise MgwError("M (the number of routed rows) is needed without y")
-    M = int(M)
+    M = _size(M, "M")
     _status(status)
     dev = _one_device(dout, y, row_of, weights, dy, dweights, status)
     side = None if stream is None else _side(stream, dev)

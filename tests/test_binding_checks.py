@@ -181,3 +181,35 @@ def test_mixed_devices_rejected(lib):
     other = torch.zeros(xs.shape, dtype=torch.uint8, device="meta")
     _rejects(lib, mgw.grouped_wgrad_mxfp8, gq, gs, xq, other, i32(*OFF), M)
     _rejects(lib, mgw.mxfp8_quantize, bf(M, N), i32(*OFF), status=torch.zeros(1, dtype=torch.int32, device="meta"))
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+BIG = 2 ** 32 + 4     # cut to 32 bits: 4
+
+
+def _meta(*shape, dtype):
+    """A tensor without storage, as the binding sees one."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda: mgw.moe_route(_meta(BIG, 1, dtype=torch.bfloat16), 1),
+    lambda: mgw.moe_route_backward(_meta(BIG, 1, dtype=torch.bfloat16), _meta(BIG, 1, dtype=torch.int32), None),
+    lambda: mgw.moe_dispatch(_meta(BIG, 1, dtype=torch.int32), 4),
+    lambda: mgw.moe_dispatch(_meta(4, 1, dtype=torch.int32), BIG),
+    lambda: mgw.moe_combine(_meta(BIG, 8, dtype=torch.bfloat16), _meta(4, 1, dtype=torch.int32)),
+    lambda: mgw.moe_combine(_meta(4, 8, dtype=torch.bfloat16), _meta(BIG, 1, dtype=torch.int32)),
+    lambda: mgw.moe_combine_backward(_meta(4, 8, dtype=torch.bfloat16), None, _meta(4, 1, dtype=torch.int32), M=BIG),
+    lambda: mgw.mxfp8_quantize(_meta(BIG, 128, dtype=torch.bfloat16), _meta(3, dtype=torch.int32), Mcap=384),
+    lambda: mgw.mxfp8_quantize_rows(_meta(4, 128, dtype=torch.bfloat16), _meta(3, dtype=torch.int32), Mcap=384,
+                                    row_index=_meta(BIG, dtype=torch.int32)),
+    lambda: mgw.grouped_wgrad_mxfp8(*(_meta(*s, dtype=torch.uint8) for s in ((128, 384), (1536,), (256, 384), (3072,))),
+                                    _meta(3, dtype=torch.int32), BIG),
+    lambda: mgw.grouped_fprop_mxfp8(*(_meta(*s, dtype=torch.uint8) for s in ((384, 128), (1536,), (512, 128), (2048,))),
+                                    _meta(3, dtype=torch.int32), 64, BIG),
+    lambda: mgw.grouped_fprop_mxfp8_act(*(_meta(*s, dtype=torch.uint8) for s in ((384, 128), (1536,), (512, 128), (2048,))),
+                                        _meta(3, dtype=torch.int32), BIG, 256),
+    lambda: mgw.grouped_act_backward(_meta(BIG, 256, dtype=torch.bfloat16), None, _meta(3, dtype=torch.int32), mgw.ACT_NONE),
+])
+def test_sizes_that_the_c_abi_cannot_hold_are_refused(lib, call):
+    _rejects(lib, call)
