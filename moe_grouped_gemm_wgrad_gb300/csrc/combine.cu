@@ -13,8 +13,9 @@
 // and asks for the pieces of eight slots before it uses the first (their rows and weights come
 // from shared memory, read once per CTA).  Rows whose width is not a multiple of 16 bytes
 // start between 16-byte boundaries: a thread then takes two to four narrower words of each row,
-// a warp's width apart, so that a warp's loads stay contiguous.  8192 x 8 x 4096 bf16: forward
-// 101 us (6.6 TB/s, the copy rate), backward 164 us (6.9 TB/s; part of y is still in L2).
+// a warp's width apart, so that a warp's loads stay contiguous.  8192 x 8 x 4096 bf16, a graph's
+// replay less an empty one's 4 us: forward with residual 101 us (6.6 TB/s, the copy rate), backward
+// 164 us (6.9 TB/s; part of y is still in L2).
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -105,9 +106,9 @@ struct Piece {
 };
 
 // grid: (tokens, column blocks); a thread owns one piece of the token.
-// Five CTAs of 256 threads per SM: with four (57 registers) 8192 x 8 x 4096 took 121 us instead
-// of 109, with six the eight pieces spill out of flight (120 us); CTAs of 128 or 512 threads 129
-// and 119 us.
+// Five CTAs of 256 threads per SM.  8192 x 8 x 4096 without a residual, events around a call with
+// dirty lines of other data in L2: 107 us, with four CTAs 111, with six, where the eight pieces
+// spill out of flight, 119; CTAs of 128 or 512 threads cost 18 and 9% more.
 template <typename T, int AB>
 __global__ void __launch_bounds__(kMaxThreads, 5) combine_kernel(CombineArgs a) {
   using P = Piece<T, AB>;
