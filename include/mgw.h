@@ -78,6 +78,7 @@ typedef int mgw_status;
 #define MGW_ACT_GEGLU 5
 
 #define MGW_MAX_TOP_K 32
+#define MGW_MAX_RANK 128 /* of a low-rank adapter */
 #define MGW_MAX_GROUPS 32
 
 /* Human-readable name of a return code (static string). */
@@ -475,6 +476,63 @@ mgw_status mgw_moe_combine(const void *y, int dtype, int M, const int32_t *row_o
 mgw_status mgw_moe_combine_backward(const void *dout, const void *y, int dtype, int M,
                                     const int32_t *row_of, const float *weights, int T, int top_k,
                                     int H, void *dy, float *dweights, int *status_dev, void *stream);
+
+/* ------------------------------------------------------------ low-rank adapters
+ * Adapters of many requests at once beside a shared projection, or one for every expert: a
+ * grouped product of small inner size.  Rows are sorted by adapter as the grouped products' are
+ * by expert, so mgw_moe_dispatch makes the tables (top_k = 1, the adapter of every token; for
+ * tokens without one an extra last expert, whose offset is then left out). */
+
+/* mgw_grouped_lora --
+ *   u[r, j]   = sum_k x[t(r), k] * a[e(r), j, k]
+ *   out[o, n] = base[o, n] + scale[e(r)] * sum_j u[r, j] * b[e(r), n, j]      with o = o(r)
+ * for the rows r of adapter e, adapter_off[e] <= r < adapter_off[e+1]; t(r) = row_index[r] and
+ * o(r) = out_index[r], or r itself without the index.  Rows behind adapter_off[E] have no
+ * adapter: out = base there, and u = 0.
+ * Sums are fp32, out is rounded once; the intermediate enters the second product as two bf16
+ * parts (17 bits).
+ * x           device, bf16 [x_rows, K]; row_index device int32 [M], nullable (then x_rows >= M).
+ * a           device, bf16 [E, R, K];  b: device, bf16 [E, N, R].
+ * scale       device fp32 [E], nullable (1).
+ * adapter_off device int32 [E+1], 0 = off[0] <= ... <= off[E] <= M, 1 <= E <= MGW_MAX_EXPERTS.
+ * base        device, bf16 [out_rows, N], nullable (0); may be out itself.
+ * out_index   device int32 [M], nullable (then out_rows >= M).  No two rows name one row of out;
+ *             rows of out that no row names are not written.
+ * out         device, bf16 [out_rows, N].
+ * u           device fp32 [M, R], nullable: the intermediate, for the backward pass.
+ * K, N, R multiples of 8 (pad an adapter's rank with zeros), R <= MGW_MAX_RANK, K, N <= 2^23 (else
+ * MGW_ERR_UNSUPPORTED).  An index out of range sets MGW_DEV_BAD_INDEX: a row of x then counts as
+ * zeros, a row of out is not written. */
+mgw_status mgw_grouped_lora(const void *x_bf16, int x_rows, const int32_t *row_index, int M, int K,
+                            const void *a_bf16, const void *b_bf16, const float *scale,
+                            const int32_t *adapter_off, int E, int R, int N,
+                            const void *base_bf16, const int32_t *out_index, int out_rows,
+                            void *out_bf16, float *u, int *status_dev, void *stream);
+
+/* mgw_grouped_lora_backward --
+ *   v[r, j]     = sum_n dy[o(r), n] * b[e, n, j]
+ *   dx[o(r), k] = dx_base[o(r), k] + scale[e] * sum_j v[r, j] * a[e, j, k]
+ *   da[e, j, k] = scale[e] * sum over the rows r of adapter e of v[r, j] * x[t(r), k]
+ *   db[e, n, j] = scale[e] * sum over the rows r of adapter e of dy[o(r), n] * u[r, j]
+ * (the gradient to base is dy).  dx has the rows of dy: a layer that gathers rows of x several
+ * times adds them up with mgw_moe_combine.  Adapters without rows get zeros; rows without an
+ * adapter dx_base.  All sums are fp32 in an order that the sizes fix; each output is rounded once.
+ * dy, dx_base device, bf16 [out_rows, N] and [out_rows, K] (dx_base nullable (0); may be dx).
+ * u           device fp32 [M, R] from the forward call; needed with db.
+ * dx          device, bf16 [out_rows, K], nullable.  da: device, bf16 [E, R, K], nullable.
+ * db          device, bf16 [E, N, R], nullable.  x is needed with da only.
+ * workspace   device, 16-byte aligned, mgw_grouped_lora_backward_workspace_bytes bytes, when da is
+ *             given; need not be initialised.
+ * Everything else as in the forward call. */
+mgw_status mgw_grouped_lora_backward(const void *dy_bf16, int out_rows, const int32_t *out_index,
+                                     const void *x_bf16, int x_rows, const int32_t *row_index,
+                                     int M, int K, const void *a_bf16, const void *b_bf16,
+                                     const float *scale, const int32_t *adapter_off, int E, int R,
+                                     int N, const float *u, const void *dx_base_bf16,
+                                     void *dx_bf16, void *da_bf16, void *db_bf16, void *workspace,
+                                     size_t workspace_bytes, int *status_dev, void *stream);
+/* Host only; 0 for invalid sizes. */
+size_t mgw_grouped_lora_backward_workspace_bytes(int M, int R);
 
 #ifdef __cplusplus
 }

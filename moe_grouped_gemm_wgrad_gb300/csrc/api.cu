@@ -863,6 +863,156 @@ mgw_status mgw_moe_combine_backward(const void* dout, const void* y, int dtype, 
 
 }  // extern "C"
 
+// ------------------------------------------------------------------- low-rank adapters
+namespace {
+
+mgw_status lora_check(const void* x, int x_rows, const int32_t* row_index, int M, int K, const void* a,
+                      const void* b, const float* scale, const int32_t* adapter_off, int E, int R, int N,
+                      const int32_t* out_index, int out_rows) {
+  if (!a || !b || !adapter_off || (M > 0 && !x)) return MGW_ERR_INVALID_ARG;
+  if (M < 0 || K <= 0 || N <= 0 || R <= 0 || x_rows < 0 || out_rows < 0 || E < 1 || E > MGW_MAX_EXPERTS)
+    return MGW_ERR_INVALID_ARG;
+  if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0 || R > MGW_MAX_RANK || K > (1 << 23) || N > (1 << 23))
+    return MGW_ERR_UNSUPPORTED;
+  // row r is row r where there is no index
+  if ((!row_index && x_rows < M) || (!out_index && out_rows < M)) return MGW_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(row_index) || !aligned16(a) || !aligned16(b) || !aligned16(scale) ||
+      !aligned16(adapter_off) || !aligned16(out_index))
+    return MGW_ERR_INVALID_ARG;
+  return MGW_OK;
+}
+
+// 64-column boxes of `rows` rows of a bf16 matrix [total, cols].
+bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t total, uint32_t rows) {
+  return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, total, cols * 2, 64, rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// 64 x `rows` boxes of the bf16 matrices [E, outer, inner]: a box never reaches into the next one.
+bool stack_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t E, uint32_t rows) {
+  const uint64_t dims[3] = {inner, outer, E};
+  const uint64_t strides[2] = {inner * 2, inner * outer * 2};
+  const uint32_t box[3] = {64, rows, 1};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The kernel of lora.cu on W1 [E, R, K] and W2 [E, N, R] (transposed: [E, K, R] and [E, R, N]).
+mgw_status lora_launch(const void* in, int in_rows, const int32_t* in_index, int M, int K, const void* w1,
+                       const void* w2, const float* scale, const int32_t* off, int E, int R, int N,
+                       const void* base, const int32_t* out_index, int out_rows, void* out, float* u,
+                       bool transposed, int* status, int num_sms, void* stream) {
+  mgw::LoraArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const uint32_t rp = static_cast<uint32_t>((R + 15) & ~15);
+  const bool ok = rows_map(&a.tm_x, in, K, in_rows, 128) && rows_map(&a.tm_xg, in, K, in_rows, 1) &&
+                  (transposed ? stack_map(&a.tm_w1, w1, R, K, E, 64) && stack_map(&a.tm_w2, w2, N, R, E, rp)
+                              : stack_map(&a.tm_w1, w1, K, R, E, rp) && stack_map(&a.tm_w2, w2, R, N, E, 128));
+  if (!ok) return MGW_ERR_CUDA;
+  a.off = off;
+  a.in_index = in_index;
+  a.out_index = out_index;
+  a.scale = scale;
+  a.base = base;
+  a.out = out;
+  a.u = u;
+  a.E = E;
+  a.M = M;
+  a.K = K;
+  a.N = N;
+  a.R = R;
+  a.in_rows = in_rows;
+  a.out_rows = out_rows;
+  a.max_cluster = test_max_cluster();
+  a.status = status;
+  const cudaError_t err = mgw::launch_lora(a, transposed, num_sms, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+mgw_status mgw_grouped_lora(const void* x_bf16, int x_rows, const int32_t* row_index, int M, int K,
+                            const void* a_bf16, const void* b_bf16, const float* scale,
+                            const int32_t* adapter_off, int E, int R, int N, const void* base_bf16,
+                            const int32_t* out_index, int out_rows, void* out_bf16, float* u, int* status_dev,
+                            void* stream) {
+  mgw_status st = lora_check(x_bf16, x_rows, row_index, M, K, a_bf16, b_bf16, scale, adapter_off, E, R, N,
+                             out_index, out_rows);
+  if (st != MGW_OK) return st;
+  if (M > 0 && (!out_bf16 || x_rows < 1 || out_rows < 1)) return MGW_ERR_INVALID_ARG;
+  if (!aligned16(base_bf16) || !aligned16(out_bf16) || !aligned16(u)) return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK || M == 0) return st;
+  return lora_launch(x_bf16, x_rows, row_index, M, K, a_bf16, b_bf16, scale, adapter_off, E, R, N, base_bf16,
+                     out_index, out_rows, out_bf16, u, false, status_dev, dev.sms, stream);
+}
+
+size_t mgw_grouped_lora_backward_workspace_bytes(int M, int R) {
+  if (M < 0 || R <= 0 || R > MGW_MAX_RANK) return 0;
+  return sizeof(float) * static_cast<size_t>(M) * static_cast<size_t>(R);
+}
+
+mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const int32_t* out_index,
+                                     const void* x_bf16, int x_rows, const int32_t* row_index, int M, int K,
+                                     const void* a_bf16, const void* b_bf16, const float* scale,
+                                     const int32_t* adapter_off, int E, int R, int N, const float* u,
+                                     const void* dx_base_bf16, void* dx_bf16, void* da_bf16, void* db_bf16,
+                                     void* workspace, size_t workspace_bytes, int* status_dev, void* stream) {
+  mgw_status st = lora_check(da_bf16 ? x_bf16 : dy_bf16, x_rows, row_index, M, K, a_bf16, b_bf16, scale,
+                             adapter_off, E, R, N, out_index, out_rows);
+  if (st != MGW_OK) return st;
+  if (M > 0 && (!dy_bf16 || (db_bf16 && !u) || x_rows < 1 || out_rows < 1)) return MGW_ERR_INVALID_ARG;
+  if (dx_base_bf16 && !dx_bf16) return MGW_ERR_INVALID_ARG;
+  if (!aligned16(dy_bf16) || !aligned16(u) || !aligned16(dx_base_bf16) || !aligned16(dx_bf16) ||
+      !aligned16(da_bf16) || !aligned16(db_bf16) || !aligned16(workspace))
+    return MGW_ERR_INVALID_ARG;
+  if (da_bf16) {
+    const size_t need = mgw_grouped_lora_backward_workspace_bytes(M, R);
+    if (need > 0 && !workspace) return MGW_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MGW_ERR_CAPACITY;
+  }
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK) return st;
+  float* v = da_bf16 ? static_cast<float*>(workspace) : nullptr;
+  if (M > 0 && (dx_bf16 || da_bf16)) {
+    st = lora_launch(dy_bf16, out_rows, out_index, M, N, b_bf16, a_bf16, scale, adapter_off, E, R, K,
+                     dx_base_bf16, out_index, out_rows, dx_bf16, v, true, status_dev, dev.sms, stream);
+    if (st != MGW_OK) return st;
+  }
+  if (!da_bf16 && !db_bf16) return MGW_OK;
+  mgw::LoraGradArgs g;
+  std::memset(&g, 0, sizeof(g));
+  auto job = [&](const void* rows_of, int rows, const int32_t* index, const float* q, void* grad, int cols,
+                 bool by_rank) {
+    mgw::LoraGradJob& j = g.job[g.jobs++];
+    // With no row the maps are never used; they then only need a valid address.
+    const void* base = M > 0 ? rows_of : a_bf16;
+    const uint64_t n = M > 0 ? static_cast<uint64_t>(rows) : 1;
+    j.index = index;
+    j.q = q;
+    j.grad = grad;
+    j.rows = rows;
+    j.cols = cols;
+    j.by_rank = by_rank;
+    return rows_map(&j.tm, base, cols, n, 64) && rows_map(&j.tmg, base, cols, n, 1);
+  };
+  if (db_bf16 && !job(dy_bf16, out_rows, out_index, u, db_bf16, N, false)) return MGW_ERR_CUDA;
+  if (da_bf16 && !job(x_bf16, x_rows, row_index, v, da_bf16, K, true)) return MGW_ERR_CUDA;
+  g.off = adapter_off;
+  g.scale = scale;
+  g.E = E;
+  g.M = M;
+  g.R = R;
+  g.max_cluster = test_max_cluster();
+  g.status = status_dev;
+  const cudaError_t err = mgw::launch_lora_grad(g, dev.sms, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+}  // extern "C"
+
 #ifdef MGW_DIAG
 extern "C" {
 

@@ -53,6 +53,7 @@ ACT_SWIGLU = 4       # silu(gate) * up, the product's columns being gate then up
 ACT_GEGLU = 5        # gelu(gate) * up
 GATED_ACTS = (ACT_SWIGLU, ACT_GEGLU)
 MAX_TOP_K = 32
+MAX_RANK = 128       # of a low-rank adapter
 MAX_SIZE = 2 ** 31 - 1   # of every size and count in the C ABI
 
 EXPORTS = (
@@ -64,6 +65,7 @@ EXPORTS = (
     "mgw_moe_route", "mgw_moe_route_backward", "mgw_moe_dispatch",
     "mgw_moe_dispatch_workspace_bytes", "mgw_grouped_fprop_mxfp8_act", "mgw_grouped_act_backward",
     "mgw_grouped_act_backward_workspace_bytes", "mgw_moe_combine", "mgw_moe_combine_backward",
+    "mgw_grouped_lora", "mgw_grouped_lora_backward", "mgw_grouped_lora_backward_workspace_bytes",
 )
 
 
@@ -135,6 +137,13 @@ def bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mgw_moe_combine.restype = I
     lib.mgw_moe_combine_backward.argtypes = [P, P, I, I, P, P, I, I, I, P, P, P, P]
     lib.mgw_moe_combine_backward.restype = I
+    lib.mgw_grouped_lora.argtypes = [P, I, P, I, I, P, P, P, P, I, I, I, P, P, I, P, P, P, P]
+    lib.mgw_grouped_lora.restype = I
+    lib.mgw_grouped_lora_backward.argtypes = [P, I, P, P, I, P, I, I, P, P, P, P, I, I, I, P, P, P, P, P, P, SZ,
+                                              P, P]
+    lib.mgw_grouped_lora_backward.restype = I
+    lib.mgw_grouped_lora_backward_workspace_bytes.argtypes = [I, I]
+    lib.mgw_grouped_lora_backward_workspace_bytes.restype = SZ
     return lib
 
 
@@ -887,3 +896,135 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: tor
     if side is not None:
         _used_on(side, dout, y, row_of, weights, dy, dweights, status)
     return dy, dweights
+
+
+# ------------------------------------------------------------------- low-rank adapters
+def _adapters(a, b, adapter_off, scale, row_index, out_index):
+    """Checks the adapters and the row tables; returns (E, R, K, N)."""
+    _dev_tensor(a, torch.bfloat16, "a", 3)
+    E, R, K = a.shape
+    _dev_tensor(b, torch.bfloat16, "b", 3)
+    N = b.shape[1]
+    _shaped(b, (E, N, R), torch.bfloat16, "b")
+    _dev_tensor(adapter_off, torch.int32, "adapter_off", 1)
+    if adapter_off.numel() != E + 1:
+        raise MgwError(f"adapter_off has {adapter_off.numel()} entries; {E} adapters need {E + 1}")
+    if scale is not None:
+        _shaped(scale, (E,), torch.float32, "scale")
+    if row_index is not None:
+        _dev_tensor(row_index, torch.int32, "row_index", 1)
+    if out_index is not None:
+        _dev_tensor(out_index, torch.int32, "out_index", 1)
+        if row_index is not None and row_index.numel() != out_index.numel():
+            raise MgwError(f"row_index and out_index name {row_index.numel()} and {out_index.numel()} rows")
+    return E, R, K, N
+
+
+def grouped_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_off: torch.Tensor,
+                 row_index: torch.Tensor | None = None, out_index: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None, base: torch.Tensor | None = None,
+                 save_u: bool = False, out: torch.Tensor | None = None, u: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, stream=None):
+    """out[o] = base[o] + scale[e] * (x[t] a[e]^T) b[e]^T for every row of every adapter, x [rows, K]
+    bf16, a [E, R, K], b [E, N, R] -> out [rows of base, N] bf16; with ``save_u`` (or ``u``) also the
+    intermediate u = x a^T, fp32 [M, R], for :func:`grouped_lora_backward`.
+
+    Adapter e has the rows adapter_off[e] .. adapter_off[e+1]-1; row r reads x[row_index[r]] and is
+    out's row out_index[r] (r itself without an index).  Rows behind adapter_off[E] have no adapter
+    and keep their base.  For requests in token order both indices are the row_index of
+    :func:`moe_dispatch` (top_k 1; an extra last expert for tokens without an adapter, whose offset
+    is left out of ``adapter_off``).  ``base`` is 0 when not given, and may be ``out``.  Rows of out
+    that ``out_index`` does not name are not written."""
+    _dev_tensor(x, torch.bfloat16, "x", 2)
+    E, R, K, N = _adapters(a, b, adapter_off, scale, row_index, out_index)
+    if x.shape[1] != K:
+        raise MgwError(f"x [rows, {x.shape[1]}] and a [E, R, {K}] must share the contraction width")
+    M = x.shape[0] if row_index is None and out_index is None else \
+        (row_index if row_index is not None else out_index).numel()
+    rows = M
+    if base is not None:
+        _dev_tensor(base, torch.bfloat16, "base", 2)
+        rows = base.shape[0]
+        _shaped(base, (rows, N), torch.bfloat16, "base")
+    elif isinstance(out, torch.Tensor) and out.dim() == 2:
+        rows = out.shape[0]
+    if (row_index is None and x.shape[0] < M) or (out_index is None and rows < M):
+        raise MgwError(f"{M} rows need an index, or as many rows of x ({x.shape[0]}) and of out ({rows})")
+    _status(status)
+    dev = _one_device(x, a, b, adapter_off, row_index, out_index, scale, base, out, u, status)
+    side = None if stream is None else _side(stream, dev)
+    out = _out(out, (rows, N), torch.bfloat16, dev, "out", side)
+    if save_u or u is not None:
+        u = _out(u, (M, R), torch.float32, dev, "u", side)
+    with _device(dev):
+        st = load().mgw_grouped_lora(_ptr(x), x.shape[0], _ptr(row_index), M, K, _ptr(a), _ptr(b),
+                                     _ptr(scale), _ptr(adapter_off), E, R, N, _ptr(base),
+                                     _ptr(out_index), rows, _ptr(out), _ptr(u), _ptr(status),
+                                     _stream(stream))
+    _check(st, "mgw_grouped_lora")
+    if side is not None:
+        _used_on(side, x, a, b, adapter_off, row_index, out_index, scale, base, out, u, status)
+    return out if u is None else (out, u)
+
+
+def grouped_lora_backward(dy: torch.Tensor, x: torch.Tensor | None, u: torch.Tensor | None,
+                          a: torch.Tensor, b: torch.Tensor, adapter_off: torch.Tensor,
+                          row_index: torch.Tensor | None = None, out_index: torch.Tensor | None = None,
+                          scale: torch.Tensor | None = None, dx_base: torch.Tensor | None = None,
+                          with_dx: bool = True, with_weights: bool = True,
+                          dx: torch.Tensor | None = None, da: torch.Tensor | None = None,
+                          db: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, stream=None):
+    """-> (dx, da, db): the backward pass of :func:`grouped_lora` from dy [rows of out, N] bf16.
+    dx [rows of out, K] bf16 = dx_base + the adapters' share (rows without an adapter: dx_base, 0
+    when not given; ``dx_base`` may be ``dx``), da [E, R, K] and db [E, N, R] bf16; ``x`` and ``u``
+    as in the forward call.  Without ``with_dx`` dx is None; without ``with_weights`` da and db are,
+    and ``x`` and ``u`` may be None.  ``workspace`` (uint8) is allocated when none is given."""
+    _dev_tensor(dy, torch.bfloat16, "dy", 2)
+    E, R, K, N = _adapters(a, b, adapter_off, scale, row_index, out_index)
+    rows = dy.shape[0]
+    if dy.shape[1] != N:
+        raise MgwError(f"dy [rows, {dy.shape[1]}] does not match b [E, {N}, R]")
+    if not with_dx and (dx is not None or dx_base is not None):
+        raise MgwError("dx and dx_base need with_dx")
+    if not with_weights and (da is not None or db is not None):
+        raise MgwError("da and db need with_weights")
+    if with_weights:
+        if x is None or u is None:
+            raise MgwError("x and u are needed for the adapters' gradients")
+        _dev_tensor(x, torch.bfloat16, "x", 2)
+        if x.shape[1] != K:
+            raise MgwError(f"x [rows, {x.shape[1]}] and a [E, R, {K}] must share the contraction width")
+    x_rows = rows if x is None else x.shape[0]
+    M = rows if row_index is None and out_index is None else \
+        (row_index if row_index is not None else out_index).numel()
+    if (row_index is None and x_rows < M) or (out_index is None and rows < M):
+        raise MgwError(f"{M} rows need an index, or as many rows of x ({x_rows}) and of dy ({rows})")
+    if u is not None:
+        _shaped(u, (M, R), torch.float32, "u")
+    if dx_base is not None:
+        _shaped(dx_base, (rows, K), torch.bfloat16, "dx_base")
+    _status(status)
+    dev = _one_device(dy, x, u, a, b, adapter_off, row_index, out_index, scale, dx_base, dx, da, db,
+                      workspace, status)
+    side = None if stream is None else _side(stream, dev)
+    lib = load()
+    if with_dx:
+        dx = _out(dx, (rows, K), torch.bfloat16, dev, "dx", side)
+    if with_weights:
+        da = _out(da, (E, R, K), torch.bfloat16, dev, "da", side)
+        db = _out(db, (E, N, R), torch.bfloat16, dev, "db", side)
+        need = int(lib.mgw_grouped_lora_backward_workspace_bytes(M, R))
+        workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side)
+    with _device(dev):
+        st = lib.mgw_grouped_lora_backward(_ptr(dy), rows, _ptr(out_index), _ptr(x), x_rows,
+                                           _ptr(row_index), M, K, _ptr(a), _ptr(b), _ptr(scale),
+                                           _ptr(adapter_off), E, R, N, _ptr(u), _ptr(dx_base),
+                                           _ptr(dx), _ptr(da), _ptr(db), _ptr(workspace),
+                                           0 if workspace is None else workspace.numel(),
+                                           _ptr(status), _stream(stream))
+    _check(st, "mgw_grouped_lora_backward")
+    if side is not None:
+        _used_on(side, dy, x, u, a, b, adapter_off, row_index, out_index, scale, dx_base, dx, da, db,
+                 workspace, status)
+    return dx, da, db
