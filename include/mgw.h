@@ -518,11 +518,11 @@ mgw_status mgw_grouped_lora(const void *x_bf16, int x_rows, const int32_t *row_i
  * times adds them up with mgw_moe_combine.  Adapters without rows get zeros; rows without an
  * adapter dx_base.  All sums are fp32 in an order that the sizes fix; each output is rounded once.
  * dy, dx_base device, bf16 [out_rows, N] and [out_rows, K] (dx_base nullable (0); may be dx).
- * u           device fp32 [M, R] from the forward call; needed with db.
- * dx          device, bf16 [out_rows, K], nullable.  da: device, bf16 [E, R, K], nullable.
- * db          device, bf16 [E, N, R], nullable.  x is needed with da only.
- * workspace   device, 16-byte aligned, mgw_grouped_lora_backward_workspace_bytes bytes, when da is
- *             given; need not be initialised.
+ * dx          device, bf16 [out_rows, K], nullable.
+ * da, db      device, bf16 [E, R, K] and [E, N, R], fully written; both or (null) neither.
+ * x, u        (fp32 [M, R] from the forward call) are needed with da and db only.
+ * workspace   device, 16-byte aligned, mgw_grouped_lora_backward_workspace_bytes bytes, when da and
+ *             db are given; need not be initialised.  Calls sharing it must not overlap.
  * Everything else as in the forward call. */
 mgw_status mgw_grouped_lora_backward(const void *dy_bf16, int out_rows, const int32_t *out_index,
                                      const void *x_bf16, int x_rows, const int32_t *row_index,
@@ -532,7 +532,7 @@ mgw_status mgw_grouped_lora_backward(const void *dy_bf16, int out_rows, const in
                                      void *dx_bf16, void *da_bf16, void *db_bf16, void *workspace,
                                      size_t workspace_bytes, int *status_dev, void *stream);
 /* Host only; 0 for invalid sizes. */
-size_t mgw_grouped_lora_backward_workspace_bytes(int M, int R);
+size_t mgw_grouped_lora_backward_workspace_bytes(int E, int M, int K, int N, int R);
 
 #ifdef __cplusplus
 }

@@ -899,14 +899,18 @@ bool stack_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
 mgw_status lora_launch(const void* in, int in_rows, const int32_t* in_index, int M, int K, const void* w1,
                        const void* w2, const float* scale, const int32_t* off, int E, int R, int N,
                        const void* base, const int32_t* out_index, int out_rows, void* out, float* u,
-                       bool transposed, int* status, int num_sms, void* stream) {
+                       bool transposed, const float* u_in, uint8_t* qu, uint8_t* qv, int* status, int num_sms,
+                       void* stream) {
   mgw::LoraArgs a;
   std::memset(&a, 0, sizeof(a));
   const uint32_t rp = static_cast<uint32_t>((R + 15) & ~15);
-  const bool ok = rows_map(&a.tm_x, in, K, in_rows, 128) && rows_map(&a.tm_xg, in, K, in_rows, 1) &&
+  const bool ok = rows_map(&a.tm_x, in, K, in_rows, 128) &&
                   (transposed ? stack_map(&a.tm_w1, w1, R, K, E, 64) && stack_map(&a.tm_w2, w2, N, R, E, rp)
-                              : stack_map(&a.tm_w1, w1, K, R, E, rp) && stack_map(&a.tm_w2, w2, R, N, E, 128));
+                              : stack_map(&a.tm_w1, w1, K, R, E, rp) && stack_map(&a.tm_w2, w2, R, N, E, 64)) &&
+                  (!base || rows_map(&a.tm_base, base, N, out_rows, 128)) &&
+                  (!out || rows_map(&a.tm_out, out, N, out_rows, 32));
   if (!ok) return MGW_ERR_CUDA;
+  a.in = in;
   a.off = off;
   a.in_index = in_index;
   a.out_index = out_index;
@@ -914,6 +918,9 @@ mgw_status lora_launch(const void* in, int in_rows, const int32_t* in_index, int
   a.base = base;
   a.out = out;
   a.u = u;
+  a.u_in = u_in;
+  a.qu = qu;
+  a.qv = qv;
   a.E = E;
   a.M = M;
   a.K = K;
@@ -945,12 +952,12 @@ mgw_status mgw_grouped_lora(const void* x_bf16, int x_rows, const int32_t* row_i
   st = current_device(&dev);
   if (st != MGW_OK || M == 0) return st;
   return lora_launch(x_bf16, x_rows, row_index, M, K, a_bf16, b_bf16, scale, adapter_off, E, R, N, base_bf16,
-                     out_index, out_rows, out_bf16, u, false, status_dev, dev.sms, stream);
+                     out_index, out_rows, out_bf16, u, false, nullptr, nullptr, nullptr, status_dev, dev.sms, stream);
 }
 
-size_t mgw_grouped_lora_backward_workspace_bytes(int M, int R) {
-  if (M < 0 || R <= 0 || R > MGW_MAX_RANK) return 0;
-  return sizeof(float) * static_cast<size_t>(M) * static_cast<size_t>(R);
+size_t mgw_grouped_lora_backward_workspace_bytes(int E, int M, int K, int N, int R) {
+  if (E < 1 || E > MGW_MAX_EXPERTS || M < 0 || K <= 0 || N <= 0 || R <= 0 || R > MGW_MAX_RANK) return 0;
+  return 2 * mgw::lora_q_bytes(M, E, R) + mgw::lora_partial_bytes(K, N, R);
 }
 
 mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const int32_t* out_index,
@@ -962,52 +969,58 @@ mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const in
   mgw_status st = lora_check(da_bf16 ? x_bf16 : dy_bf16, x_rows, row_index, M, K, a_bf16, b_bf16, scale,
                              adapter_off, E, R, N, out_index, out_rows);
   if (st != MGW_OK) return st;
-  if (M > 0 && (!dy_bf16 || (db_bf16 && !u) || x_rows < 1 || out_rows < 1)) return MGW_ERR_INVALID_ARG;
+  const bool weights = da_bf16 != nullptr;
+  if (weights != (db_bf16 != nullptr)) return MGW_ERR_INVALID_ARG;
+  if (M > 0 && (!dy_bf16 || (weights && !u) || x_rows < 1 || out_rows < 1)) return MGW_ERR_INVALID_ARG;
   if (dx_base_bf16 && !dx_bf16) return MGW_ERR_INVALID_ARG;
   if (!aligned16(dy_bf16) || !aligned16(u) || !aligned16(dx_base_bf16) || !aligned16(dx_bf16) ||
       !aligned16(da_bf16) || !aligned16(db_bf16) || !aligned16(workspace))
     return MGW_ERR_INVALID_ARG;
-  if (da_bf16) {
-    const size_t need = mgw_grouped_lora_backward_workspace_bytes(M, R);
+  if (weights) {
+    const size_t need = mgw_grouped_lora_backward_workspace_bytes(E, M, K, N, R);
     if (need > 0 && !workspace) return MGW_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MGW_ERR_CAPACITY;
   }
   DeviceInfo dev;
   st = current_device(&dev);
-  if (st != MGW_OK) return st;
-  float* v = da_bf16 ? static_cast<float*>(workspace) : nullptr;
-  if (M > 0 && (dx_bf16 || da_bf16)) {
+  if (st != MGW_OK || (!weights && !dx_bf16)) return st;
+  const size_t q_bytes = mgw::lora_q_bytes(M, E, R);
+  uint8_t* qu = weights ? static_cast<uint8_t*>(workspace) : nullptr;
+  uint8_t* qv = weights ? qu + q_bytes : nullptr;
+  if (M > 0) {
     st = lora_launch(dy_bf16, out_rows, out_index, M, N, b_bf16, a_bf16, scale, adapter_off, E, R, K,
-                     dx_base_bf16, out_index, out_rows, dx_bf16, v, true, status_dev, dev.sms, stream);
+                     dx_base_bf16, out_index, out_rows, dx_bf16, nullptr, true, u, qu, qv, status_dev, dev.sms,
+                     stream);
     if (st != MGW_OK) return st;
   }
-  if (!da_bf16 && !db_bf16) return MGW_OK;
+  if (!weights) return MGW_OK;
   mgw::LoraGradArgs g;
   std::memset(&g, 0, sizeof(g));
-  auto job = [&](const void* rows_of, int rows, const int32_t* index, const float* q, void* grad, int cols,
-                 bool by_rank) {
-    mgw::LoraGradJob& j = g.job[g.jobs++];
+  auto job = [&](mgw::LoraGradJob& j, const void* rows_of, int rows, const int32_t* index, const uint8_t* q,
+                 void* grad, int cols, bool by_rank) {
     // With no row the maps are never used; they then only need a valid address.
     const void* base = M > 0 ? rows_of : a_bf16;
     const uint64_t n = M > 0 ? static_cast<uint64_t>(rows) : 1;
+    j.x = rows_of;
     j.index = index;
     j.q = q;
     j.grad = grad;
     j.rows = rows;
     j.cols = cols;
     j.by_rank = by_rank;
-    return rows_map(&j.tm, base, cols, n, 64) && rows_map(&j.tmg, base, cols, n, 1);
+    return rows_map(&j.tm, base, cols, n, 64);
   };
-  if (db_bf16 && !job(dy_bf16, out_rows, out_index, u, db_bf16, N, false)) return MGW_ERR_CUDA;
-  if (da_bf16 && !job(x_bf16, x_rows, row_index, v, da_bf16, K, true)) return MGW_ERR_CUDA;
+  if (!job(g.job[0], dy_bf16, out_rows, out_index, qu, db_bf16, N, false) ||
+      !job(g.job[1], x_bf16, x_rows, row_index, qv, da_bf16, K, true))
+    return MGW_ERR_CUDA;
   g.off = adapter_off;
-  g.scale = scale;
+  g.partial = reinterpret_cast<float*>(qu + 2 * q_bytes);
   g.E = E;
   g.M = M;
   g.R = R;
   g.max_cluster = test_max_cluster();
   g.status = status_dev;
-  const cudaError_t err = mgw::launch_lora_grad(g, dev.sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = mgw::launch_lora_grad(g, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
 }
 

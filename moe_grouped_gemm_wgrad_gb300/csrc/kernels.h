@@ -214,45 +214,52 @@ cudaError_t launch_combine_backward(const CombineBwdArgs& a, bool f32, cudaStrea
 constexpr int kMaxRank = 128;
 struct LoraArgs {
   CUtensorMap tm_x;    // in bf16 [in_rows, K], box 64 columns x 128 rows, 128B swizzle
-  CUtensorMap tm_xg;   // the same, box 64 columns x 1 row
   CUtensorMap tm_w1;   // [E, R, K]: box 64 x padded rank; transposed [E, K, R]: box 64 x 64
-  CUtensorMap tm_w2;   // [E, N, R]: box 64 x 128; transposed [E, R, N]: box 64 x padded rank
+  CUtensorMap tm_w2;   // [E, N, R]: box 64 x 64; transposed [E, R, N]: box 64 x padded rank
+  CUtensorMap tm_base; // base bf16 [out_rows, N], box 64 columns x 128 rows (when given)
+  CUtensorMap tm_out;  // out bf16 [out_rows, N], box 64 columns x 32 rows (when given)
   const int32_t* off;        // [E + 1], off[E] <= M: rows behind it have no adapter
+  const void* in;
   const int32_t* in_index;   // [M] or null: row r reads row in_index[r] of in
   const int32_t* out_index;  // [M] or null: row r is row out_index[r] of base and out
   const float* scale;        // [E] or null
   const void* base;          // bf16 [out_rows, N] or null
   void* out;                 // bf16 [out_rows, N]; null: u only
   float* u;                  // fp32 [M, R] in W1^T, or null
+  // For lora_grad.cu (transposed, or null): u of the forward pass (fp32 [M, R]) and v = in W1^T, both
+  // scaled, in blocks of 64 rows of an adapter: two blocks for each of its row tiles of 128, a
+  // block [2 padded ranks][64 rows], the high parts before the low ones, in 128-byte swizzled rows.
+  const float* u_in;
+  uint8_t* qu;
+  uint8_t* qv;
   int E, M, K, N, R, in_rows, out_rows;
-  int cluster;               // set by the launch
+  int cluster, ring;         // set by the launch
   int max_cluster;           // test hook, as DispatchArgs::max_cluster
   int* status;
 };
 cudaError_t launch_lora(const LoraArgs& a, bool transposed, int num_sms, cudaStream_t stream);
 
-// Gradients of the adapters (lora_grad.cu): grad = scale X^T Q over the rows of every adapter.
+// Gradients of the adapters (lora_grad.cu): grad = X^T Q over the rows of every adapter.
 struct LoraGradJob {
   CUtensorMap tm;        // X bf16 [rows, cols], box 64 columns x 64 rows, 128B swizzle
-  CUtensorMap tmg;       // the same, box 64 columns x 1 row
+  const void* x;
   const int32_t* index;  // [M] or null: row r is row index[r] of X
-  const float* q;        // fp32 [M, R]
+  const uint8_t* q;      // Q's blocks of 64 tokens (LoraArgs::qu, qv)
   void* grad;            // bf16 [E, R, cols] (by_rank) or [E, cols, R]
   int rows, cols, by_rank;
 };
 struct LoraGradArgs {
   LoraGradJob job[2];
   const int32_t* off;
-  const float* scale;
-  int jobs, E, M, R;
-  int first[2], stages, cluster;  // set by the launch
-  uint32_t tmem_cols;
-  int max_cluster;
+  float* partial;        // lora_partial_bytes
+  int E, M, R;
+  int first1, stages, cluster;  // set by the launch
+  int max_cluster;       // test hook, as DispatchArgs::max_cluster
   int* status;
 };
-// Work items of one gradient (counted in 32 bits).
-long long lora_grad_items(int E, int cols, int R);
-cudaError_t launch_lora_grad(const LoraGradArgs& a, int num_sms, cudaStream_t stream);
+size_t lora_q_bytes(int M, int E, int R);
+size_t lora_partial_bytes(int K, int N, int R);
+cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream);
 
 struct DgradArgs {
   CUtensorMap tm_w;    // W fp32 [E*out_f, in_f], box 256 columns x 32 rows, no swizzle

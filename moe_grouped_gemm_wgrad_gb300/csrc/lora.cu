@@ -14,9 +14,13 @@
 // backward pass wants it), one launch does it all, and few rows still use many SMs: a decode step's
 // rows stream their adapters through eight SMs each.
 //
-// Roles (192 threads): warp 0 loads operands by TMA (x rows by gather4 where they are not a whole
-// tile in order), warp 1 issues the MMAs, warps 2-5 hold the TMEM lane quarters: partial sums, then
-// the output's epilogue (accumulator + base, rounded once, whole 128-byte row pieces).
+// Both halves stream through one ring of shared-memory slots: 64 columns of 128 rows (the input's,
+// then the base's, which become the output's in place) and the weight's tile that goes with them.
+// Roles (320 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-9 are two sets, each a warp
+// to a TMEM lane quarter.  They copy the input's rows where these are few or lie apart (16 bytes a
+// lane; gathered by TMA, four rows an instruction, 65536 rows took 1.5 times as long), turn the
+// partial sums into the intermediate, and take the output's tiles in turns: accumulator + base, rounded
+// once, stored by TMA, or as whole 128-byte row pieces where rows lie apart.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -28,62 +32,91 @@ namespace {
 
 using namespace lora;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
+constexpr int kBound = 384;           // registers are given out to four warps at a time
 constexpr int kRows = 128;
-constexpr int kBk = 64;               // input columns per stage
-constexpr int kBn = 128;              // output columns per tile
+constexpr int kBk = 64;               // columns per slot, of the input and of the output
 constexpr int kXBytes = kRows * 128;  // 128 rows of 64 bf16
-constexpr uint32_t kTmemCols = 256;   // two output tiles; the partial sums use the first one's
-constexpr int kBars = 2 * 6 + 1 + 2 + 2 + 2 + 2 + 1;
+constexpr int kMaxSlots = 12;
+constexpr int kBufs = 4;              // accumulators of 64 columns
+constexpr uint32_t kTmemCols = 256;   // those; before them the partial sums
+constexpr int kBars = 4 * kMaxSlots + 1 + 2 * kBufs + 1;
+constexpr int kTmpBytes = 80;         // find_tile's 18 ints; then [4] TMEM [5] abort
 
-// RB: 64-wide blocks of the rank.  The ring's memory is used again behind the contraction: partial
-// sums (then the epilogue's staging), the intermediate's two parts, two tiles of W2.
-template <int RB>
+// RQ: the rank, rounded up to 32, 64 or 128.  The intermediate's two parts are 2 RQ columns, in
+// 64-wide tiles.  The ring's slots are as large as the tile's rows and the rank need, so that few rows
+// have all their loads on the way at once; the tensor core reads 128 rows all the same, into the
+// slots behind (those rows' results go nowhere).
+template <int RQ>
 struct Plan {
-  static constexpr int kStages = RB == 1 ? 4 : 6;
-  static constexpr int kStage = kXBytes + RB * 8192;
-  static constexpr int kPart = 0;
-  static constexpr int kU = RB * 32768;
-  static constexpr int kULo = kU + RB * kXBytes;
-  static constexpr int kW2 = RB * 65536;
-  static constexpr int kW2Tile = RB * 16384;
-  static constexpr int kOffBar = RB * 98304;
-  static constexpr int kOffTmp = kOffBar + kBars * 8;       // find_tile; [4] TMEM [5] abort
-  static constexpr int kOffRows = (kOffTmp + 80 + 15) & ~15;  // place of the 128 output rows
-  static constexpr size_t kSmem = kOffRows + kRows * 4 + 1024;
-  static_assert(kStages * kStage <= kOffBar, "ring");
-  static_assert(2 * kStages + 7 <= kBars, "barriers");
+  static constexpr int kWBytes = RQ == 128 ? 16384 : 8192;  // of a slot, at most
+  static constexpr int kU = RQ * 512;
+  // Partial sums are kept in this many accumulators in turn, added up at the end: the tensor core
+  // cuts each addition's low bits off, always downwards, so a long chain drifts (u of K = 4096: 4.4e-6
+  // relative in one chain, 4.7e-7 in four).
+  static constexpr int kChains = RQ == 128 ? 2 : 4;
+  // The ring: two CTAs an SM, or one with a long ring where there are few.
+  static constexpr int kShort = (RQ == 128 ? 160 : (RQ == 64 ? 78 : 94)) * 1024;
+  static constexpr int kLong = (RQ == 128 ? 160 : (RQ == 64 ? 192 : 208)) * 1024;
+  static constexpr size_t smem(int ring) {
+    return static_cast<size_t>(ring) + kU + kBars * 8 + kTmpBytes + kRows * 4 + 1024;
+  }
+  // the CTAs' partial sums lie at the ring's end while they are exchanged; two slots remain
+  static_assert(kShort - RQ * 512 >= kXBytes + kWBytes && kXBytes <= kU, "ring");
 };
-static_assert(2 * Plan<1>::kSmem <= 227 * 1024 && Plan<2>::kSmem <= 227 * 1024, "shared memory budget");
+static_assert(2 * (Plan<32>::smem(Plan<32>::kShort) + 1024) <= 228 * 1024 &&
+                  2 * (Plan<64>::smem(Plan<64>::kShort) + 1024) <= 228 * 1024 &&
+                  Plan<32>::smem(Plan<32>::kLong) <= 227 * 1024 && Plan<64>::smem(Plan<64>::kLong) <= 227 * 1024 &&
+                  Plan<128>::smem(Plan<128>::kLong) <= 227 * 1024,
+              "shared memory budget");
+static_assert(kBars * 8 % 16 == 0, "alignment");
 
-template <bool TRANS, int RB>
-__global__ void __launch_bounds__(kThreads, RB == 1 ? 2 : 1) lora_kernel(const __grid_constant__ LoraArgs a) {
-  using P = Plan<RB>;
-  constexpr int S = P::kStages;
+// A place in a ring of n: its slot and the parity of its round.
+struct Turn {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ void step(int by, int n) {
+    slot += by;
+    if (slot >= n) slot -= n, phase ^= 1u;
+  }
+};
+
+template <bool TRANS, int RQ>
+__global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+  using P = Plan<RQ>;
+  constexpr int G = P::kChains;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  int* s_tmp = reinterpret_cast<int*>(smem + P::kOffTmp);
-  int* s_rows = reinterpret_cast<int*>(smem + P::kOffRows);
+  const uint32_t su = sbase + a.ring;  // the intermediate
+  const uint32_t bar0 = su + P::kU;
+  uint8_t* misc = smem + a.ring + P::kU + kBars * 8;
+  int* s_tmp = reinterpret_cast<int*>(misc);                          // find_tile; [4] TMEM [5] abort
+  int* s_rows = reinterpret_cast<int*>(misc + kTmpBytes);                    // place of the 128 output rows
   volatile int* abort_flag = reinterpret_cast<volatile int*>(s_tmp + 5);
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t lane = lane_id();
   const int C = a.cluster;
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  if (tid == 0) {
+    tma_prefetch_desc(&a.tm_x);
+    tma_prefetch_desc(&a.tm_w1);
+    tma_prefetch_desc(&a.tm_w2);
+  }
 
   RowTile t;
   if (!find_tile<kThreads, kRows>(a.off, a.E, a.M, static_cast<int>(blockIdx.x) / C, s_tmp, a.status, t)) return;
   if (t.nrows == 0) return;
   const int N = a.N;
-  const int ntiles = (N + kBn - 1) / kBn;
+  const int ntiles = (N + kBk - 1) / kBk;
   const int nt0 = static_cast<int>(static_cast<long long>(ntiles) * rank / C);
-  const int nt1 = static_cast<int>(static_cast<long long>(ntiles) * (rank + 1) / C);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
   const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.base);
+  const int nt1 = out == nullptr ? nt0 : static_cast<int>(static_cast<long long>(ntiles) * (rank + 1) / C);
 
   if (t.e == a.E) {
     // Rows without an adapter: their base, or zeros.
-    const int c0 = nt0 * kBn, c1 = min(nt1 * kBn, N);
+    const int c0 = nt0 * kBk, c1 = min(nt1 * kBk, N);
     for (int i = warp; i < t.nrows; i += kThreads / 32) {
       const int r = t.row0 + i;
       if (a.u != nullptr && rank == 0)
@@ -101,38 +134,55 @@ __global__ void __launch_bounds__(kThreads, RB == 1 ? 2 : 1) lora_kernel(const _
     return;
   }
 
-  const uint32_t bar0 = sbase + P::kOffBar;
+  // Rows in order come as one box, a tile's last rows too as long as they are many: the rows behind
+  // them, another adapter's, meet nothing of this one's.  Others are copied.
+  const bool many = t.nrows >= kRows / 2;
+  const bool in_box = a.in_index == nullptr && many, out_box = a.out_index == nullptr && many;
+  const bool copy_base = base != nullptr && !out_box;
+  const int RP = (a.R + 15) & ~15;
+  const int rows8 = many ? kRows : (t.nrows + 7) & ~7;
+  const int x_tile = rows8 * 128;  // bytes of a slot's rows; the weight's tile lies behind them
+  const int w1_tile = TRANS ? P::kWBytes : RP * 128, w2_tile = TRANS ? RP * 128 : P::kWBytes;
+  const int slot1 = x_tile + w1_tile, slot2 = x_tile + w2_tile;
+  const int S1 = min(kMaxSlots, a.ring / slot1), S2 = min(kMaxSlots, a.ring / slot2);
+  const int part_at = a.ring - rows8 * RP * 4;
+  const uint32_t part = sbase + part_at;  // partial sums
+  // Slots of the output's half that may be filled while the partial sums are exchanged.
+  const int early = C > 1 ? min(S2, part_at / slot2) : S2;
+  const int nch = (a.K + kBk - 1) / kBk;
+  const int c0 = static_cast<int>(static_cast<long long>(nch) * rank / C);
+  const int c1 = static_cast<int>(static_cast<long long>(nch) * (rank + 1) / C);
+  const int chunks = c1 - c0, tiles = nt1 - nt0;
+
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
-  auto bar_empty = [&](int s) { return bar0 + 8u * (S + s); };
-  const uint32_t bar_sum = bar0 + 8u * (2 * S);
-  auto bar_wfull = [&](int s) { return bar0 + 8u * (2 * S + 1 + s); };
-  auto bar_wempty = [&](int s) { return bar0 + 8u * (2 * S + 3 + s); };
-  auto bar_acc = [&](int s) { return bar0 + 8u * (2 * S + 5 + s); };
-  auto bar_free = [&](int s) { return bar0 + 8u * (2 * S + 7 + s); };
-  const uint32_t bar_done = bar0 + 8u * (2 * S + 9);
+  auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxSlots + s); };
+  auto bar_bfull = [&](int s) { return bar0 + 8u * (2 * kMaxSlots + s); };
+  auto bar_bempty = [&](int s) { return bar0 + 8u * (3 * kMaxSlots + s); };
+  const uint32_t bar_sum = bar0 + 8u * (4 * kMaxSlots);
+  auto bar_acc = [&](int s) { return bar0 + 8u * (4 * kMaxSlots + 1 + s); };
+  auto bar_free = [&](int s) { return bar0 + 8u * (4 * kMaxSlots + 1 + kBufs + s); };
+  const uint32_t bar_done = bar0 + 8u * (4 * kMaxSlots + 1 + 2 * kBufs);
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(bar_full(s), 1);
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(bar_full(s), in_box ? 1 : 1 + 256);
       mbar_init(bar_empty(s), 1);
+      mbar_init(bar_bfull(s), 1);
+      mbar_init(bar_bempty(s), 4);
     }
     mbar_init(bar_sum, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar_wfull(s), 1);
-      mbar_init(bar_wempty(s), 1);
+    for (int s = 0; s < kBufs; ++s) {
       mbar_init(bar_acc(s), 1);
       mbar_init(bar_free(s), 4);
     }
     mbar_init(bar_done, 1);
     fence_mbar_init();
     s_tmp[5] = 0;
-    tma_prefetch_desc(&a.tm_w1);
-    tma_prefetch_desc(&a.tm_w2);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmp + 4), kTmemCols);
     tmem_relinquish();
   }
-  if (tid >= 64) {
+  if (tid >= 64 && tid < 64 + kRows) {
     const int i = tid - 64;
     s_rows[i] = i < t.nrows ? row_place(a.out_index, t.row0 + i, a.out_rows, rank == 0 ? a.status : nullptr) : -1;
   }
@@ -140,111 +190,90 @@ __global__ void __launch_bounds__(kThreads, RB == 1 ? 2 : 1) lora_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(s_tmp[4]);
-  const int RP = (a.R + 15) & ~15;
-  const int nch = (a.K + kBk - 1) / kBk;
-  const int c0 = static_cast<int>(static_cast<long long>(nch) * rank / C);
-  const int c1 = static_cast<int>(static_cast<long long>(nch) * (rank + 1) / C);
+  bool ok = true;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const bool whole = a.in_index == nullptr && t.nrows == kRows;
-    int idx[4];
-    const int groups = (t.nrows + 3) >> 2;
-    if (!whole) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 4 * static_cast<int>(lane) + j;
-        idx[j] = i < t.nrows ? row_place(a.in_index, t.row0 + i, a.in_rows, rank == 0 ? a.status : nullptr) : -1;
-      }
-    }
-    const uint32_t w1_bytes = TRANS ? RB * 8192u : static_cast<uint32_t>(RP) * 128u;
-    const uint32_t x_bytes = whole ? static_cast<uint32_t>(kXBytes) : static_cast<uint32_t>(groups) * 512u;
-    bool ok = true;
-    int stage = 0, n = 0;
-    uint32_t phase = 0;
+    Turn in = {0, 0};
+    int n = 0;
     for (int c = c0; c < c1; ++c) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag))) {
-        ok = false;
-        break;
-      }
-      const uint32_t fb = bar_full(stage);
-      const uint32_t sx = sbase + stage * P::kStage, sw = sx + kXBytes;
+      ok = wait_all(bar_empty(in.slot), in.phase ^ 1u, abort_flag);
+      if (!ok) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(fb, x_bytes + w1_bytes);
+        const uint32_t fb = bar_full(in.slot), sx = sbase + in.slot * slot1, sw = sx + x_tile;
+        mbar_arrive_expect_tx(fb, (in_box ? static_cast<uint32_t>(kXBytes) : 0u) + w1_tile);
         if constexpr (TRANS) {
 #pragma unroll
-          for (int b = 0; b < RB; ++b) tma_load_3d(sw + b * 8192, &a.tm_w1, 64 * b, c * kBk, t.e, fb);
+          for (int b = 0; b < P::kWBytes / 8192; ++b) tma_load_3d(sw + b * 8192, &a.tm_w1, 64 * b, c * kBk, t.e, fb);
         } else {
           tma_load_3d(sw, &a.tm_w1, c * kBk, 0, t.e, fb);
         }
-        if (whole) tma_load_2d(sx, &a.tm_x, c * kBk, t.row0, fb);
+        if (in_box) tma_load_2d(sx, &a.tm_x, c * kBk, t.row0, fb);
       }
       __syncwarp();
-      if (!whole && static_cast<int>(lane) < groups) tma_gather4(sx + lane * 512u, &a.tm_xg, c * kBk, idx, fb);
       ++n;
-      if (++stage == S) stage = 0, phase ^= 1u;
+      in.step(1, S1);
     }
-    // W2 lies in the ring's memory: behind the last MMA that reads the ring.
-    ok = __all_sync(0xffffffffu, ok && mbar_wait(bar_sum, 0, abort_flag));
-    int w = 0;
-    auto load_w2 = [&](int nt) {
-      const uint32_t fb = bar_wfull(w & 1), dst = sbase + P::kW2 + (w & 1) * P::kW2Tile;
+    // Behind the last MMA that reads them the slots serve the output's half.
+    ok = ok && wait_all(bar_sum, 0, abort_flag);
+    const bool base_box = base != nullptr && out_box;
+    Turn to = {0, 0};
+    int i = 0;
+    auto load_tile = [&]() {
       if (lane == 0) {
+        const uint32_t fb = bar_bfull(to.slot), dst = sbase + to.slot * slot2, sw = dst + x_tile;
+        const int col = (nt0 + i) * kBk;
+        mbar_arrive_expect_tx(fb, (base_box ? static_cast<uint32_t>(kXBytes) : 0u) + w2_tile);
+        if (base_box) tma_load_2d(dst, &a.tm_base, col, t.row0, fb);
         if constexpr (TRANS) {
-          mbar_arrive_expect_tx(fb, 2u * RP * 128u);
-          tma_load_3d(dst, &a.tm_w2, nt * kBn, 0, t.e, fb);
-          tma_load_3d(dst + P::kW2Tile / 2, &a.tm_w2, nt * kBn + 64, 0, t.e, fb);
+          tma_load_3d(sw, &a.tm_w2, col, 0, t.e, fb);
         } else {
-          mbar_arrive_expect_tx(fb, P::kW2Tile);
 #pragma unroll
-          for (int b = 0; b < RB; ++b) tma_load_3d(dst + b * 16384, &a.tm_w2, 64 * b, nt * kBn, t.e, fb);
+          for (int b = 0; b < P::kWBytes / 8192; ++b) tma_load_3d(sw + b * 8192, &a.tm_w2, 64 * b, col, t.e, fb);
         }
       }
-      ++w;
+      __syncwarp();
+      ++i;
+      to.step(1, S2);
     };
-    int nt = nt0;
-    if (ok && out != nullptr)
-      for (; nt < nt1 && w < 2; ++nt) load_w2(nt);
-    __syncwarp();
+    while (ok && i < tiles && i < early) load_tile();
     cluster_sync();  // partial sums are there
     cluster_sync();  // the intermediate is
-    for (; ok && out != nullptr && nt < nt1; ++nt) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_wempty(w & 1), ((w >> 1) & 1) ^ 1u, abort_flag));
-      if (ok) load_w2(nt);
-      __syncwarp();
+    fence_async_all();
+    while (ok && i < tiles) {
+      ok = wait_all(bar_bempty(to.slot), to.phase ^ 1u, abort_flag);
+      if (ok) load_tile();
     }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      if (a.status) atomicOr(a.status, kDevTimeout);
-    }
-    // Never leave the CTA with copies still landing in shared memory.
-    for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait_drain(bar_full(i % S), (i / S) & 1u);
-    for (int i = w > 2 ? w - 2 : 0; i < w; ++i) mbar_wait_drain(bar_wfull(i & 1), (i >> 1) & 1u);
+    if (!ok && lane == 0) give_up(abort_flag, a.status);
+    // Never leave the CTA with copies still landing in shared memory (behind a wait that ran out they
+    // have long landed).
+    bool landed = true;
+    for (int k = n > S1 ? n - S1 : 0; landed && k < n; ++k) landed = mbar_wait_drain(bar_full(k % S1), (k / S1) & 1u);
+    for (int k = i > S2 ? i - S2 : 0; landed && k < i; ++k) landed = mbar_wait_drain(bar_bfull(k % S2), (k / S2) & 1u);
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     const bool issue = elect_one();
-    bool ok = true;
     {
       const uint32_t idesc = idesc_bf16(RP, false, TRANS);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int c = c0; c < c1; ++c) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag))) {
-          ok = false;
-          break;
-        }
+      Turn in = {0, 0};
+      for (int i = 0; i < chunks; ++i) {
+        ok = wait_all(bar_full(in.slot), in.phase, abort_flag);
+        if (!ok) break;
+        if (!in_box) fence_async_smem();  // the copies are generic writes
         tc_fence_after();
-        const uint32_t sx = sbase + stage * P::kStage, sw = sx + kXBytes;
+        const uint32_t sx = sbase + in.slot * slot1, sw = sx + x_tile;
         const uint64_t ad = sdesc_kmajor_sw128(sx);
         const uint64_t bd = TRANS ? sdesc_mn_sw128(sw, 8192) : sdesc_kmajor_sw128(sw);
+        const uint32_t d = tmem + static_cast<uint32_t>(i % G * RP);
         if (issue) {
 #pragma unroll
           for (uint32_t k = 0; k < kBk / 16; ++k)
-            mma_bf16(tmem, ad + kStepK * k, bd + (TRANS ? kStepMn : kStepK) * k, idesc, c != c0 || k != 0);
-          mma_commit(bar_empty(stage));
+            mma_bf16(d, ad + kStepK * k, bd + (TRANS ? kStepMn : kStepK) * k, idesc, i >= G || k != 0);
+          mma_commit(bar_empty(in.slot));
         }
         __syncwarp();
-        if (++stage == S) stage = 0, phase ^= 1u;
+        in.step(1, S1);
       }
       if (issue) mma_commit(bar_sum);
       __syncwarp();
@@ -253,178 +282,301 @@ __global__ void __launch_bounds__(kThreads, RB == 1 ? 2 : 1) lora_kernel(const _
     cluster_sync();
     tc_fence_after();
     fence_async_all();
-    if (out != nullptr) {
-      const uint32_t idesc = idesc_bf16(kBn, false, TRANS);
-      for (int nt = nt0, i = 0; ok && nt < nt1; ++nt, ++i) {
-        const int s = i & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_wfull(s), (i >> 1) & 1, abort_flag) &&
-                                         mbar_wait(bar_free(s), ((i >> 1) & 1) ^ 1u, abort_flag))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sw = sbase + P::kW2 + s * P::kW2Tile;
-        const uint32_t d = tmem + static_cast<uint32_t>(s * kBn);
-        if (issue) {
-          for (int part = 0; part < 2; ++part) {
-            for (int k = 0; k < RP / 16; ++k) {
-              // 16 ranks: 32 bytes within a 64-wide block of the intermediate
-              const uint32_t su = sbase + (part ? P::kULo : P::kU) + (k >> 2) * kXBytes;
-              const uint64_t ad = sdesc_kmajor_sw128(su) + kStepK * (k & 3);
-              const uint64_t bd = TRANS ? sdesc_mn_sw128(sw, P::kW2Tile / 2) + kStepMn * k
-                                        : sdesc_kmajor_sw128(sw + (k >> 2) * 16384) + kStepK * (k & 3);
-              mma_bf16(d, ad, bd, idesc, part != 0 || k != 0);
-            }
+    const uint32_t idesc = idesc_bf16(kBk, false, TRANS);
+    Turn to = {0, 0}, acc = {0, 0};
+    for (int i = 0; ok && i < tiles; ++i) {
+      ok = wait_all(bar_bfull(to.slot), to.phase, abort_flag) &&
+           wait_all(bar_free(acc.slot), acc.phase ^ 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sw = sbase + to.slot * slot2 + x_tile;
+      const uint32_t d = tmem + static_cast<uint32_t>(acc.slot * kBk);
+      if (issue) {
+        for (int p = 0; p < 2; ++p) {
+          for (int k = 0; k < RP / 16; ++k) {
+            const int col = p * RQ + 16 * k;  // of the intermediate's two parts
+            const uint64_t ad = sdesc_kmajor_sw128(su + (col >> 6) * kXBytes) + kStepK * ((col & 63) >> 4);
+            const uint64_t bd = TRANS ? sdesc_mn_sw128(sw, 8192) + kStepMn * k
+                                      : sdesc_kmajor_sw128(sw + (k >> 2) * 8192) + kStepK * (k & 3);
+            mma_bf16(d, ad, bd, idesc, p != 0 || k != 0);
           }
-          mma_commit(bar_wempty(s));
-          mma_commit(bar_acc(s));
         }
-        __syncwarp();
+        mma_commit(bar_acc(acc.slot));
       }
+      __syncwarp();
+      to.step(1, S2);
+      acc.step(1, kBufs);
     }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      if (a.status) atomicOr(a.status, kDevTimeout);
-    }
+    if (!ok && lane == 0) give_up(abort_flag, a.status);
     if (issue) {
       mma_commit(bar_done);
       mbar_wait_drain(bar_done, 0);
     }
     __syncwarp();
   } else {
-    // ------------------------------------------- partial sums, then the epilogue
-    const int quarter = warp & 3;
+    const int ew = warp - 2, quarter = warp & 3, set = ew >> 2;
+    const int sub = static_cast<int>(lane >> 3), ch = static_cast<int>(lane & 7);
+    const float scale = a.scale != nullptr ? a.scale[t.e] : 1.0f;
+    if (!in_box) {
+      // ------------------------------------------- the input's rows: 16 a warp, eight lanes a row
+      // Rows behind the tile's last stay as they are: whatever they hold goes into rows that nobody
+      // stores.
+      const __nv_bfloat16* src[4];
+      uint32_t dst[4];
+      bool there[4];
+      int live = 0;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int r = 16 * ew + 4 * p + sub;
+        int o = -1;
+        if (r < t.nrows)
+          o = row_place(a.in_index, t.row0 + r, a.in_rows, rank == 0 && ch == 0 ? a.status : nullptr), ++live;
+        there[p] = o >= 0;
+        src[p] = static_cast<const __nv_bfloat16*>(a.in) + static_cast<size_t>(max(o, 0)) * a.K + 8 * ch;
+        dst[p] = sbase + swz(r, ch);
+      }
+      Turn in = {0, 0};
+      for (int i = 0; i < chunks; ++i) {
+        ok = wait_all(bar_empty(in.slot), in.phase ^ 1u, abort_flag);
+        if (!ok) break;
+        const int col = (c0 + i) * kBk;
+        const bool inside = col + 8 * ch < a.K;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          if (p < live) copy16(dst[p] + in.slot * slot1, src[p] + (inside ? col : -8 * ch), inside && there[p]);
+        copy_arrive(bar_full(in.slot));
+        in.step(1, S1);
+      }
+    }
+    // Eight ranks of a row into its block of Q (see LoraArgs): two bytes at a time, a warp's rows side
+    // by side.
+    auto q_column = [&](uint8_t* q, int r, int j8, const float (&f)[8]) {
+      uint8_t* block = q + (2 * static_cast<size_t>(static_cast<int>(blockIdx.x) / C) + (r >> 6)) * (256u * RP);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t hi, lo;
+        split2(f[j], f[j + 1], hi, lo);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t at = swz(8 * j8 + j + k, (r & 63) >> 3) + 2u * (r & 7);
+          *reinterpret_cast<uint16_t*>(block + at) = static_cast<uint16_t>(hi >> (16 * k));
+          *reinterpret_cast<uint16_t*>(block + RP * 128 + at) = static_cast<uint16_t>(lo >> (16 * k));
+        }
+      }
+    };
+    // Rows of the tile that Q's blocks need: they are read up to a multiple of 16.
+    const int q_rows = TRANS && a.qv != nullptr ? (t.nrows + 15) & ~15 : t.nrows;
+    if constexpr (TRANS) {
+      // u's block, while the products run
+      if (a.qv != nullptr) {
+        const int per = (q_rows - rank + C - 1) / C;
+        for (int i = tid - 64; i < per * (RP / 8); i += 256) {
+          const int r = rank + C * (i % per), j8 = i / per;
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+          if (r < t.nrows && 8 * j8 < a.R) {
+            const float4* u = reinterpret_cast<const float4*>(a.u_in + static_cast<size_t>(t.row0 + r) * a.R + 8 * j8);
+            const float4 x = u[0], y = u[1];
+            f[0] = scale * x.x, f[1] = scale * x.y, f[2] = scale * x.z, f[3] = scale * x.w;
+            f[4] = scale * y.x, f[5] = scale * y.y, f[6] = scale * y.z, f[7] = scale * y.w;
+          }
+          q_column(a.qu, r, j8, f);
+        }
+        __syncwarp();
+      }
+    }
+    // ------------------------------------------- the partial sums
     const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t part = sbase + P::kPart;
-    bool ok = __all_sync(0xffffffffu, mbar_wait(bar_sum, 0, abort_flag));
+    const int row = quarter * 32 + static_cast<int>(lane);
+    ok = wait_all(bar_sum, 0, abort_flag) && ok;
     tc_fence_after();
-    // Partial sums as [RP / 4][128 rows] of four ranks: a warp's 32 rows lie side by side.
-    if (ok) {
-      const uint32_t row = static_cast<uint32_t>(quarter * 32) + lane;
-      for (int j = 0; j < RP; j += 16) {
-        uint32_t r[16];
-        tmem_ld_x16(tq + j, r);
+    // Eight ranks from 8 j8 on of a row: u, and the two parts into the CTAs' intermediates.
+    auto finish = [&](int r, int j8, float (&v)[8]) {
+      const bool live = r < t.nrows && 8 * j8 < a.R;
+      if (live && a.u != nullptr) {
+        float4* u = reinterpret_cast<float4*>(a.u + static_cast<size_t>(t.row0 + r) * a.R + 8 * j8);
+        u[0] = make_float4(v[0], v[1], v[2], v[3]);
+        u[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = live ? v[j] * scale : 0.0f;
+      if constexpr (TRANS) {
+        if (a.qv != nullptr) q_column(a.qv, r, j8, v);
+      }
+      uint4 hi, lo;
+      split2(v[0], v[1], hi.x, lo.x);
+      split2(v[2], v[3], hi.y, lo.y);
+      split2(v[4], v[5], hi.z, lo.z);
+      split2(v[6], v[7], hi.w, lo.w);
+      const uint32_t hc = 8u * j8, lc = RQ + 8u * j8;
+      const uint32_t to_hi = su + (hc >> 6) * kXBytes + swz(r, (hc & 63) >> 3);
+      const uint32_t to_lo = su + (lc >> 6) * kXBytes + swz(r, (lc & 63) >> 3);
+      if (C == 1) {
+        st_shared_u4(to_hi, hi);
+        st_shared_u4(to_lo, lo);
+      } else {
+        for (int p = 0; p < C; ++p) {
+          st_cluster_u4(map_to_cta(to_hi, p), hi);
+          st_cluster_u4(map_to_cta(to_lo, p), lo);
+        }
+      }
+    };
+    const int chains = min(G, chunks);
+    for (int j = 16 * set; j < RP; j += 32) {
+      float v[2][8];
+      uint32_t r[16];
+      for (int g = 0; g < chains && ok; ++g) {
+        tmem_ld_x16(tq + g * RP + j, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_shared_f4(part + ((j / 4 + q) * kRows + row) * 16u, __uint_as_float(r[4 * q]),
-                       __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
-                       __uint_as_float(r[4 * q + 3]));
+        for (int k = 0; k < 16; ++k)
+          v[k >> 3][k & 7] = g == 0 ? __uint_as_float(r[k]) : v[k >> 3][k & 7] + __uint_as_float(r[k]);
       }
+      if (C == 1) {
+        finish(row, j / 8, v[0]);
+        finish(row, j / 8 + 1, v[1]);
+      } else if (row < rows8) {
+        // [RP / 4][rows] of four ranks: a warp's 32 rows lie side by side
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          st_shared_f4(part + ((j / 4 + q) * rows8 + row) * 16u, v[q >> 1][4 * (q & 1)], v[q >> 1][4 * (q & 1) + 1],
+                       v[q >> 1][4 * (q & 1) + 2], v[q >> 1][4 * (q & 1) + 3]);
+      }
+    }
+    // -------------------------------------- the base's rows where they are copied
+    // A warp copies its own 32 rows of its set's next tiles, `ahead` of them: nobody else reads them.
+    const __nv_bfloat16* src[8];
+    const int ahead = max(1, min((S2 - 1) / 2, early / 2));
+    Turn fetch = {set, 0};
+    int fetched = set;
+    auto fetch_base = [&]() {
+      if (fetched < tiles) {
+        const int col = (nt0 + fetched) * kBk;
+        const bool inside = col + 8 * ch < N;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int r = quarter * 32 + 4 * p + sub;
+          if (r < t.nrows)
+            copy16(sbase + fetch.slot * slot2 + swz(r, ch), src[p] == nullptr ? base : src[p] + (inside ? col : -8 * ch),
+                   inside && src[p] != nullptr);
+        }
+      }
+      copy_commit();
+      fetched += 2;
+      fetch.step(2, S2);
+    };
+    const bool pre = early >= 2 * ahead;
+    if (copy_base) {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int o = s_rows[quarter * 32 + 4 * p + sub];
+        src[p] = o >= 0 ? base + static_cast<size_t>(o) * N + 8 * ch : nullptr;
+      }
+      if (pre)
+        for (int k = 0; k < ahead; ++k) fetch_base();
     }
     tc_fence_before();
     __syncwarp();
     cluster_sync();
-    {
-      // This CTA's rows of the tile: summed over the CTAs in their order, eight ranks at a time.
-      const float scale = a.scale != nullptr ? a.scale[t.e] : 1.0f;
-      const int per = kRows / C, r0 = rank * per;
-      for (int i = tid - 64; i < per * (RP / 8); i += 128) {
-        const int row = r0 + i % per, j8 = i / per;
+    if (C > 1) {
+      // This CTA's rows of the tile, summed over the CTAs in their order.  Rows are dealt out one by
+      // one, so that few rows are many CTAs' work too.
+      const int per = (q_rows - rank + C - 1) / C;
+      for (int i = tid - 64; i < per * (RP / 8); i += 256) {
+        const int r = rank + C * (i % per), j8 = i / per;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (row < t.nrows && 8 * j8 < a.R) {
-          const uint32_t at = part + (2u * j8 * kRows + row) * 16u;
-          for (int p = 0; p < C; ++p) {
-            const uint32_t from = map_to_cta(at, p);
-            const float4 x = ld_cluster_f4(from), y = ld_cluster_f4(from + kRows * 16u);
-            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-          }
-          if (a.u != nullptr) {
-            float4* u = reinterpret_cast<float4*>(a.u + static_cast<size_t>(t.row0 + row) * a.R + 8 * j8);
-            u[0] = make_float4(v[0], v[1], v[2], v[3]);
-            u[1] = make_float4(v[4], v[5], v[6], v[7]);
-          }
+        const uint32_t at = part + (2u * j8 * rows8 + r) * 16u;
+        for (int p = 0; p < C && r < t.nrows; ++p) {
+          const uint32_t from = map_to_cta(at, p);
+          const float4 x = ld_cluster_f4(from), y = ld_cluster_f4(from + rows8 * 16u);
+          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+          v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
         }
-        uint4 hi, lo;
-        split2(v[0] * scale, v[1] * scale, hi.x, lo.x);
-        split2(v[2] * scale, v[3] * scale, hi.y, lo.y);
-        split2(v[4] * scale, v[5] * scale, hi.z, lo.z);
-        split2(v[6] * scale, v[7] * scale, hi.w, lo.w);
-        const uint32_t to = sbase + P::kU + (j8 >> 3) * kXBytes + swz(row, j8 & 7);
-        for (int p = 0; p < C; ++p) {
-          const uint32_t dst = map_to_cta(to, p);
-          st_cluster_u4(dst, hi);
-          st_cluster_u4(dst + RB * kXBytes, lo);
-        }
+        finish(r, j8, v);
       }
     }
     fence_async_all();
     __syncwarp();
     cluster_sync();
-    if (out != nullptr) {
-      // Half a tile (64 columns) at a time: fp32 sums into this warp's staging (32 rows of 16 chunks
-      // of 16 bytes, chunk c of row r at c ^ (r & 7)), and out again as whole row pieces, eight lanes
-      // to a row.
-      const uint32_t stage = sbase + P::kPart + static_cast<uint32_t>(warp - 2) * 8192u;
-      const int sub = static_cast<int>(lane >> 3), ch = static_cast<int>(lane & 7);
-      int place[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) place[p] = s_rows[quarter * 32 + 4 * p + sub];
-      const uint32_t odd = static_cast<uint32_t>(ch >> 2);
-      for (int nt = nt0, i = 0; nt < nt1; ++nt, ++i) {
-        const int s = i & 1;
+    if (copy_base && !pre)
+      for (int k = 0; k < ahead; ++k) fetch_base();
+    // ------------------------------------------------------------ epilogue
+    // A lane has a row: 64 columns of accumulators plus its base, in place in the slot.
+    const bool by_tma = out_box && quarter * 32 + 32 <= t.nrows;
+    const bool mine = row < rows8;
+    Turn to = {set, 0}, acc = {set, 0};
+    for (int i = set; ok && i < tiles; i += 2) {
+      const uint32_t tile = sbase + to.slot * slot2;
+      ok = wait_all(bar_bfull(to.slot), to.phase, abort_flag) && wait_all(bar_acc(acc.slot), acc.phase, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      if (copy_base) {
+        copy_wait_left(ahead - 1);
+        __syncwarp();
+      }
+      if (quarter * 32 < t.nrows) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int col = nt * kBn + 64 * h + 8 * ch;
-          uint4 bv[8];
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tq + acc.slot * kBk + 32 * h, r);
+          uint4 b[4];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            bv[p] = make_uint4(0u, 0u, 0u, 0u);
-            if (base != nullptr && place[p] >= 0 && col < N)
-              bv[p] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(place[p]) * N + col);
+          for (int c = 0; c < 4; ++c) {
+            b[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (base != nullptr && mine) b[c] = ld_shared_u4(tile + swz(row, 4 * h + c));
           }
-          if (h == 0) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_acc(s), (i >> 1) & 1, abort_flag));
-            tc_fence_after();
-          }
-          if (!ok) break;
+          tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tq + s * kBn + 64 * h + 32 * q, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              st_shared_f4(stage + lane * 256u + (((8u * q + c) ^ (lane & 7u)) << 4), __uint_as_float(r[4 * c]),
-                           __uint_as_float(r[4 * c + 1]), __uint_as_float(r[4 * c + 2]),
-                           __uint_as_float(r[4 * c + 3]));
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t* x = r + 8 * c;
+            auto add2 = [](uint32_t u, uint32_t p, uint32_t q) {
+              const float2 f = unpack_bf16(u);
+              return pack_bf16(f.x + __uint_as_float(p), f.y + __uint_as_float(q));
+            };
+            b[c].x = add2(b[c].x, x[0], x[1]);
+            b[c].y = add2(b[c].y, x[2], x[3]);
+            b[c].z = add2(b[c].z, x[4], x[5]);
+            b[c].w = add2(b[c].w, x[6], x[7]);
+            if (mine) st_shared_u4(tile + swz(row, 4 * h + c), b[c]);
           }
-          if (h == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_free(s));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint32_t r = 4u * p + sub, at = stage + r * 256u;
-            // lanes 4 .. 7 of a row read their second chunk first: eight different bank groups
-            float4 f[2];
-            f[0] = ld_shared_f4(at + (((2u * ch + odd) ^ (r & 7u)) << 4));
-            f[1] = ld_shared_f4(at + (((2u * ch + 1u - odd) ^ (r & 7u)) << 4));
-            const float4 x = odd ? f[1] : f[0], y = odd ? f[0] : f[1];
-            const float2 b0 = unpack_bf16(bv[p].x), b1 = unpack_bf16(bv[p].y), b2 = unpack_bf16(bv[p].z),
-                         b3 = unpack_bf16(bv[p].w);
-            uint4 v;
-            v.x = pack_bf16(b0.x + x.x, b0.y + x.y);
-            v.y = pack_bf16(b1.x + x.z, b1.y + x.w);
-            v.z = pack_bf16(b2.x + y.x, b2.y + y.y);
-            v.w = pack_bf16(b3.x + y.z, b3.y + y.w);
-            if (place[p] >= 0 && col < N)
-              *reinterpret_cast<uint4*>(out + static_cast<size_t>(place[p]) * N + col) = v;
-          }
-          __syncwarp();
         }
-        if (!ok) break;
       }
+      tc_fence_before();
+      if (by_tma) fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free(acc.slot));
+      if (by_tma) {
+        if (lane == 0) {
+          tma_store_2d(&a.tm_out, (nt0 + i) * kBk, t.row0 + quarter * 32, tile + quarter * 4096u);
+          bulk_commit();
+          bulk_wait_read0();  // it has left the slot; the other set works meanwhile
+          mbar_arrive(bar_bempty(to.slot));
+        }
+      } else {
+        const int col = (nt0 + i) * kBk + 8 * ch;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int q = quarter * 32 + 4 * p + sub;
+          const int o = q < t.nrows && col < N ? s_rows[q] : -1;
+          if (o >= 0)
+            *reinterpret_cast<uint4*>(out + static_cast<size_t>(o) * N + col) = ld_shared_u4(tile + swz(q, ch));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_bempty(to.slot));
+      }
+      if (copy_base) {
+        // its slot has been read by the tile before in it, which may be the other set's
+        if (fetched < tiles && fetched >= S2) ok = wait_all(bar_bempty(fetch.slot), fetch.phase ^ 1u, abort_flag);
+        fetch_base();
+      }
+      to.step(2, S2);
+      acc.step(2, kBufs);
     }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      if (a.status) atomicOr(a.status, kDevTimeout);
-    }
+    copy_wait<0>();
+    if (!ok && lane == 0) give_up(abort_flag, a.status);
   }
   tc_fence_before();
   __syncthreads();
@@ -432,18 +584,17 @@ __global__ void __launch_bounds__(kThreads, RB == 1 ? 2 : 1) lora_kernel(const _
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool TRANS, int RB>
+template <bool TRANS, int RQ>
 cudaError_t set_smem() {
   static thread_local uint64_t attr_ctx = 0;
-  return set_smem_attr_once(reinterpret_cast<const void*>(lora_kernel<TRANS, RB>), Plan<RB>::kSmem, &attr_ctx);
+  return set_smem_attr_once(reinterpret_cast<const void*>(lora_kernel<TRANS, RQ>), 227 * 1024, &attr_ctx);
 }
 
-template <bool TRANS, int RB>
-cudaLaunchConfig_t config(int cluster, long long tiles, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t config(int cluster, long long tiles, size_t smem, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Plan<RB>::kSmem;
+  cfg.dynamicSmemBytes = smem;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = static_cast<unsigned>(cluster);
   attr->val.clusterDim.y = 1;
@@ -453,59 +604,69 @@ cudaLaunchConfig_t config(int cluster, long long tiles, cudaLaunchAttribute* att
   return cfg;
 }
 
-// The largest cluster, up to eight CTAs, that the current context can run (a share of the SMs may be
-// too small for it).  Asked once per context and thread.
-template <bool TRANS, int RB>
-int largest_cluster() {
+constexpr int kMaxCluster = 8;
+// A kernel that needs as much of an SM as lora_kernel does, but for tensor memory: for kernels that
+// allocate that, the occupancy calculation answers one CTA an SM, though two (256 columns each) run.
+__global__ void __launch_bounds__(kBound, 2) lora_room_kernel() {}
+
+// Clusters of c CTAs, with the short or the long ring, that the current context runs at once (none
+// where it has a share of the SMs that is too small).  Asked once per context and thread.
+template <int RQ>
+long long clusters_at_once(int c, bool longer) {
+  using P = Plan<RQ>;
   static thread_local uint64_t asked_ctx = 0;
-  static thread_local int largest = 1;
-  if (asked_ctx != 0 && asked_ctx == current_context_id()) return largest;
-  largest = 1;
-  for (int c = 8; c > 1; c /= 2) {
-    cudaLaunchAttribute attr = {};
-    const cudaLaunchConfig_t cfg = config<TRANS, RB>(c, 1, &attr);
-    int active = 0;
-    if (cudaOccupancyMaxActiveClusters(&active, lora_kernel<TRANS, RB>, &cfg) != cudaSuccess) {
-      (void)cudaGetLastError();  // a size that does not fit is no error of the call
-      active = 0;
-    }
-    if (active > 0) {
-      largest = c;
-      break;
-    }
+  static thread_local int active[2][kMaxCluster + 1];
+  if (asked_ctx == 0 || asked_ctx != current_context_id()) {
+    static thread_local uint64_t attr_ctx = 0;
+    if (set_smem_attr_once(reinterpret_cast<const void*>(lora_room_kernel), 227 * 1024, &attr_ctx) != cudaSuccess)
+      return 0;
+    for (int l = 0; l < 2; ++l)
+      for (int k = 2; k <= kMaxCluster; ++k) {
+        cudaLaunchAttribute attr = {};
+        const cudaLaunchConfig_t cfg = config(k, 1, P::smem(l ? P::kLong : P::kShort), &attr);
+        if (cudaOccupancyMaxActiveClusters(&active[l][k], lora_room_kernel, &cfg) != cudaSuccess) {
+          (void)cudaGetLastError();  // a size that does not fit is no error of the call
+          active[l][k] = 0;
+        }
+      }
+    asked_ctx = current_context_id();
   }
-  asked_ctx = current_context_id();
-  return largest;
+  return active[longer][c];
 }
 
-template <bool TRANS, int RB>
+template <bool TRANS, int RQ>
 cudaError_t launch(LoraArgs a, int num_sms, cudaStream_t stream) {
-  cudaError_t err = set_smem<TRANS, RB>();
+  using P = Plan<RQ>;
+  cudaError_t err = set_smem<TRANS, RQ>();
   if (err != cudaSuccess) return err;
-  // The exact number of tiles is known on the device only: at most this many, the tiles of rows
-  // without an adapter included.
-  const long long some = a.M < a.E ? a.M : a.E;
-  const long long tiles = a.M / kRows + some + 1;
-  // As many CTAs to a tile as the SMs have room for; each needs some columns of its own.
-  const long long expected = (a.M + kRows - 1) / kRows + some / 2;
+  // The exact number of tiles is known on the device only: at most this many, and one more of rows
+  // without an adapter.
+  const long long tiles = (a.M + kRows - 1) / kRows + (a.M < a.E ? a.M : a.E);
+  // As many CTAs to a tile, each with some columns of its own, as run at once: a cluster that waits
+  // for another one's end costs as much again.
   const int nch = (a.K + kBk - 1) / kBk;
-  int most = largest_cluster<TRANS, RB>();
-  if (a.max_cluster > 0 && a.max_cluster < most) most = a.max_cluster;
+  const int most = a.max_cluster > 0 && a.max_cluster < kMaxCluster ? a.max_cluster : kMaxCluster;
   int c = 1;
-  while (2 * c <= most && 2 * c <= nch && expected * 2 * c <= num_sms * (RB == 1 ? 2 : 1)) c *= 2;
+  for (int k = 2; k <= most && k <= nch; ++k)
+    if (tiles <= clusters_at_once<RQ>(k, false)) c = k;
   a.cluster = c;
+  a.ring = (c == 1 ? tiles <= num_sms : tiles <= clusters_at_once<RQ>(c, true)) ? P::kLong : P::kShort;
   cudaLaunchAttribute attr = {};
-  cudaLaunchConfig_t cfg = config<TRANS, RB>(c, tiles, &attr);
+  cudaLaunchConfig_t cfg = config(c, tiles + 1, P::smem(a.ring), &attr);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<TRANS, RB>, a);
+  return cudaLaunchKernelEx(&cfg, lora_kernel<TRANS, RQ>, a);
+}
+
+template <bool TRANS>
+cudaError_t launch_rank(const LoraArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.R > 64) return launch<TRANS, 128>(a, num_sms, stream);
+  return a.R > 32 ? launch<TRANS, 64>(a, num_sms, stream) : launch<TRANS, 32>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_lora(const LoraArgs& a, bool transposed, int num_sms, cudaStream_t stream) {
-  if (a.R > 64)
-    return transposed ? launch<true, 2>(a, num_sms, stream) : launch<false, 2>(a, num_sms, stream);
-  return transposed ? launch<true, 1>(a, num_sms, stream) : launch<false, 1>(a, num_sms, stream);
+  return transposed ? launch_rank<true>(a, num_sms, stream) : launch_rank<false>(a, num_sms, stream);
 }
 
 }  // namespace mgw

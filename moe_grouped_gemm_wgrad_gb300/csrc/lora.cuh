@@ -1,5 +1,5 @@
 // Device helpers of the low-rank adapter kernels (lora.cu, lora_grad.cu): bf16 tcgen05 products,
-// operand tiles in either major order, row gathers by TMA, and where a row tile lies.
+// operand tiles in either major order, gathered rows, and where a row tile lies.
 //
 // Every operand tile is a stack of 64-element, 128-byte rows in the 128-byte swizzle (8-row atoms
 // of 1024 bytes), as a TMA box 64 elements wide writes them.  The tensor core reads such a tile
@@ -26,14 +26,44 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
-// Four rows of a map with a one-row box; a row of -1 arrives as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, int c0, const int (&r)[4],
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-      : "memory");
+// 16 bytes global -> shared, asynchronously; zeros where `there` is false (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16u : 0u)
+               : "memory");
+}
+// The calling thread's arrival on `bar`, by itself, once all its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// All of this thread's groups but the last `left` have landed.
+__device__ __forceinline__ void copy_wait_left(int left) {
+  switch (left) {
+    case 0: copy_wait<0>(); break;
+    case 1: copy_wait<1>(); break;
+    case 2: copy_wait<2>(); break;
+    case 3: copy_wait<3>(); break;
+    case 4: copy_wait<4>(); break;
+    case 5: copy_wait<5>(); break;
+    case 6: copy_wait<6>(); break;
+    case 7: copy_wait<7>(); break;
+    case 8: copy_wait<8>(); break;
+    case 9: copy_wait<9>(); break;
+    default: copy_wait<10>(); break;
+  }
+}
+// Waits, all lanes of a warp together, and says to all whether the phase came.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void give_up(volatile int* abort, int* status) {
+  *abort = 1;
+  if (status != nullptr) atomicOr(status, kDevTimeout);
 }
 // Orders generic-proxy accesses of any memory before later async-proxy ones (TMA, tcgen05).
 __device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -92,6 +122,14 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ float ld_shared_f1(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -108,9 +146,9 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   int never = 0;
-  (void)mbar_wait(bar, parity, &never);
+  return mbar_wait(bar, parity, &never);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

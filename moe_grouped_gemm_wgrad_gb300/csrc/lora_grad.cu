@@ -2,17 +2,23 @@
 //
 //   dA[e][j][k] = scale[e] sum_r v[r][j] x[t(r)][k]      dB[e][n][j] = scale[e] sum_r dy[o(r)][n] u[r][j]
 //
-// Both are grad = X^T Q, X bf16 rows contracted over the rows (as the weight gradient of an expert),
-// Q fp32 [M, R] rank-wide.  X's rows arrive as they lie in memory, 64 tokens by 64 features, and
-// the tensor core reads them across (MN-major, see lora.cuh): nothing is transposed.  Q is split into
-// two bf16 parts (split2) on the way, both in one product of twice the rank's width.
+// Both are grad = X^T Q, X bf16 rows contracted over the rows (as an expert's weight gradient is), Q
+// rank-wide.  X's rows arrive as they lie in memory, 64 tokens by 64 features, and the tensor core
+// reads them across (MN-major, see lora.cuh): nothing is transposed.  Q comes from the data gradient's
+// launch in blocks of 64 tokens, already scaled, split into two bf16 parts (split2) and laid out as
+// the operand tile that the tensor core reads: one bulk copy each.  Both parts go through one product of
+// twice the rank's width and are added up in the epilogue.
 //
-// A work item is (adapter, 128 or 256 features); a cluster of up to eight CTAs shares its rows and
-// adds up its fp32 sums, in the CTAs' order, through distributed shared memory: no atomics and no
-// workspace, the same bits on every run.
+// A cluster has 256 features of one of the two gradients and all token blocks, of all adapters one
+// after the other, in equal shares: however unevenly the rows fall on the adapters, the CTAs have
+// the same work.  An adapter whose blocks lie in one share is stored from TMEM; one that shares divide
+// is written as fp32 partial sums to the workspace, and behind a cluster barrier its CTAs add them up
+// in the order of the shares, a part of the features each.  No atomics, no second launch, the same
+// bits on every run.
 //
-// Roles (192 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-5 split Q (a thread a
-// rank and eight tokens: reads along the ranks, writes 16 bytes of one rank's tokens), then store.
+// Roles (320 threads): warp 0 loads by TMA, warps 6-9 copy rows that lie apart and an adapter's last
+// rows, warp 1 issues the MMAs, warps 2-5 are the epilogue, which overlaps the next adapter's blocks
+// where two accumulators fit into TMEM (rank up to 64).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -24,41 +30,31 @@ namespace {
 
 using namespace lora;
 
-constexpr int kThreads = 192;
-constexpr int kTok = 64;  // tokens per stage
+constexpr int kThreads = 320;
+constexpr int kTok = 64;           // tokens per stage
+constexpr int kWidth = 256;        // features per CTA
+constexpr int kXBytes = 4 * 8192;  // 64 tokens of 256 features
 constexpr int kMaxStages = 6;
-constexpr int kMiscBytes = 8 * (3 * kMaxStages + 2) + 16 + 1024;
+constexpr int kMaxCluster = 8;
+constexpr int kSms = 152;          // of a GB300: the workspace's size has no device to ask
+constexpr int kBarBytes = 8 * (2 * kMaxStages + 4);
 
-struct Shape {
-  int fb, stages, stage_bytes;
-  uint32_t tmem_cols;
-  size_t smem;
-};
 __host__ __device__ constexpr int padded_rank(int R) { return (R + 15) & ~15; }
-__host__ __device__ constexpr int feature_blocks(int R) { return padded_rank(R) <= 32 ? 1 : 2; }
-__host__ __device__ constexpr Shape shape_of(int R) {
-  const int rp = padded_rank(R);
-  Shape s = {};
-  s.fb = feature_blocks(R);
-  s.stage_bytes = s.fb * 16384 + 2 * rp * 256;  // X, Q in fp32, its two parts
-  // two CTAs an SM up to rank 32, one beyond (deep enough rings do not fit twice)
-  const int room = (s.fb == 1 ? 113 : 226) * 1024 - kMiscBytes;
-  s.stages = room / s.stage_bytes < kMaxStages ? room / s.stage_bytes : kMaxStages;
-  s.tmem_cols = 32;
-  while (s.tmem_cols < static_cast<uint32_t>(s.fb * 2 * rp)) s.tmem_cols *= 2;
-  s.smem = static_cast<size_t>(s.stages) * s.stage_bytes + kMiscBytes;
-  return s;
+__host__ __device__ constexpr int stage_bytes(int RP) { return kXBytes + 256 * RP; }
+constexpr size_t misc_bytes(int E) { return kBarBytes + 16 + sizeof(int) * (static_cast<size_t>(E) + 1) + 1024; }
+constexpr int stages_of(int RP) {
+  const int n = static_cast<int>((227 * 1024 - misc_bytes(kMaxExperts)) / stage_bytes(RP));
+  return n < kMaxStages ? n : kMaxStages;
 }
-static_assert(shape_of(16).stages >= 3 && shape_of(32).stages >= 3 && shape_of(64).stages >= 3 &&
-                  shape_of(128).stages >= 2 && shape_of(128).tmem_cols <= 512,
-              "ring");
-// the CTA's fp32 sums lie in the ring at the end
-static_assert(128 * 2 * 128 * 4 <= shape_of(128).stages * shape_of(128).stage_bytes &&
-                  128 * 2 * 48 * 4 <= shape_of(48).stages * shape_of(48).stage_bytes,
-              "sums");
+static_assert(stages_of(128) == 3 && stages_of(64) == 4 && stages_of(16) == 6, "ring");
+constexpr size_t part_floats(int RP) { return static_cast<size_t>(kWidth) * RP; }
 
-template <int FB>
-__global__ void __launch_bounds__(kThreads, FB == 1 ? 2 : 1) lora_grad_kernel(const __grid_constant__ LoraGradArgs a) {
+// The share of the token blocks of CTA p of C.
+__device__ __forceinline__ int share(int blocks, int p, int C) {
+  return static_cast<int>(static_cast<long long>(blocks) * p / C);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_constant__ LoraGradArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -66,73 +62,58 @@ __global__ void __launch_bounds__(kThreads, FB == 1 ? 2 : 1) lora_grad_kernel(co
   const uint32_t lane = lane_id();
   const int C = a.cluster;
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int R = a.R, RP = padded_rank(R);
-  const int S = a.stages, stage_bytes = FB * 16384 + 2 * RP * 256;
-  const uint32_t raw_at = FB * 16384, part_at = raw_at + RP * 256;
-  uint8_t* misc = smem + S * stage_bytes;
-  int* s_misc = reinterpret_cast<int*>(misc + 8 * (3 * kMaxStages + 2));  // [0] TMEM [1] abort
+  const int E = a.E, R = a.R, RP = padded_rank(R);
+  const int S = a.stages;
+  uint8_t* bars = smem + S * stage_bytes(RP);
+  int* s_misc = reinterpret_cast<int*>(bars + kBarBytes);  // [0] TMEM [1] abort [2] token blocks
+  int* s_off = s_misc + 4;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(s_misc + 1);
+  int item = static_cast<int>(blockIdx.x) / C;
+  const int which = item >= a.first1 ? 1 : 0;
+  if (which) item -= a.first1;
+  const LoraGradJob& job = a.job[which];
+  const int cols = job.cols, f0 = item * kWidth;
 
-  int bad = 0;
-  for (int i = tid; i < a.E; i += kThreads) bad |= a.off[i + 1] < a.off[i];
-  if (tid == 0) bad |= a.off[0] != 0 || a.off[a.E] > a.M;
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto bar_acc = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
+  auto bar_free = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 2 + s); };
+  if (tid == 0) {
+    tma_prefetch_desc(&job.tm);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar_full(s), 1 + 128);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_acc(s), 1);
+      mbar_init(bar_free(s), 4);
+    }
+    fence_mbar_init();
+    s_misc[1] = 0;
+    s_misc[2] = 0;
+  }
+  for (int i = tid; i <= E; i += kThreads) s_off[i] = a.off[i];
+  __syncthreads();
+  int bad = 0, mine = 0;
+  for (int i = tid; i < E; i += kThreads) {
+    const int n = s_off[i + 1] - s_off[i];
+    bad |= n < 0;
+    mine += (n + kTok - 1) / kTok;
+  }
+  if (tid == 0) bad |= s_off[0] != 0 || s_off[E] > a.M;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) atomicAdd(&s_misc[2], mine);
   if (__syncthreads_or(bad)) {
     if (tid == 0 && a.status != nullptr) atomicOr(a.status, kDevBadOffsets);
     return;
   }
-  int item = static_cast<int>(blockIdx.x) / C;
-  const int which = item >= a.first[1] ? 1 : 0;
-  item -= a.first[which];
-  const LoraGradJob& job = a.job[which];
-  const int width = FB * 128;
-  const int blocks = (job.cols + width - 1) / width;
-  const int e = item / blocks, f0 = item % blocks * width;
-  const int lo = a.off[e], n = a.off[e + 1] - lo;
-  const int cols = job.cols;
-  __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(job.grad);
-
-  // Stores four neighbouring ranks of feature f0 + f.
-  auto store4 = [&](int f, int j, float4 v) {
-    const int c = f0 + f;
-    if (c >= cols || j >= R) return;
-    const uint32_t p0 = pack_bf16(v.x, v.y), p1 = pack_bf16(v.z, v.w);
-    if (job.by_rank) {
-      __nv_bfloat16* g = grad + (static_cast<size_t>(e) * R + j) * cols + c;
-      g[0] = __ushort_as_bfloat16(static_cast<unsigned short>(p0));
-      g[cols] = __ushort_as_bfloat16(static_cast<unsigned short>(p0 >> 16));
-      g[2 * static_cast<size_t>(cols)] = __ushort_as_bfloat16(static_cast<unsigned short>(p1));
-      g[3 * static_cast<size_t>(cols)] = __ushort_as_bfloat16(static_cast<unsigned short>(p1 >> 16));
-    } else {
-      *reinterpret_cast<uint2*>(grad + (static_cast<size_t>(e) * cols + c) * R + j) = make_uint2(p0, p1);
-    }
-  };
-  const int per = width / C;  // features that this CTA stores
-  if (n == 0) {
-    for (int i = tid; i < per * (RP / 4); i += kThreads)
-      store4(rank * per + i % per, i / per * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-    return;
-  }
-  const int tiles = (n + kTok - 1) / kTok;
-  const int t0 = static_cast<int>(static_cast<long long>(tiles) * rank / C);
-  const int t1 = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / C);
-
-  const uint32_t bar0 = smem_u32(misc);
-  auto bar_full = [&](int s) { return bar0 + 8u * s; };
-  auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-  auto bar_part = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
-  const uint32_t bar_acc = bar0 + 8u * (3 * kMaxStages);
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
-      mbar_init(bar_part(s), 4);
-    }
-    mbar_init(bar_acc, 1);
-    fence_mbar_init();
-    s_misc[1] = 0;
-  }
+  const int blocks = s_misc[2];
+  const int t0 = share(blocks, rank, C), t1 = share(blocks, rank + 1, C);
+  const uint32_t tmem_cols = RP <= 16 ? 128u : (RP <= 32 ? 256u : 512u);
+  const int bufs = RP <= 64 ? 2 : 1;
   if (warp == 1) {
-    tmem_alloc(smem_u32(s_misc), a.tmem_cols);
+    tmem_alloc(smem_u32(s_misc), tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -140,65 +121,60 @@ __global__ void __launch_bounds__(kThreads, FB == 1 ? 2 : 1) lora_grad_kernel(co
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(s_misc[0]);
 
+  // Walks the adapters' token blocks in this CTA's share, one adapter at a time.
+  struct Walk {
+    const int* off;
+    int e, at, pad;  // adapter, its first block (counted over all), its first row tile of 128
+    int lo, n;       // its rows
+    int b0, b1;      // its blocks within the share, counted within the adapter
+    __device__ __forceinline__ bool next(int t0, int t1, int E) {
+      if (t0 >= t1) return false;
+      while (++e < E) {
+        at += (n + kTok - 1) / kTok;
+        pad += (n + 127) / 128;
+        lo = off[e];
+        n = off[e + 1] - lo;
+        const int end = at + (n + kTok - 1) / kTok;
+        if (at >= t1) return false;
+        if (n > 0 && end > t0) {
+          b0 = max(t0 - at, 0);
+          b1 = min(t1, end) - at;
+          return true;
+        }
+      }
+      return false;
+    }
+  };
+  Walk w = {s_off, -1, 0, 0, 0, 0, 0, 0};
+  // Rows behind an adapter's last one must be zeros (their products with Q's zeros would not be 0
+  // for infinities): only whole blocks come as one box.
+  auto in_box = [&](int left) { return job.index == nullptr && left >= kTok; };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const int l = static_cast<int>(lane & 15u);
     bool ok = true;
     int stage = 0, filled = 0;
     uint32_t phase = 0;
-    int idx[4];
-    auto load_idx = [&](int t) {
-      if (job.index == nullptr) return;
+    while (ok && w.next(t0, t1, E)) {
+      for (int b = w.b0; b < w.b1; ++b) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const bool box = in_box(w.n - b * kTok);
+          const uint32_t fb = bar_full(stage), sx = sbase + stage * stage_bytes(RP), q_bytes = 256u * RP;
+          mbar_arrive_expect_tx(fb, (box ? static_cast<uint32_t>(kXBytes) : 0u) + q_bytes);
+          bulk_load(sx + kXBytes, job.q + (2ll * w.pad + b) * q_bytes, q_bytes, fb);
+          if (box) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = t * kTok + 4 * l + j;
-        idx[j] = t < t1 && i < n ? job.index[lo + i] : -1;
-      }
-    };
-    load_idx(t0);
-    for (int t = t0; t < t1; ++t) {
-      const int valid = min(kTok, n - t * kTok);
-      const int groups = ((valid + 15) & ~15) >> 2;  // the tokens that the MMAs read
-      const bool whole = job.index == nullptr && valid == kTok;
-      int r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 4 * l + j;
-        r[j] = -1;
-        if (i < valid) {
-          r[j] = job.index == nullptr ? lo + t * kTok + i : idx[j];
-          if (r[j] < 0 || r[j] >= job.rows) {
-            if (a.status != nullptr) atomicOr(a.status, kDevBadIndex);
-            r[j] = -1;
+            for (int k = 0; k < 4; ++k) tma_load_2d(sx + k * 8192, &job.tm, f0 + 64 * k, w.lo + b * kTok, fb);
           }
         }
+        __syncwarp();
+        ++filled;
+        if (++stage == S) stage = 0, phase ^= 1u;
       }
-      load_idx(t + 1);
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag))) {
-        ok = false;
-        break;
-      }
-      const uint32_t fb = bar_full(stage), sx = sbase + stage * stage_bytes;
-      if (lane == 0) {
-        const uint32_t q_bytes = static_cast<uint32_t>(valid * R) * 4u;
-        mbar_arrive_expect_tx(fb, (whole ? FB * 16384u : static_cast<uint32_t>(groups) * 512u * 2 * FB) + q_bytes);
-        bulk_load(sx + raw_at, job.q + static_cast<size_t>(lo + t * kTok) * R, q_bytes, fb);
-        if (whole) {
-#pragma unroll
-          for (int b = 0; b < 2 * FB; ++b)
-            tma_load_2d(sx + b * 8192, &job.tm, f0 + 64 * b, lo + t * kTok, fb);
-        }
-      }
-      __syncwarp();
-      if (!whole && l < groups) {
-#pragma unroll
-        for (int b = 0; b < FB; ++b) {
-          const int at = 2 * b + static_cast<int>(lane >> 4);
-          tma_gather4(sx + at * 8192 + l * 512, &job.tmg, f0 + 64 * at, r, fb);
-        }
-      }
-      ++filled;
-      if (++stage == S) stage = 0, phase ^= 1u;
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -212,134 +188,194 @@ __global__ void __launch_bounds__(kThreads, FB == 1 ? 2 : 1) lora_grad_kernel(co
     const bool issue = elect_one();
     const uint32_t idesc = idesc_bf16(2 * RP, true, false);
     bool ok = true;
-    int stage = 0;
+    int stage = 0, i = 0;
     uint32_t phase = 0;
-    for (int t = t0; t < t1; ++t) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag) &&
-                                       mbar_wait(bar_part(stage), phase, abort_flag))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t sx = sbase + stage * stage_bytes;
-      const int steps = (min(kTok, n - t * kTok) + 15) >> 4;
-      if (issue) {
-        const uint64_t bd = sdesc_kmajor_sw128(sx + part_at);
+    for (; ok && w.next(t0, t1, E); ++i) {
+      const int buf = bufs == 2 ? i & 1 : 0, use = bufs == 2 ? i >> 1 : i;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_free(buf), (use & 1) ^ 1u, abort_flag));
+      const uint32_t d = tmem + static_cast<uint32_t>(buf * 4 * RP);
+      for (int b = w.b0; ok && b < w.b1; ++b) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag));
+        if (!ok) break;
+        fence_async_smem();  // copied rows are generic writes
+        tc_fence_after();
+        const uint32_t sx = sbase + stage * stage_bytes(RP);
+        const int steps = (min(kTok, w.n - b * kTok) + 15) >> 4;
+        if (issue) {
+          const uint64_t bd = sdesc_kmajor_sw128(sx + kXBytes);
 #pragma unroll
-        for (int b = 0; b < FB; ++b) {
-          const uint64_t ad = sdesc_mn_sw128(sx + b * 16384, 8192);
-          for (int k = 0; k < steps; ++k)
-            mma_bf16(tmem + b * 2 * RP, ad + kStepMn * k, bd + kStepK * k, idesc, t != t0 || k != 0);
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t ad = sdesc_mn_sw128(sx + h * 16384, 8192);
+            for (int k = 0; k < steps; ++k)
+              mma_bf16(d + h * 2 * RP, ad + kStepMn * k, bd + kStepK * k, idesc, b != w.b0 || k != 0);
+          }
+          mma_commit(bar_empty(stage));
         }
-        mma_commit(bar_empty(stage));
+        __syncwarp();
+        if (++stage == S) stage = 0, phase ^= 1u;
       }
+      if (ok && issue) mma_commit(bar_acc(buf));
       __syncwarp();
-      if (++stage == S) stage = 0, phase ^= 1u;
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
       if (a.status) atomicOr(a.status, kDevTimeout);
     }
-    if (issue) {
-      mma_commit(bar_acc);
-      mbar_wait_drain(bar_acc, 0);
+    // All MMAs have completed before TMEM is released: the epilogue waits for every accumulator but
+    // one that a time-out cut short.
+    if (!ok && issue) {
+      mma_commit(bar_acc(0));
+      mma_commit(bar_acc(1));
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------- Q's two parts, then the sums
-    const float scale = a.scale != nullptr ? a.scale[e] : 1.0f;
-    const int ct = tid - 64;  // 0 .. 127
+  } else if (warp >= 6) {
+    // ------------------------------------------------- rows that lie apart
+    // A warp has 16 of a block's tokens, all lanes one row at a time (512 bytes).  Blocks that come
+    // as a box it only passes on, in step.
+    const int q0 = (warp - 6) * 16, ch = static_cast<int>(lane & 7);
+    const uint32_t part = (lane >> 3) * 8192u;
+    const int col = f0 + 8 * static_cast<int>(lane);
+    const bool there = col < cols;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(job.x) + (there ? col : 0);
     bool ok = true;
-    int stage = 0;
-    uint32_t phase = 0;
-    for (int t = t0; t < t1; ++t) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag))) {
-        ok = false;
-        break;
-      }
-      const int valid = min(kTok, n - t * kTok);
-      const uint32_t sx = sbase + stage * stage_bytes;
-      for (int i = ct; i < RP * 8; i += 128) {
-        const int j = i % RP, o = i / RP;  // rank, eight tokens
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int tok = 8 * o + k;
-          v[k] = j < R && tok < valid ? scale * ld_shared_f1(sx + raw_at + static_cast<uint32_t>(tok * R + j) * 4u) : 0.0f;
+    int i = 0;
+    while (ok && w.next(t0, t1, E)) {
+      // the place of this lane's token of the next block, loaded a block ahead
+      auto place_of = [&](int b) {
+        const int r = b * kTok + q0 + static_cast<int>(lane & 15u);
+        return r < w.n ? row_place(job.index, w.lo + r, job.rows, lane < 16 && f0 == 0 ? a.status : nullptr) : -1;
+      };
+      int ahead = in_box(w.n - w.b0 * kTok) ? -1 : place_of(w.b0);
+      for (int b = w.b0; b < w.b1; ++b, ++i) {
+        const int left = w.n - b * kTok, place = ahead;
+        if (b + 1 < w.b1 && !in_box(left - kTok)) ahead = place_of(b + 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_empty(i % S), ((i / S) & 1) ^ 1u, abort_flag));
+        if (!ok) break;
+        if (!in_box(left)) {
+          const uint32_t sx = sbase + (i % S) * stage_bytes(RP) + part;
+          const int rows = min(16, ((min(left, kTok) + 15) & ~15) - q0);  // those that the MMAs read
+          for (int p = 0; p < rows; ++p) {
+            const int o = __shfl_sync(0xffffffffu, place, p);
+            copy16(sx + swz(q0 + p, ch), x + static_cast<size_t>(max(o, 0)) * cols, there && o >= 0);
+          }
         }
-        uint4 hi, lo4;
-        split2(v[0], v[1], hi.x, lo4.x);
-        split2(v[2], v[3], hi.y, lo4.y);
-        split2(v[4], v[5], hi.z, lo4.z);
-        split2(v[6], v[7], hi.w, lo4.w);
-        const uint32_t at = sx + part_at + swz(j, o);
-        st_shared_u4(at, hi);
-        st_shared_u4(at + RP * 128, lo4);
+        copy_arrive(bar_full(i % S));
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_part(stage));
-      if (++stage == S) stage = 0, phase ^= 1u;
     }
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_acc, 0, abort_flag));
+    copy_wait<0>();
     if (!ok && lane == 0) {
       *abort_flag = 1;
       if (a.status) atomicOr(a.status, kDevTimeout);
     }
-    tc_fence_after();
-    // this CTA's sums as [RP / 4][width] of four ranks
+  }
+
+  __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(job.grad);
+  // Stores four neighbouring ranks of feature f0 + f of adapter e.
+  auto store4 = [&](int e, int f, int j, float4 v) {
+    const int c = f0 + f;
+    if (c >= cols || j >= R) return;
+    const uint32_t p0 = pack_bf16(v.x, v.y), p1 = pack_bf16(v.z, v.w);
+    if (job.by_rank) {
+      __nv_bfloat16* g = grad + (static_cast<size_t>(e) * R + j) * cols + c;
+      g[0] = __ushort_as_bfloat16(static_cast<unsigned short>(p0));
+      g[cols] = __ushort_as_bfloat16(static_cast<unsigned short>(p0 >> 16));
+      g[2 * static_cast<size_t>(cols)] = __ushort_as_bfloat16(static_cast<unsigned short>(p1));
+      g[3 * static_cast<size_t>(cols)] = __ushort_as_bfloat16(static_cast<unsigned short>(p1 >> 16));
+    } else {
+      *reinterpret_cast<uint2*>(grad + (static_cast<size_t>(e) * cols + c) * R + j) = make_uint2(p0, p1);
+    }
+  };
+  // Partial sums of a CTA: those of the adapter that reaches in from the share before (0) and of the
+  // one that reaches out into the next (1), [RP / 4][256 features] of four ranks.
+  auto partial = [&](int p, int slot) {
+    return reinterpret_cast<float4*>(a.partial) +
+           ((static_cast<size_t>(blockIdx.x) / C * C + p) * 2 + slot) * (part_floats(RP) / 4);
+  };
+  if (warp >= 2 && warp < 6) {
+    // ------------------------------------------------------------ epilogue
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
-    for (int b = 0; b < FB; ++b) {
-      const uint32_t f = b * 128u + quarter * 32u + lane;
-      for (int j = 0; j < RP; j += 16) {
-        uint32_t h[16], l[16];
-        if (t1 > t0 && ok) {
-          const uint32_t ta = tmem + (quarter * 32u << 16) + b * 2 * RP + j;
-          tmem_ld_x16(ta, h);
-          tmem_ld_x16(ta + RP, l);
+    bool ok = true;
+    for (int i = 0; ok && w.next(t0, t1, E); ++i) {
+      const int buf = bufs == 2 ? i & 1 : 0, use = bufs == 2 ? i >> 1 : i;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_acc(buf), use & 1, abort_flag)) && !*abort_flag;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const bool whole = w.b0 == 0 && w.b1 == (w.n + kTok - 1) / kTok;
+      float4* to = partial(rank, w.b0 > 0 ? 0 : 1);
+      for (int h = 0; h < 2; ++h) {
+        const int f = h * 128 + static_cast<int>(quarter * 32 + lane);
+        for (int j = 0; j < RP; j += 16) {
+          uint32_t x[16], y[16];
+          const uint32_t ta = tmem + (quarter * 32u << 16) + buf * 4 * RP + h * 2 * RP + j;
+          tmem_ld_x16(ta, x);
+          tmem_ld_x16(ta + RP, y);
           tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) h[k] = l[k] = 0u;
+          for (int q = 0; q < 4; ++q) {
+            const float4 v = make_float4(__uint_as_float(x[4 * q]) + __uint_as_float(y[4 * q]),
+                                         __uint_as_float(x[4 * q + 1]) + __uint_as_float(y[4 * q + 1]),
+                                         __uint_as_float(x[4 * q + 2]) + __uint_as_float(y[4 * q + 2]),
+                                         __uint_as_float(x[4 * q + 3]) + __uint_as_float(y[4 * q + 3]));
+            if (whole)
+              store4(w.e, f, j + 4 * q, v);
+            else
+              to[(j / 4 + q) * kWidth + f] = v;
+          }
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_shared_f4(sbase + (static_cast<uint32_t>((j / 4 + q) * width) + f) * 16u,
-                       __uint_as_float(h[4 * q]) + __uint_as_float(l[4 * q]),
-                       __uint_as_float(h[4 * q + 1]) + __uint_as_float(l[4 * q + 1]),
-                       __uint_as_float(h[4 * q + 2]) + __uint_as_float(l[4 * q + 2]),
-                       __uint_as_float(h[4 * q + 3]) + __uint_as_float(l[4 * q + 3]));
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free(buf));
     }
-    tc_fence_before();
-    __syncwarp();
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      if (a.status) atomicOr(a.status, kDevTimeout);
+    }
+    // adapters without rows, dealt out to the cluster's CTAs
+    for (int e = rank; e < E; e += C) {
+      if (s_off[e + 1] != s_off[e]) continue;
+      for (int i = tid - 64; i < kWidth * (RP / 4); i += 128)
+        store4(e, i % kWidth, i / kWidth * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    }
   }
+  tc_fence_before();
   __syncthreads();
-  cluster_sync();  // every CTA's sums are there
-  if (!*abort_flag) {
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, tmem_cols);
+  if (C == 1) return;
+  __syncwarp();
+  cluster_sync();  // every CTA's partial sums are in the workspace
+  if (*abort_flag) return;
+  Walk v = {s_off, -1, 0, 0, 0, 0, 0, 0};
+  while (v.next(t0, t1, E)) {
+    const int end = v.at + (v.n + kTok - 1) / kTok;
+    if (v.at >= t0 && end <= t1) continue;
+    // the CTAs with blocks of this adapter
+    uint32_t with = 0;
+    for (int p = 0; p < C; ++p) {
+      const int p0 = share(blocks, p, C), p1 = share(blocks, p + 1, C);
+      if (p0 < p1 && p0 < end && p1 > v.at) with |= 1u << p;
+    }
+    const int count = __popc(with), k = __popc(with & ((1u << rank) - 1u));
+    const int g0 = kWidth * k / count, per = kWidth * (k + 1) / count - g0;
     for (int i = tid; i < per * (RP / 4); i += kThreads) {
-      const int f = rank * per + i % per, j4 = i / per;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int p = 0; p < C; ++p) {
-        const float4 x = ld_cluster_f4(map_to_cta(sbase + static_cast<uint32_t>(j4 * width + f) * 16u, p));
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      const int f = g0 + i % per, j4 = i / per;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (uint32_t m = with; m != 0; m &= m - 1) {
+        const int p = __ffs(m) - 1;
+        const float4 x = __ldcg(partial(p, v.at < share(blocks, p, C) ? 0 : 1) + j4 * kWidth + f);
+        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
       }
-      store4(f, 4 * j4, v);
+      store4(v.e, f, 4 * j4, s);
     }
   }
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
-  __syncwarp();
-  cluster_sync();  // nobody reads this CTA's sums any more
 }
 
-template <int FB>
 cudaError_t set_smem() {
   static thread_local uint64_t attr_ctx = 0;
-  return set_smem_attr_once(reinterpret_cast<const void*>(lora_grad_kernel<FB>), 227 * 1024, &attr_ctx);
+  return set_smem_attr_once(reinterpret_cast<const void*>(lora_grad_kernel), 227 * 1024, &attr_ctx);
 }
 
-template <int FB>
 cudaLaunchConfig_t config(int cluster, long long items, size_t smem, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * cluster));
@@ -354,64 +390,58 @@ cudaLaunchConfig_t config(int cluster, long long items, size_t smem, cudaLaunchA
   return cfg;
 }
 
-// The largest cluster, up to eight CTAs, that the current context can run; asked once per context
-// and thread, for the largest shared memory.
-template <int FB>
-int largest_cluster() {
+// Clusters of c CTAs that the current context runs at once (none where it has a share of the SMs
+// that is too small).  Asked once per context and thread.
+int clusters_at_once(int c) {
   static thread_local uint64_t asked_ctx = 0;
-  static thread_local int largest = 1;
-  if (asked_ctx != 0 && asked_ctx == current_context_id()) return largest;
-  largest = 1;
-  for (int c = 8; c > 1; c /= 2) {
-    cudaLaunchAttribute attr = {};
-    const cudaLaunchConfig_t cfg = config<FB>(c, 1, 226 * 1024, &attr);
-    int active = 0;
-    if (cudaOccupancyMaxActiveClusters(&active, lora_grad_kernel<FB>, &cfg) != cudaSuccess) {
-      (void)cudaGetLastError();  // a size that does not fit is no error of the call
-      active = 0;
+  static thread_local int active[kMaxCluster + 1];
+  if (asked_ctx == 0 || asked_ctx != current_context_id()) {
+    for (int k = 2; k <= kMaxCluster; ++k) {
+      cudaLaunchAttribute attr = {};
+      const cudaLaunchConfig_t cfg = config(k, 1, 227 * 1024, &attr);
+      if (cudaOccupancyMaxActiveClusters(&active[k], lora_grad_kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();  // a size that does not fit is no error of the call
+        active[k] = 0;
+      }
     }
-    if (active > 0) {
-      largest = c;
-      break;
-    }
+    asked_ctx = current_context_id();
   }
-  asked_ctx = current_context_id();
-  return largest;
+  return active[c];
 }
 
-template <int FB>
-cudaError_t launch(LoraGradArgs a, int num_sms, cudaStream_t stream) {
-  const cudaError_t err = set_smem<FB>();
-  if (err != cudaSuccess) return err;
-  const Shape s = shape_of(a.R);
-  long long items[2] = {0, 0};
-  for (int i = 0; i < a.jobs; ++i)
-    items[i] = static_cast<long long>(a.E) * ((a.job[i].cols + FB * 128 - 1) / (FB * 128));
-  a.first[0] = 0;
-  a.first[1] = a.jobs == 2 ? static_cast<int>(items[0]) : 0x7fffffff;
-  a.stages = s.stages;
-  a.tmem_cols = s.tmem_cols;
-  int most = largest_cluster<FB>();
-  if (a.max_cluster > 0 && a.max_cluster < most) most = a.max_cluster;
-  const long long total = items[0] + items[1];
-  int c = 1;
-  while (2 * c <= most && 2 * c * kTok <= a.M && total * 2 * c <= num_sms * (FB == 1 ? 2 : 1)) c *= 2;
-  a.cluster = c;
-  cudaLaunchAttribute attr = {};
-  cudaLaunchConfig_t cfg = config<FB>(c, total, s.smem, &attr);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, lora_grad_kernel<FB>, a);
-}
+long long items_of(int cols) { return (static_cast<long long>(cols) + kWidth - 1) / kWidth; }
 
 }  // namespace
 
-long long lora_grad_items(int E, int cols, int R) {
-  const int width = feature_blocks(R) * 128;
-  return static_cast<long long>(E) * ((cols + width - 1) / width);
+size_t lora_q_bytes(int M, int E, int R) {
+  const long long tiles = M / 128 + (M < E ? M : E);
+  return static_cast<size_t>(tiles) * 2 * 256 * padded_rank(R);
 }
 
-cudaError_t launch_lora_grad(const LoraGradArgs& a, int num_sms, cudaStream_t stream) {
-  return feature_blocks(a.R) == 1 ? launch<1>(a, num_sms, stream) : launch<2>(a, num_sms, stream);
+size_t lora_partial_bytes(int K, int N, int R) {
+  // clusters of several CTAs only where all CTAs together are at most kSms
+  if (2 * (items_of(K) + items_of(N)) > kSms) return 0;
+  return sizeof(float) * kSms * 2 * part_floats(padded_rank(R));
+}
+
+cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream) {
+  const cudaError_t err = set_smem();
+  if (err != cudaSuccess) return err;
+  const int RP = padded_rank(a.R);
+  const long long items = items_of(a.job[0].cols) + items_of(a.job[1].cols);
+  a.first1 = static_cast<int>(items_of(a.job[0].cols));
+  a.stages = stages_of(RP);
+  // As many CTAs to a feature block as run at once: 15 clusters of eight, 36 of four.
+  const int most = a.max_cluster > 0 && a.max_cluster < kMaxCluster ? a.max_cluster : kMaxCluster;
+  int c = 1;
+  for (int k = 2; k <= most; ++k)
+    if (items * k <= kSms && static_cast<long long>(k) * kTok <= a.M && items <= clusters_at_once(k)) c = k;
+  a.cluster = c;
+  cudaLaunchAttribute attr = {};
+  cudaLaunchConfig_t cfg =
+      config(c, items, static_cast<size_t>(a.stages) * stage_bytes(RP) + misc_bytes(a.E), &attr);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, lora_grad_kernel, a);
 }
 
 }  // namespace mgw

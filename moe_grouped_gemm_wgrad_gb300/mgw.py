@@ -142,7 +142,7 @@ def bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mgw_grouped_lora_backward.argtypes = [P, I, P, P, I, P, I, I, P, P, P, P, I, I, I, P, P, P, P, P, P, SZ,
                                               P, P]
     lib.mgw_grouped_lora_backward.restype = I
-    lib.mgw_grouped_lora_backward_workspace_bytes.argtypes = [I, I]
+    lib.mgw_grouped_lora_backward_workspace_bytes.argtypes = [I, I, I, I, I]
     lib.mgw_grouped_lora_backward_workspace_bytes.restype = SZ
     return lib
 
@@ -1014,7 +1014,7 @@ def grouped_lora_backward(dy: torch.Tensor, x: torch.Tensor | None, u: torch.Ten
     if with_weights:
         da = _out(da, (E, R, K), torch.bfloat16, dev, "da", side)
         db = _out(db, (E, N, R), torch.bfloat16, dev, "db", side)
-        need = int(lib.mgw_grouped_lora_backward_workspace_bytes(M, R))
+        need = int(lib.mgw_grouped_lora_backward_workspace_bytes(E, M, K, N, R))
         workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side)
     with _device(dev):
         st = lib.mgw_grouped_lora_backward(_ptr(dy), rows, _ptr(out_index), _ptr(x), x_rows,
