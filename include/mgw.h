@@ -534,6 +534,38 @@ mgw_status mgw_grouped_lora_backward(const void *dy_bf16, int out_rows, const in
 /* Host only; 0 for invalid sizes. */
 size_t mgw_grouped_lora_backward_workspace_bytes(int E, int M, int K, int N, int R);
 
+/* ------------------------------------------------- gradient norm and clipping
+ * Over all gradients of a model at once: grad_w of the experts, adapters, biases, in any mix of
+ * sizes and of bf16 and fp32.  grads, outs, sizes and dtypes are HOST arrays of n entries (read
+ * before the call returns; a captured call keeps the pointers in them): device pointers aligned
+ * to their element, elements (>= 0), MGW_TYPE_*.  At most 2^42 bytes and 2^24 tensors. */
+
+/* mgw_grad_norm -- norm = sqrt(sum over all tensors and elements of g^2), 0 for no elements.
+ * The sum's order is fixed by the sizes and alignments; right to a few fp32 roundings wherever
+ * the norm is an fp32 number, however large or small the elements' squares.
+ * norm       device fp32, one number.
+ * workspace  device, 16-byte aligned, mgw_grad_workspace_bytes(n) bytes; need not be initialised.
+ *            Calls sharing it must not overlap. */
+mgw_status mgw_grad_norm(const void *const *grads, const int64_t *sizes, const int *dtypes, int n,
+                         float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/* mgw_grad_clip -- outs[i] = grads[i] * min(1, max_norm / (norm + eps)), each rounded once.
+ * outs       null: in place.  Otherwise each of its tensor's type and size; the tensor itself, or
+ *            memory that overlaps no tensor of the call.  No tensor is listed twice.
+ * max_norm, eps >= 0.
+ * norm_in    device fp32, nullable: a norm known already (of several processes' gradients, say).
+ *            Null: the norm of the gradients, which is written to `norm`; exactly one of the two
+ *            is given.
+ * An infinite norm gives factor 0 (and infinities times 0 are none); a norm that is not a number
+ * makes every gradient none.
+ * workspace  as for mgw_grad_norm. */
+mgw_status mgw_grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
+                         const int *dtypes, int n, float max_norm, float eps,
+                         const float *norm_in, float *norm, void *workspace,
+                         size_t workspace_bytes, void *stream);
+/* Host only; 0 for invalid n. */
+size_t mgw_grad_workspace_bytes(int n);
+
 #ifdef __cplusplus
 }
 #endif

@@ -140,6 +140,7 @@ bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint6
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 
@@ -1021,6 +1022,89 @@ mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const in
   g.max_cluster = test_max_cluster();
   g.status = status_dev;
   const cudaError_t err = mgw::launch_lora_grad(g, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------- gradient norm and clipping
+namespace {
+
+mgw_status grad_check(const void* const* grads, const int64_t* sizes, const int* dtypes, int n,
+                      const void* workspace, size_t workspace_bytes) {
+  static_assert(mgw::kGradF32 == MGW_TYPE_F32, "element types");
+  if (n < 0 || (n > 0 && (!grads || !sizes || !dtypes))) return MGW_ERR_INVALID_ARG;
+  int64_t bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!element_type(dtypes[i]) || sizes[i] < 0 || (sizes[i] > 0 && !grads[i])) return MGW_ERR_INVALID_ARG;
+    const int size = dtypes[i] == MGW_TYPE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(grads[i]) % size != 0) return MGW_ERR_INVALID_ARG;
+    // chunks are counted in 32 bits
+    if (sizes[i] > (int64_t(1) << 40)) return MGW_ERR_UNSUPPORTED;
+    bytes += sizes[i] * size;
+    if (bytes > (int64_t(1) << 42)) return MGW_ERR_UNSUPPORTED;
+  }
+  if (n > (1 << 24)) return MGW_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace)) return MGW_ERR_INVALID_ARG;
+  return workspace_bytes < mgw::grad_workspace_bytes(n) ? MGW_ERR_CAPACITY : MGW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mgw_grad_workspace_bytes(int n) { return n < 0 || n > (1 << 24) ? 0 : mgw::grad_workspace_bytes(n); }
+
+mgw_status mgw_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int n, float* norm,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  mgw_status st = grad_check(grads, sizes, dtypes, n, workspace, workspace_bytes);
+  if (st != MGW_OK) return st;
+  if (!norm || !aligned4(norm)) return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK) return st;
+  mgw::GradArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.grads = grads;
+  a.sizes = sizes;
+  a.dtypes = dtypes;
+  a.count = n;
+  a.sums = static_cast<double*>(workspace);
+  a.norm = norm;
+  a.sms = dev.sms;
+  const cudaError_t err = mgw::launch_grad(a, false, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
+}
+
+mgw_status mgw_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes,
+                         int n, float max_norm, float eps, const float* norm_in, float* norm, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  mgw_status st = grad_check(grads, sizes, dtypes, n, workspace, workspace_bytes);
+  if (st != MGW_OK) return st;
+  // (also refuses numbers that are none)
+  if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return MGW_ERR_INVALID_ARG;
+  if (!norm_in == !norm || !aligned4(norm_in) || !aligned4(norm)) return MGW_ERR_INVALID_ARG;
+  for (int i = 0; outs && i < n; ++i)
+    if (sizes[i] > 0 &&
+        (!outs[i] || reinterpret_cast<uintptr_t>(outs[i]) % (dtypes[i] == MGW_TYPE_F32 ? 4 : 2) != 0))
+      return MGW_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MGW_OK) return st;
+  mgw::GradArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.grads = grads;
+  a.outs = outs;
+  a.sizes = sizes;
+  a.dtypes = dtypes;
+  a.count = n;
+  a.sums = static_cast<double*>(workspace);
+  a.norm_in = norm_in;
+  a.norm = norm;
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.sms = dev.sms;
+  const cudaError_t err = mgw::launch_grad(a, true, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
 }
 

@@ -1,0 +1,394 @@
+// The norm of all gradients of a model together, and the gradients scaled down to a largest norm:
+//
+//   norm = sqrt(sum over all tensors and elements of g^2)
+//   out  = g * min(1, max_norm / (norm + eps))
+//
+// HBM bounds both.  The tensors' table (address, size, type of each) rides in the kernel's
+// parameters, up to 32 KB of them: nothing is copied to the device and a captured call replays as it
+// is.  Every tensor is cut into chunks of 16 KB, and every CTA takes a run of the chunks of all tensors
+// that is equally long for all CTAs, so large and tiny tensors mix without a tail.
+//
+// Squares are summed in fp32 over one thread's share of a chunk (at most 32 elements, in four
+// sums), these are added without loss (a pair of fp32 numbers, each addition's rounding error kept) and
+// meet in fp64.  A share whose sum overflows, or is too small to be right (below 2^-80 though not all
+// zeros), is summed again in fp64 from the values at hand: the norm is right wherever it is itself
+// an fp32 number.
+//
+// The clipping launch adds the CTAs' sums up in every CTA (a few KB, always in the same order) rather
+// than wait for a launch in between; it walks the chunks backwards, so that what the norm read last is
+// still in L2.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace mgw {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 16384;                // bytes
+constexpr int kVecs = kChunk / 16 / kThreads;  // 16-byte pieces a thread has of a chunk
+constexpr int kCtasPerSm = 4;
+constexpr int kSmallTable = 96, kLargeTable = 1024;  // tensors of a launch
+constexpr int kMostSms = 160;  // that a launch is sized for
+
+struct Entry {
+  const void* g;
+  void* out;  // null: the norm only
+  int64_t n;  // elements
+};
+// The tensors of one launch.  first[i]: chunks before tensor i; f32 as bits.
+template <int CAP>
+struct Table {
+  Entry t[CAP];
+  int first[CAP + 1];
+  uint32_t f32[(CAP + 31) / 32];
+  int count;
+  double* sums;        // one per CTA of every launch
+  int sums_at, total;  // this launch's first one; how many there are in all
+  float* norm;
+  const float* norm_in;  // clip to this norm; null: to that of the sums
+  float max_norm, eps;
+};
+static_assert(sizeof(Table<kLargeTable>) <= 32764, "kernel parameters");
+static_assert(sizeof(Table<kSmallTable>) <= 4096, "kernel parameters");
+
+// A chunk of a tensor: whole 16-byte pieces (of the input's alignment) and, in the tensor's first and
+// last chunk, the elements before and behind them.
+struct Piece {
+  const uint8_t* g;
+  uint8_t* out;
+  int64_t lo, hi;      // bytes of the chunk's 16-byte pieces, from the first aligned address on
+  int head, tail;      // elements before and behind (first and last chunk)
+  int64_t tail_at;     // element
+  int skip;            // bytes from g to the first aligned address
+  bool f32;
+};
+
+template <int CAP>
+__device__ __forceinline__ Piece piece_of(const Table<CAP>& a, int i, int chunk) {
+  const Entry& e = a.t[i];
+  Piece p;
+  p.f32 = (a.f32[i >> 5] >> (i & 31)) & 1u;
+  const int size = p.f32 ? 4 : 2;
+  p.g = static_cast<const uint8_t*>(e.g);
+  p.out = static_cast<uint8_t*>(e.out);
+  const int64_t bytes = e.n * size;
+  int64_t skip = (16 - (reinterpret_cast<uintptr_t>(e.g) & 15)) & 15;
+  if (skip > bytes) skip = bytes;
+  p.skip = static_cast<int>(skip);
+  const int64_t whole = (bytes - skip) & ~int64_t(15);
+  const int64_t k = chunk - a.first[i];
+  p.lo = k * kChunk;
+  p.hi = p.lo + kChunk < whole ? p.lo + kChunk : whole;
+  p.head = k == 0 ? p.skip / size : 0;
+  const bool last = chunk + 1 == a.first[i + 1];
+  p.tail = last ? static_cast<int>((bytes - skip - whole) / size) : 0;
+  p.tail_at = (skip + whole) / size;
+  return p;
+}
+
+// The largest i with first[i] <= chunk and a chunk of its own (tensors without elements have none).
+template <int CAP>
+__device__ __forceinline__ int locate(const Table<CAP>& a, int chunk) {
+  int lo = 0, hi = a.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float element(const Piece& p, int64_t i) {
+  return p.f32 ? reinterpret_cast<const float*>(p.g)[i]
+               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.g)[i]);
+}
+
+// The sum of a CTA's doubles, in every thread; s holds kWarps.
+__device__ __forceinline__ double block_sum(double v, double* s) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += s[w];
+  return sum;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_norm_kernel(const __grid_constant__ Table<CAP> a) {
+  __shared__ double s_sum[kWarps];
+  const int chunks = a.first[a.count];
+  const int c0 = static_cast<int>(static_cast<long long>(chunks) * blockIdx.x / gridDim.x);
+  const int c1 = static_cast<int>(static_cast<long long>(chunks) * (blockIdx.x + 1) / gridDim.x);
+  float hi = 0.0f, lo = 0.0f;  // their sum is exact but for lo's own rounding
+  double rest = 0.0;           // shares that fp32 cannot hold
+  auto add = [&](float s, uint32_t any, auto again) {
+    if (s < 0x1p120f && (s >= 0x1p-80f || any == 0u)) {
+      const float t = hi + s, z = t - hi;
+      lo += (hi - (t - z)) + (s - z);
+      hi = t;
+      if (hi >= 0x1p120f) rest += hi, hi = 0.0f;
+    } else {
+      rest += again();
+    }
+  };
+  int i = c0 < c1 ? locate(a, c0) : 0;
+  for (int c = c0; c < c1; ++c) {
+    while (c >= a.first[i + 1]) ++i;
+    const Piece p = piece_of(a, i, c);
+    const uint4* v = reinterpret_cast<const uint4*>(p.g + p.skip);
+    uint4 w[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t at = p.lo / 16 + threadIdx.x + k * kThreads;
+      w[k] = at < p.hi / 16 ? __ldg(v + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t any = 0u;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        any |= u[j];
+        if (p.f32) {
+          const float f = __uint_as_float(u[j]);
+          s[j] += f * f;
+        } else {
+          const float2 f = bf16_pair(u[j]);
+          s[j] += f.x * f.x;
+          s[j] += f.y * f.y;
+        }
+      }
+    }
+    add((s[0] + s[1]) + (s[2] + s[3]), any, [&] {
+      double d = 0.0;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (p.f32) {
+            const double f = __uint_as_float(u[j]);
+            d += f * f;
+          } else {
+            const float2 f = bf16_pair(u[j]);
+            d += static_cast<double>(f.x) * f.x + static_cast<double>(f.y) * f.y;
+          }
+        }
+      }
+      return d;
+    });
+    const int t = static_cast<int>(threadIdx.x);
+    if (t < p.head + p.tail) {  // at most seven elements each
+      const double f = element(p, t < p.head ? t : p.tail_at + (t - p.head));
+      rest += f * f;
+    }
+  }
+  const double sum = block_sum(static_cast<double>(hi) + static_cast<double>(lo) + rest, s_sum);
+  if (threadIdx.x == 0) a.sums[a.sums_at + blockIdx.x] = sum;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// norm from all CTAs' sums, the same in every CTA.
+__device__ __forceinline__ float total_norm(const double* sums, int total, double* s) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < total; i += kThreads) v += sums[i];
+  return static_cast<float>(sqrt(block_sum(v, s)));
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_end_kernel(const double* sums, int total, float* norm) {
+  __shared__ double s_sum[kWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float n = total_norm(sums, total, s_sum);
+  if (threadIdx.x == 0) *norm = n;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_clip_kernel(const __grid_constant__ Table<CAP> a) {
+  __shared__ double s_sum[kWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float norm = a.norm_in != nullptr ? *a.norm_in : total_norm(a.sums, a.total, s_sum);
+  if (a.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+  // min(1, ..), but not for a norm that is not a number: then every gradient is none
+  float f = a.max_norm / (norm + a.eps);
+  f = f > 1.0f ? 1.0f : f;
+  const int chunks = a.first[a.count];
+  const int c0 = static_cast<int>(static_cast<long long>(chunks) * blockIdx.x / gridDim.x);
+  const int c1 = static_cast<int>(static_cast<long long>(chunks) * (blockIdx.x + 1) / gridDim.x);
+  int i = c0 < c1 ? locate(a, c1 - 1) : 0;
+  for (int c = c1 - 1; c >= c0; --c) {
+    while (c < a.first[i]) --i;
+    const Piece p = piece_of(a, i, c);
+    if (f == 1.0f && p.out == p.g) continue;  // times 1, in place
+    const uint4* v = reinterpret_cast<const uint4*>(p.g + p.skip);
+    uint4 w[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t at = p.lo / 16 + threadIdx.x + k * kThreads;
+      if (at < p.hi / 16) w[k] = v[at];
+    }
+    // the output's 16-byte pieces lie as the input's do, or they are stored element by element
+    const bool same = ((reinterpret_cast<uintptr_t>(p.out) ^ reinterpret_cast<uintptr_t>(p.g)) & 15) == 0;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t at = p.lo / 16 + threadIdx.x + k * kThreads;
+      if (at >= p.hi / 16) continue;
+      uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (p.f32) {
+          u[j] = __float_as_uint(__uint_as_float(u[j]) * f);
+        } else {
+          const float2 x = bf16_pair(u[j]);
+          const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * f, x.y * f);
+          u[j] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      uint8_t* to = p.out + p.skip + at * 16;
+      if (same) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (p.f32) {
+            reinterpret_cast<uint32_t*>(to)[j] = u[j];
+          } else {
+            reinterpret_cast<uint16_t*>(to)[2 * j] = static_cast<uint16_t>(u[j]);
+            reinterpret_cast<uint16_t*>(to)[2 * j + 1] = static_cast<uint16_t>(u[j] >> 16);
+          }
+        }
+      }
+    }
+    const int t = static_cast<int>(threadIdx.x);
+    if (t < p.head + p.tail) {
+      const int64_t at = t < p.head ? t : p.tail_at + (t - p.head);
+      const float x = element(p, at) * f;
+      if (p.f32)
+        reinterpret_cast<float*>(p.out)[at] = x;
+      else
+        reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+    }
+  }
+}
+
+// Starts while the launch before ends; the kernel waits for its results itself.
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int grid, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+bool is_f32(const GradArgs& a, int i) { return a.dtypes[i] == kGradF32; }
+
+int64_t chunks_of(const GradArgs& a, int i) {
+  const int64_t bytes = a.sizes[i] * (is_f32(a, i) ? 4 : 2);
+  int64_t skip = (16 - (reinterpret_cast<uintptr_t>(a.grads[i]) & 15)) & 15;
+  if (skip > bytes) skip = bytes;
+  const int64_t whole = (bytes - skip) & ~int64_t(15);
+  if (bytes == 0) return 0;
+  return whole > 0 ? (whole + kChunk - 1) / kChunk : 1;
+}
+
+// The tensors of one launch, and its CTAs.
+struct Group {
+  int begin, end, grid;
+};
+Group group_from(const GradArgs& a, int begin) {
+  Group g = {begin, begin, 0};
+  int64_t chunks = 0;
+  while (g.end < a.count && g.end - begin < kLargeTable) chunks += chunks_of(a, g.end++);
+  const int64_t most = static_cast<int64_t>(a.sms < kMostSms ? a.sms : kMostSms) * kCtasPerSm;
+  g.grid = static_cast<int>(chunks < 1 ? 1 : (chunks < most ? chunks : most));
+  return g;
+}
+
+template <int CAP>
+void fill(Table<CAP>* k, const GradArgs& a, const Group& g) {
+  k->count = g.end - g.begin;
+  int at = 0;
+  for (uint32_t& w : k->f32) w = 0;
+  for (int j = 0; j < k->count; ++j) {
+    const int i = g.begin + j;
+    k->t[j].g = a.grads[i];
+    k->t[j].out = a.outs != nullptr ? a.outs[i] : const_cast<void*>(a.grads[i]);
+    k->t[j].n = a.sizes[i];
+    k->first[j] = at;
+    at += static_cast<int>(chunks_of(a, i));
+    if (is_f32(a, i)) k->f32[j >> 5] |= 1u << (j & 31);
+  }
+  k->first[k->count] = at;
+}
+
+template <int CAP>
+cudaError_t launch_table(const GradArgs& a, const Group& g, int sums_at, int total, bool clip, cudaStream_t stream) {
+  Table<CAP> k;
+  fill(&k, a, g);
+  k.sums = a.sums;
+  k.sums_at = sums_at;
+  k.total = total;
+  k.norm = g.begin == 0 ? a.norm : nullptr;
+  k.norm_in = a.norm_in;
+  k.max_norm = a.max_norm;
+  k.eps = a.eps;
+  if (clip) return launch_after(grad_clip_kernel<CAP>, g.grid, stream, k);
+  grad_norm_kernel<CAP><<<static_cast<unsigned>(g.grid), kThreads, 0, stream>>>(k);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_group(const GradArgs& a, const Group& g, int sums_at, int total, bool clip, cudaStream_t stream) {
+  return g.end - g.begin <= kSmallTable ? launch_table<kSmallTable>(a, g, sums_at, total, clip, stream)
+                                        : launch_table<kLargeTable>(a, g, sums_at, total, clip, stream);
+}
+
+}  // namespace
+
+size_t grad_workspace_bytes(int count) {
+  // a sum for every CTA of every launch
+  const size_t launches = count > 0 ? (static_cast<size_t>(count) + kLargeTable - 1) / kLargeTable : 1;
+  return sizeof(double) * launches * kMostSms * kCtasPerSm;
+}
+
+cudaError_t launch_grad(const GradArgs& a, bool clip, cudaStream_t stream) {
+  int total = 0;
+  if (a.norm_in == nullptr) {
+    for (int i = 0; i < a.count;) {
+      const Group g = group_from(a, i);
+      const cudaError_t err = launch_group(a, g, total, 0, false, stream);
+      if (err != cudaSuccess) return err;
+      total += g.grid;
+      i = g.end;
+    }
+    if (!clip || a.count == 0)
+      return launch_after(grad_norm_end_kernel, 1, stream, static_cast<const double*>(a.sums), total, a.norm);
+  }
+  for (int i = 0; i < a.count;) {
+    const Group g = group_from(a, i);
+    const cudaError_t err = launch_group(a, g, 0, total, true, stream);
+    if (err != cudaSuccess) return err;
+    i = g.end;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace mgw

@@ -261,6 +261,23 @@ size_t lora_q_bytes(int M, int E, int R);
 size_t lora_partial_bytes(int K, int N, int R);
 cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream);
 
+// Gradient norm and clipping (grad_norm.cu): host arrays of `count` tensors.
+constexpr int kGradF32 = 1;  // of dtypes; else bf16
+struct GradArgs {
+  const void* const* grads;
+  void* const* outs;     // null: in place
+  const int64_t* sizes;  // elements
+  const int* dtypes;
+  int count;
+  double* sums;          // grad_workspace_bytes
+  const float* norm_in;  // device: clip to this norm; null: to the gradients'
+  float* norm;           // device; may be null when clipping
+  float max_norm, eps;
+  int sms;
+};
+size_t grad_workspace_bytes(int count);
+cudaError_t launch_grad(const GradArgs& a, bool clip, cudaStream_t stream);
+
 struct DgradArgs {
   CUtensorMap tm_w;    // W fp32 [E*out_f, in_f], box 256 columns x 32 rows, no swizzle
   CUtensorMap tm_dy;   // dy fp32 [rows, out_f], box 32 columns x 128 rows, 128B swizzle

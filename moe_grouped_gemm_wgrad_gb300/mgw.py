@@ -66,6 +66,7 @@ EXPORTS = (
     "mgw_moe_dispatch_workspace_bytes", "mgw_grouped_fprop_mxfp8_act", "mgw_grouped_act_backward",
     "mgw_grouped_act_backward_workspace_bytes", "mgw_moe_combine", "mgw_moe_combine_backward",
     "mgw_grouped_lora", "mgw_grouped_lora_backward", "mgw_grouped_lora_backward_workspace_bytes",
+    "mgw_grad_norm", "mgw_grad_clip", "mgw_grad_workspace_bytes",
 )
 
 
@@ -144,6 +145,12 @@ def bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mgw_grouped_lora_backward.restype = I
     lib.mgw_grouped_lora_backward_workspace_bytes.argtypes = [I, I, I, I, I]
     lib.mgw_grouped_lora_backward_workspace_bytes.restype = SZ
+    lib.mgw_grad_norm.argtypes = [P, P, P, I, P, P, SZ, P]
+    lib.mgw_grad_norm.restype = I
+    lib.mgw_grad_clip.argtypes = [P, P, P, P, I, FL, FL, P, P, P, SZ, P]
+    lib.mgw_grad_clip.restype = I
+    lib.mgw_grad_workspace_bytes.argtypes = [I]
+    lib.mgw_grad_workspace_bytes.restype = SZ
     return lib
 
 
@@ -1028,3 +1035,110 @@ def grouped_lora_backward(dy: torch.Tensor, x: torch.Tensor | None, u: torch.Ten
         _used_on(side, dy, x, u, a, b, adapter_off, row_index, out_index, scale, dx_base, dx, da, db,
                  workspace, status)
     return dx, da, db
+
+
+# ------------------------------------------------------------------- gradient norm and clipping
+class GradTable:
+    """The gradients (bf16 and fp32 tensors, any sizes, contiguous, on one device) that
+    :func:`grad_norm` and :func:`clip_grads` take, checked once: for a program whose gradient buffers
+    stay where they are from step to step, and for captured calls.  ``out``: tensors of the same
+    types and sizes that the clipped gradients go to, the gradients themselves or memory that
+    overlaps none of the call's tensors (without it: in place).  Holds the tensors."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = None if out is None else list(out)
+        self.device, self._kinds, sizes = self._checked(self.grads, "grads")
+        n = self.n = len(self.grads)
+        at = [t.data_ptr() for t in self.grads]
+        self._grads = (ctypes.c_void_p * n)(*at)
+        self._sizes = (ctypes.c_int64 * n)(*sizes)
+        self._dtypes = (ctypes.c_int * n)(*self._kinds)
+        self._out = None
+        if self.out is not None:
+            dev, kinds, out_sizes = self._checked(self.out, "out")
+            if kinds != self._kinds or out_sizes != sizes or (n and dev != self.device):
+                raise MgwError("out must hold one tensor of the same type, size and device for every gradient")
+            at = [t.data_ptr() for t in self.out]
+            self._out = (ctypes.c_void_p * n)(*at)
+        used = [p for p, s in zip(at, sizes) if s]
+        self._twice = len(set(used)) != len(used)
+
+    @staticmethod
+    def _checked(ts, name):
+        dev, kinds, sizes = None, [], []
+        for t in ts:
+            kinds.append(_element_type(t, name))
+            if not _on_cuda(t):
+                raise MgwError(f"{name} must be CUDA tensors")
+            if not t.is_contiguous():
+                raise MgwError(f"{name} must be contiguous")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise MgwError(f"all tensors must be on one CUDA device, got {dev} and {t.device} in {name}")
+            sizes.append(t.numel())
+        return dev, kinds, sizes
+
+
+def _grad_call(grads, norm, workspace, stream):
+    """The table of ``grads`` and the checked or new buffers -> (table, device, side, norm, workspace)."""
+    table = grads if isinstance(grads, GradTable) else GradTable(grads)
+    dev = table.device
+    if dev is None:  # no gradients at all
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if norm is not None:
+        _dev_tensor(norm, torch.float32, "norm")
+        _need(norm, 1, "norm")
+    if workspace is not None:
+        _dev_tensor(workspace, torch.uint8, "workspace")
+    for t in (norm, workspace):
+        if t is not None and t.device != dev:
+            raise MgwError(f"all tensors must be on one CUDA device, got {sorted({str(dev), str(t.device)})}")
+    side = None if stream is None else _side(stream, dev)
+    need = int(load().mgw_grad_workspace_bytes(_size(table.n, "the number of gradients")))
+    workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side)
+    return table, dev, side, workspace
+
+
+def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """The norm of all ``grads`` together (a :class:`GradTable` or a list of bf16 and fp32 tensors)
+    -> fp32 [1]: sqrt of the sum of all elements' squares, 0 for no elements."""
+    table, dev, side, workspace = _grad_call(grads, norm, workspace, stream)
+    norm = _out(norm, (1,), torch.float32, dev, "norm", side)
+    with _device(dev):
+        st = load().mgw_grad_norm(table._grads, table._sizes, table._dtypes, table.n, _ptr(norm),
+                                  _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "mgw_grad_norm")
+    if side is not None:
+        _used_on(side, norm, workspace, *table.grads)
+    return norm
+
+
+def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, known_norm: torch.Tensor | None = None,
+               eps: float = 1e-6, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Multiplies all ``grads`` (a :class:`GradTable`, into its ``out`` if it has one, or a list) by
+    min(1, max_norm / (norm + eps)) -> their norm, fp32 [1], as :func:`grad_norm` gives it.
+    ``known_norm`` (fp32 [1]), where given, is taken for the norm and returned: that of several
+    processes' gradients, for example."""
+    table, dev, side, workspace = _grad_call(grads, norm, workspace, stream)
+    if table._twice:
+        raise MgwError("a tensor that is written is listed twice")
+    if known_norm is not None:
+        if norm is not None:
+            raise MgwError("norm is not computed where known_norm is given")
+        _dev_tensor(known_norm, torch.float32, "known_norm")
+        _need(known_norm, 1, "known_norm")
+        if known_norm.device != dev:
+            raise MgwError(f"all tensors must be on one CUDA device, got {dev} and {known_norm.device}")
+    else:
+        norm = _out(norm, (1,), torch.float32, dev, "norm", side)
+    with _device(dev):
+        st = load().mgw_grad_clip(table._grads, table._out, table._sizes, table._dtypes, table.n,
+                                  float(max_norm), float(eps), _ptr(known_norm), _ptr(norm),
+                                  _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "mgw_grad_clip")
+    if side is not None:
+        _used_on(side, norm, known_norm, workspace, *table.grads, *(table.out or ()))
+    return norm if known_norm is None else known_norm
