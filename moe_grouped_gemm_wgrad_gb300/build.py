@@ -28,7 +28,7 @@ LIB_DIAG = os.path.join(HERE, "libmgw_diag.so")
 DIAG_SOURCES = ["api.cu", "wgrad.cu", "dgrad.cu", "dgrad_pair.cu"]
 SOURCES = ["api.cu", "quantize.cu", "quantize_rows.cu", "wgrad.cu", "wgrad_balanced.cu", "wgrad_noalloc.cu", "grouped_mm.cu", "dgrad.cu", "dgrad_pair.cu",
            "route.cu", "dispatch.cu", "combine.cu", "grouped_act.cu", "act_backward.cu",
-           "lora.cu", "lora_grad.cu", "grad_norm.cu"]
+           "lora.cu", "lora_few.cu", "lora_grad.cu", "grad_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-Xptxas", "-v"]

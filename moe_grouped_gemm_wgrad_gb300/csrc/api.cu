@@ -904,14 +904,19 @@ mgw_status lora_launch(const void* in, int in_rows, const int32_t* in_index, int
                        void* stream) {
   mgw::LoraArgs a;
   std::memset(&a, 0, sizeof(a));
+  const bool few = !transposed && M <= mgw::kFewRows;
   const uint32_t rp = static_cast<uint32_t>((R + 15) & ~15);
-  const bool ok = rows_map(&a.tm_x, in, K, in_rows, 128) &&
-                  (transposed ? stack_map(&a.tm_w1, w1, R, K, E, 64) && stack_map(&a.tm_w2, w2, N, R, E, rp)
-                              : stack_map(&a.tm_w1, w1, K, R, E, rp) && stack_map(&a.tm_w2, w2, R, N, E, 64)) &&
-                  (!base || rows_map(&a.tm_base, base, N, out_rows, 128)) &&
-                  (!out || rows_map(&a.tm_out, out, N, out_rows, 32));
-  if (!ok) return MGW_ERR_CUDA;
+  if (!few) {
+    const bool ok =
+        rows_map(&a.tm_x, in, K, in_rows, 128) &&
+        (transposed ? stack_map(&a.tm_w1, w1, R, K, E, 64) && stack_map(&a.tm_w2, w2, N, R, E, rp)
+                    : stack_map(&a.tm_w1, w1, K, R, E, rp) && stack_map(&a.tm_w2, w2, R, N, E, 64)) &&
+        (!base || rows_map(&a.tm_base, base, N, out_rows, 128)) && (!out || rows_map(&a.tm_out, out, N, out_rows, 32));
+    if (!ok) return MGW_ERR_CUDA;
+  }
   a.in = in;
+  a.w1 = w1;
+  a.w2 = w2;
   a.off = off;
   a.in_index = in_index;
   a.out_index = out_index;
@@ -931,7 +936,8 @@ mgw_status lora_launch(const void* in, int in_rows, const int32_t* in_index, int
   a.out_rows = out_rows;
   a.max_cluster = test_max_cluster();
   a.status = status;
-  const cudaError_t err = mgw::launch_lora(a, transposed, num_sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = few ? mgw::launch_lora_few(a, static_cast<cudaStream_t>(stream))
+                              : mgw::launch_lora(a, transposed, num_sms, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
 }
 

@@ -220,6 +220,8 @@ struct LoraArgs {
   CUtensorMap tm_out;  // out bf16 [out_rows, N], box 64 columns x 32 rows (when given)
   const int32_t* off;        // [E + 1], off[E] <= M: rows behind it have no adapter
   const void* in;
+  const void* w1;
+  const void* w2;
   const int32_t* in_index;   // [M] or null: row r reads row in_index[r] of in
   const int32_t* out_index;  // [M] or null: row r is row out_index[r] of base and out
   const float* scale;        // [E] or null
@@ -238,6 +240,9 @@ struct LoraArgs {
   int* status;
 };
 cudaError_t launch_lora(const LoraArgs& a, bool transposed, int num_sms, cudaStream_t stream);
+// The forward call for few rows (lora_few.cu); uses none of the maps.
+constexpr int kFewRows = 256;
+cudaError_t launch_lora_few(const LoraArgs& a, cudaStream_t stream);
 
 // Gradients of the adapters (lora_grad.cu): grad = X^T Q over the rows of every adapter.
 struct LoraGradJob {
