@@ -16,8 +16,8 @@
 //
 // Both halves stream through one ring of shared-memory slots: 64 columns of 128 rows (the input's,
 // then the base's, which become the output's in place) and the weight's tile that goes with them.
-// Roles (320 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-9 are two sets, each a warp
-// to a TMEM lane quarter.  They copy the input's rows where these are few or lie apart (16 bytes a
+// Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-5 (where one CTA fills an SM, 6-9 too, a
+// second set) have a TMEM lane quarter each.  They copy the input's rows where these are few or lie apart (16 bytes a
 // lane; gathered by TMA, four rows an instruction, 65536 rows took 1.5 times as long), turn the
 // partial sums into the intermediate, and take the output's tiles in turns: accumulator + base, rounded
 // once, stored by TMA, or as whole 128-byte row pieces where rows lie apart.
@@ -32,8 +32,6 @@ namespace {
 
 using namespace lora;
 
-constexpr int kThreads = 320;
-constexpr int kBound = 384;           // registers are given out to four warps at a time
 constexpr int kRows = 128;
 constexpr int kBk = 64;               // columns per slot, of the input and of the output
 constexpr int kXBytes = kRows * 128;  // 128 rows of 64 bf16
@@ -41,7 +39,13 @@ constexpr int kMaxSlots = 12;
 constexpr int kBufs = 4;              // accumulators of 64 columns
 constexpr uint32_t kTmemCols = 256;   // those; before them the partial sums
 constexpr int kBars = 4 * kMaxSlots + 1 + 2 * kBufs + 1;
-constexpr int kTmpBytes = 80;         // find_tile's 18 ints; then [4] TMEM [5] abort
+constexpr int kTmpBytes = 80;         // find_tile's ints (18 at most); then [4] TMEM [5] abort
+
+// Epilogue sets of four warps: two where one CTA fills an SM, one where two CTAs share it.  (Two CTAs of
+// two sets have 80 registers a thread; what did not fit, which no L1 holds beside this much shared
+// memory, made the output's half 1.6 times as long.)  Registers are given out to four warps at a time.
+constexpr int threads_of(int sets) { return 64 + 128 * sets; }
+constexpr int bound_of(int sets) { return (threads_of(sets) + 127) / 128 * 128; }
 
 // RQ: the rank, rounded up to 32, 64 or 128.  The intermediate's two parts are 2 RQ columns, in
 // 64-wide tiles.  The ring's slots are as large as the tile's rows and the rank need, so that few rows
@@ -81,10 +85,10 @@ struct Turn {
   }
 };
 
-template <bool TRANS, int RQ>
-__global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+template <bool TRANS, int RQ, int SETS>
+__global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel(const __grid_constant__ LoraArgs a) {
   using P = Plan<RQ>;
-  constexpr int G = P::kChains;
+  constexpr int G = P::kChains, kThreads = threads_of(SETS);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
   const uint32_t bar_done = bar0 + 8u * (4 * kMaxSlots + 1 + 2 * kBufs);
   if (tid == 0) {
     for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(bar_full(s), in_box ? 1 : 1 + 256);
+      mbar_init(bar_full(s), in_box ? 1 : 1 + 128 * SETS);
       mbar_init(bar_empty(s), 1);
       mbar_init(bar_bfull(s), 1);
       mbar_init(bar_bempty(s), 4);
@@ -236,8 +240,9 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
       ++i;
       to.step(1, S2);
     };
+    cluster_arrive();
     while (ok && i < tiles && i < early) load_tile();
-    cluster_sync();  // partial sums are there
+    cluster_wait();  // partial sums are there
     cluster_sync();  // the intermediate is
     fence_async_all();
     while (ok && i < tiles) {
@@ -318,16 +323,17 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
     const int sub = static_cast<int>(lane >> 3), ch = static_cast<int>(lane & 7);
     const float scale = a.scale != nullptr ? a.scale[t.e] : 1.0f;
     if (!in_box) {
-      // ------------------------------------------- the input's rows: 16 a warp, eight lanes a row
+      // ------------------------------------------- the input's rows: eight lanes a row
       // Rows behind the tile's last stay as they are: whatever they hold goes into rows that nobody
       // stores.
-      const __nv_bfloat16* src[4];
-      uint32_t dst[4];
-      bool there[4];
+      constexpr int kMine = 8 / SETS;  // times four rows a warp
+      const __nv_bfloat16* src[kMine];
+      uint32_t dst[kMine];
+      bool there[kMine];
       int live = 0;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int r = 16 * ew + 4 * p + sub;
+      for (int p = 0; p < kMine; ++p) {
+        const int r = 4 * kMine * ew + 4 * p + sub;
         int o = -1;
         if (r < t.nrows)
           o = row_place(a.in_index, t.row0 + r, a.in_rows, rank == 0 && ch == 0 ? a.status : nullptr), ++live;
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
         const int col = (c0 + i) * kBk;
         const bool inside = col + 8 * ch < a.K;
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+        for (int p = 0; p < kMine; ++p)
           if (p < live) copy16(dst[p] + in.slot * slot1, src[p] + (inside ? col : -8 * ch), inside && there[p]);
         copy_arrive(bar_full(in.slot));
         in.step(1, S1);
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
       // u's block, while the products run
       if (a.qv != nullptr) {
         const int per = (q_rows - rank + C - 1) / C;
-        for (int i = tid - 64; i < per * (RP / 8); i += 256) {
+        for (int i = tid - 64; i < per * (RP / 8); i += 128 * SETS) {
           const int r = rank + C * (i % per), j8 = i / per;
           float f[8];
 #pragma unroll
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
       }
     };
     const int chains = min(G, chunks);
-    for (int j = 16 * set; j < RP; j += 32) {
+    for (int j = 16 * set; j < RP; j += 16 * SETS) {
       float v[2][8];
       uint32_t r[16];
       for (int g = 0; g < chains && ok; ++g) {
@@ -446,54 +452,62 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
     }
     // -------------------------------------- the base's rows where they are copied
     // A warp copies its own 32 rows of its set's next tiles, `ahead` of them: nobody else reads them.
-    const __nv_bfloat16* src[8];
-    const int ahead = max(1, min((S2 - 1) / 2, early / 2));
+    int place[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) place[p] = s_rows[quarter * 32 + 4 * p + sub];
+    const int ahead = max(1, min(S2 - 1, early) / SETS);
     Turn fetch = {set, 0};
     int fetched = set;
     auto fetch_base = [&]() {
       if (fetched < tiles) {
-        const int col = (nt0 + fetched) * kBk;
-        const bool inside = col + 8 * ch < N;
+        const int col = (nt0 + fetched) * kBk + 8 * ch;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
           const int r = quarter * 32 + 4 * p + sub;
+          const bool there = place[p] >= 0 && col < N;
           if (r < t.nrows)
-            copy16(sbase + fetch.slot * slot2 + swz(r, ch), src[p] == nullptr ? base : src[p] + (inside ? col : -8 * ch),
-                   inside && src[p] != nullptr);
+            copy16(sbase + fetch.slot * slot2 + swz(r, ch), base + (there ? static_cast<size_t>(place[p]) * N + col : 0),
+                   there);
         }
       }
       copy_commit();
-      fetched += 2;
-      fetch.step(2, S2);
+      fetched += SETS;
+      fetch.step(SETS, S2);
     };
-    const bool pre = early >= 2 * ahead;
-    if (copy_base) {
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int o = s_rows[quarter * 32 + 4 * p + sub];
-        src[p] = o >= 0 ? base + static_cast<size_t>(o) * N + 8 * ch : nullptr;
-      }
-      if (pre)
-        for (int k = 0; k < ahead; ++k) fetch_base();
-    }
+    const bool pre = early >= SETS * ahead;
     tc_fence_before();
     __syncwarp();
-    cluster_sync();
+    cluster_arrive();
+    if (copy_base && pre)
+      for (int k = 0; k < ahead; ++k) fetch_base();
+    __syncwarp();
+    cluster_wait();
     if (C > 1) {
       // This CTA's rows of the tile, summed over the CTAs in their order.  Rows are dealt out one by
       // one, so that few rows are many CTAs' work too.
       const int per = (q_rows - rank + C - 1) / C;
-      for (int i = tid - 64; i < per * (RP / 8); i += 256) {
+      for (int i = tid - 64; i < per * (RP / 8); i += 128 * SETS) {
         const int r = rank + C * (i % per), j8 = i / per;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         const uint32_t at = part + (2u * j8 * rows8 + r) * 16u;
-        for (int p = 0; p < C && r < t.nrows; ++p) {
-          const uint32_t from = map_to_cta(at, p);
-          const float4 x = ld_cluster_f4(from), y = ld_cluster_f4(from + rows8 * 16u);
-          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-          v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        if (r < t.nrows) {
+          for (int p = 0; p < C; p += 4) {
+            float4 x[8];  // of four CTAs at a time: a load from another SM takes a while
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t from = map_to_cta(at, min(p + k, C - 1));
+              x[2 * k] = ld_cluster_f4(from);
+              x[2 * k + 1] = ld_cluster_f4(from + rows8 * 16u);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (p + k >= C) break;
+              v[0] += x[2 * k].x, v[1] += x[2 * k].y, v[2] += x[2 * k].z, v[3] += x[2 * k].w;
+              v[4] += x[2 * k + 1].x, v[5] += x[2 * k + 1].y, v[6] += x[2 * k + 1].z, v[7] += x[2 * k + 1].w;
+            }
+          }
         }
         finish(r, j8, v);
       }
@@ -507,8 +521,9 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
     // A lane has a row: 64 columns of accumulators plus its base, in place in the slot.
     const bool by_tma = out_box && quarter * 32 + 32 <= t.nrows;
     const bool mine = row < rows8;
+    int pend = -1;
     Turn to = {set, 0}, acc = {set, 0};
-    for (int i = set; ok && i < tiles; i += 2) {
+    for (int i = set; ok && i < tiles; i += SETS) {
       const uint32_t tile = sbase + to.slot * slot2;
       ok = wait_all(bar_bfull(to.slot), to.phase, abort_flag) && wait_all(bar_acc(acc.slot), acc.phase, abort_flag);
       if (!ok) break;
@@ -550,19 +565,29 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
       if (lane == 0) mbar_arrive(bar_free(acc.slot));
       if (by_tma) {
         if (lane == 0) {
+          if (pend >= 0) {
+            bulk_wait_read0();  // this warp's tile before has left its slot
+            mbar_arrive(bar_bempty(pend));
+          }
           tma_store_2d(&a.tm_out, (nt0 + i) * kBk, t.row0 + quarter * 32, tile + quarter * 4096u);
           bulk_commit();
-          bulk_wait_read0();  // it has left the slot; the other set works meanwhile
-          mbar_arrive(bar_bempty(to.slot));
+          pend = to.slot;
         }
       } else {
         const int col = (nt0 + i) * kBk + 8 * ch;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const int q = quarter * 32 + 4 * p + sub;
-          const int o = q < t.nrows && col < N ? s_rows[q] : -1;
-          if (o >= 0)
-            *reinterpret_cast<uint4*>(out + static_cast<size_t>(o) * N + col) = ld_shared_u4(tile + swz(q, ch));
+        for (int h = 0; h < 2; ++h) {
+          uint4 v[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int q = quarter * 32 + 16 * h + 4 * p + sub;
+            if (q < t.nrows) v[p] = ld_shared_u4(tile + swz(q, ch));
+          }
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int o = place[4 * h + p];
+            if (o >= 0 && col < N) *reinterpret_cast<uint4*>(out + static_cast<size_t>(o) * N + col) = v[p];
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_bempty(to.slot));
@@ -572,9 +597,10 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
         if (fetched < tiles && fetched >= S2) ok = wait_all(bar_bempty(fetch.slot), fetch.phase ^ 1u, abort_flag);
         fetch_base();
       }
-      to.step(2, S2);
-      acc.step(2, kBufs);
+      to.step(SETS, S2);
+      acc.step(SETS, kBufs);
     }
+    if (by_tma && lane == 0) bulk_wait_read0();
     copy_wait<0>();
     if (!ok && lane == 0) give_up(abort_flag, a.status);
   }
@@ -584,16 +610,16 @@ __global__ void __launch_bounds__(kBound, RQ == 128 ? 1 : 2) lora_kernel(const _
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool TRANS, int RQ>
+template <bool TRANS, int RQ, int SETS>
 cudaError_t set_smem() {
   static thread_local uint64_t attr_ctx = 0;
-  return set_smem_attr_once(reinterpret_cast<const void*>(lora_kernel<TRANS, RQ>), 227 * 1024, &attr_ctx);
+  return set_smem_attr_once(reinterpret_cast<const void*>(lora_kernel<TRANS, RQ, SETS>), 227 * 1024, &attr_ctx);
 }
 
-cudaLaunchConfig_t config(int cluster, long long tiles, size_t smem, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t config(int sets, int cluster, long long tiles, size_t smem, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(sets)));
   cfg.dynamicSmemBytes = smem;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -605,56 +631,60 @@ cudaLaunchConfig_t config(int cluster, long long tiles, size_t smem, cudaLaunchA
 }
 
 constexpr int kMaxCluster = 8;
-// A kernel that needs as much of an SM as lora_kernel does, but for tensor memory: for kernels that
-// allocate that, the occupancy calculation answers one CTA an SM, though two (256 columns each) run.
-__global__ void __launch_bounds__(kBound, 2) lora_room_kernel() {}
-
-// Clusters of c CTAs, with the short or the long ring, that the current context runs at once (none
-// where it has a share of the SMs that is too small).  Asked once per context and thread.
-template <int RQ>
-long long clusters_at_once(int c, bool longer) {
+// Clusters of c CTAs, one to an SM, that the current context runs at once (none where it has a share of
+// the SMs that is too small).  Asked once per context and thread.
+template <bool TRANS, int RQ>
+long long clusters_at_once(int c) {
   using P = Plan<RQ>;
   static thread_local uint64_t asked_ctx = 0;
-  static thread_local int active[2][kMaxCluster + 1];
+  static thread_local int active[kMaxCluster + 1];
   if (asked_ctx == 0 || asked_ctx != current_context_id()) {
-    static thread_local uint64_t attr_ctx = 0;
-    if (set_smem_attr_once(reinterpret_cast<const void*>(lora_room_kernel), 227 * 1024, &attr_ctx) != cudaSuccess)
-      return 0;
-    for (int l = 0; l < 2; ++l)
-      for (int k = 2; k <= kMaxCluster; ++k) {
-        cudaLaunchAttribute attr = {};
-        const cudaLaunchConfig_t cfg = config(k, 1, P::smem(l ? P::kLong : P::kShort), &attr);
-        if (cudaOccupancyMaxActiveClusters(&active[l][k], lora_room_kernel, &cfg) != cudaSuccess) {
-          (void)cudaGetLastError();  // a size that does not fit is no error of the call
-          active[l][k] = 0;
-        }
+    for (int k = 2; k <= kMaxCluster; ++k) {
+      cudaLaunchAttribute attr = {};
+      const cudaLaunchConfig_t cfg = config(2, k, 1, P::smem(P::kLong), &attr);
+      if (cudaOccupancyMaxActiveClusters(&active[k], lora_kernel<TRANS, RQ, 2>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();  // a size that does not fit is no error of the call
+        active[k] = 0;
       }
+    }
     asked_ctx = current_context_id();
   }
-  return active[longer][c];
+  return active[c];
+}
+
+template <bool TRANS, int RQ, int SETS>
+cudaError_t launch_sets(LoraArgs a, int cluster, long long tiles, cudaStream_t stream) {
+  using P = Plan<RQ>;
+  const cudaError_t err = set_smem<TRANS, RQ, SETS>();
+  if (err != cudaSuccess) return err;
+  a.cluster = cluster;
+  a.ring = SETS == 2 ? P::kLong : P::kShort;
+  cudaLaunchAttribute attr = {};
+  cudaLaunchConfig_t cfg = config(SETS, cluster, tiles, P::smem(a.ring), &attr);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, lora_kernel<TRANS, RQ, SETS>, a);
 }
 
 template <bool TRANS, int RQ>
-cudaError_t launch(LoraArgs a, int num_sms, cudaStream_t stream) {
-  using P = Plan<RQ>;
-  cudaError_t err = set_smem<TRANS, RQ>();
+cudaError_t launch(const LoraArgs& a, int num_sms, cudaStream_t stream) {
+  cudaError_t err = set_smem<TRANS, RQ, 2>();
   if (err != cudaSuccess) return err;
-  // The exact number of tiles is known on the device only: at most this many, and one more of rows
-  // without an adapter.
-  const long long tiles = (a.M + kRows - 1) / kRows + (a.M < a.E ? a.M : a.E);
-  // As many CTAs to a tile, each with some columns of its own, as run at once: a cluster that waits
-  // for another one's end costs as much again.
+  // The exact number of tiles is known on the device only: at most this many, one more for rows without
+  // an adapter included; about half a tile of each adapter's is empty.
+  const long long some = a.M < a.E ? a.M : a.E;
+  const long long tiles = (a.M + kRows - 1) / kRows + some + 1;
+  const long long likely = (a.M + kRows - 1) / kRows + some / 2;
+  // Where the tiles leave SMs idle: as many CTAs to a tile, each with some columns of its own, as run at
+  // once (a cluster that waits for another one's end costs as much again).
   const int nch = (a.K + kBk - 1) / kBk;
   const int most = a.max_cluster > 0 && a.max_cluster < kMaxCluster ? a.max_cluster : kMaxCluster;
   int c = 1;
   for (int k = 2; k <= most && k <= nch; ++k)
-    if (tiles <= clusters_at_once<RQ>(k, false)) c = k;
-  a.cluster = c;
-  a.ring = (c == 1 ? tiles <= num_sms : tiles <= clusters_at_once<RQ>(c, true)) ? P::kLong : P::kShort;
-  cudaLaunchAttribute attr = {};
-  cudaLaunchConfig_t cfg = config(c, tiles + 1, P::smem(a.ring), &attr);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<TRANS, RQ>, a);
+    if (likely <= clusters_at_once<TRANS, RQ>(k)) c = k;
+  // More tiles than SMs: two CTAs to an SM, one's loads under the other's exchange.
+  if constexpr (RQ < 128)
+    if (likely > num_sms) return launch_sets<TRANS, RQ, 1>(a, 1, tiles, stream);
+  return launch_sets<TRANS, RQ, 2>(a, c, tiles, stream);
 }
 
 template <bool TRANS>
