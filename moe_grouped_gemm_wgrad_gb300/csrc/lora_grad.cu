@@ -238,28 +238,38 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     const bool there = col < cols;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(job.x) + (there ? col : 0);
     bool ok = true;
-    int i = 0;
+    int stage = 0;
+    uint32_t phase = 0;
     while (ok && w.next(t0, t1, E)) {
-      // the place of this lane's token of the next block, loaded a block ahead
+      // this lane's token of a block: its row of X, loaded a block ahead and looked at when it is needed
       auto place_of = [&](int b) {
         const int r = b * kTok + q0 + static_cast<int>(lane & 15u);
-        return r < w.n ? row_place(job.index, w.lo + r, job.rows, lane < 16 && f0 == 0 ? a.status : nullptr) : -1;
+        return r < w.n ? (job.index != nullptr ? job.index[w.lo + r] : w.lo + r) : -1;
       };
-      int ahead = in_box(w.n - w.b0 * kTok) ? -1 : place_of(w.b0);
-      for (int b = w.b0; b < w.b1; ++b, ++i) {
-        const int left = w.n - b * kTok, place = ahead;
-        if (b + 1 < w.b1 && !in_box(left - kTok)) ahead = place_of(b + 1);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_empty(i % S), ((i / S) & 1) ^ 1u, abort_flag));
+      int ahead = place_of(w.b0);
+      for (int b = w.b0; b < w.b1; ++b) {
+        const int left = w.n - b * kTok;
+        int place = ahead;
+        ahead = place_of(b + 1);
+        if (q0 + static_cast<int>(lane & 15u) < left && (place < 0 || place >= job.rows)) {
+          if (a.status != nullptr && lane < 16 && f0 == 0) atomicOr(a.status, kDevBadIndex);
+          place = -1;
+        }
+        ok = wait_all(bar_empty(stage), phase ^ 1u, abort_flag);
         if (!ok) break;
         if (!in_box(left)) {
-          const uint32_t sx = sbase + (i % S) * stage_bytes(RP) + part;
-          const int rows = min(16, ((min(left, kTok) + 15) & ~15) - q0);  // those that the MMAs read
-          for (int p = 0; p < rows; ++p) {
-            const int o = __shfl_sync(0xffffffffu, place, p);
-            copy16(sx + swz(q0 + p, ch), x + static_cast<size_t>(max(o, 0)) * cols, there && o >= 0);
+          const uint32_t sx = sbase + stage * stage_bytes(RP) + part;
+          const int rows = ((min(left, kTok) + 15) & ~15) - q0;  // those that the MMAs read
+          if (rows > 0) {
+#pragma unroll
+            for (int p = 0; p < 16; ++p) {
+              const int o = __shfl_sync(0xffffffffu, place, p);
+              copy16(sx + swz(q0 + p, ch), x + static_cast<size_t>(max(o, 0)) * cols, there && o >= 0);
+            }
           }
         }
-        copy_arrive(bar_full(i % S));
+        copy_arrive(bar_full(stage));
+        if (++stage == S) stage = 0, phase ^= 1u;
       }
     }
     copy_wait<0>();
@@ -360,12 +370,15 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     const int g0 = kWidth * k / count, per = kWidth * (k + 1) / count - g0;
     for (int i = tid; i < per * (RP / 4); i += kThreads) {
       const int f = g0 + i % per, j4 = i / per;
+      // every CTA's sums at once: a load in turn for each took longer than the rest of the sum
+      float4 x[kMaxCluster];
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if ((with >> p) & 1u) x[p] = __ldcg(partial(p, v.at < share(blocks, p, C) ? 0 : 1) + j4 * kWidth + f);
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (uint32_t m = with; m != 0; m &= m - 1) {
-        const int p = __ffs(m) - 1;
-        const float4 x = __ldcg(partial(p, v.at < share(blocks, p, C) ? 0 : 1) + j4 * kWidth + f);
-        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-      }
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if ((with >> p) & 1u) s.x += x[p].x, s.y += x[p].y, s.z += x[p].z, s.w += x[p].w;
       store4(v.e, f, 4 * j4, s);
     }
   }
