@@ -32,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 16384;                // bytes
 constexpr int kVecs = kChunk / 16 / kThreads;  // 16-byte pieces a thread has of a chunk
 constexpr int kCtasPerSm = 4;
-constexpr int kSmallTable = 96, kLargeTable = 1024;  // tensors of a launch
+constexpr int kSmallTable = 128, kLargeTable = 1024;  // tensors of a launch
 constexpr int kMostSms = 160;  // that a launch is sized for
 
 struct Entry {
@@ -144,17 +144,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_norm_kernel(const _
       rest += again();
     }
   };
+  // The next chunk's loads are on their way while a chunk is summed.
   int i = c0 < c1 ? locate(a, c0) : 0;
-  for (int c = c0; c < c1; ++c) {
+  Piece p = {}, next = {};
+  uint4 w[kVecs], ahead[kVecs];
+  auto fetch = [&](int c) {
     while (c >= a.first[i + 1]) ++i;
-    const Piece p = piece_of(a, i, c);
-    const uint4* v = reinterpret_cast<const uint4*>(p.g + p.skip);
-    uint4 w[kVecs];
+    next = piece_of(a, i, c);
+    const uint4* v = reinterpret_cast<const uint4*>(next.g + next.skip);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      const int64_t at = p.lo / 16 + threadIdx.x + k * kThreads;
-      w[k] = at < p.hi / 16 ? __ldg(v + at) : make_uint4(0u, 0u, 0u, 0u);
+      const int64_t at = next.lo / 16 + threadIdx.x + k * kThreads;
+      ahead[k] = at < next.hi / 16 ? __ldg(v + at) : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+  if (c0 < c1) fetch(c0);
+  for (int c = c0; c < c1; ++c) {
+    p = next;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) w[k] = ahead[k];
+    if (c + 1 < c1) fetch(c + 1);
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t any = 0u;
 #pragma unroll

@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(s_tmp[4]);
   bool ok = true;
+  // the gradients' launch may start as soon as it finds room; it waits for this one's blocks itself
+  if constexpr (TRANS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer

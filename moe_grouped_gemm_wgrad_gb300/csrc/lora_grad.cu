@@ -49,6 +49,9 @@ constexpr int stages_of(int RP) {
 static_assert(stages_of(128) == 3 && stages_of(64) == 4 && stages_of(16) == 6, "ring");
 constexpr size_t part_floats(int RP) { return static_cast<size_t>(kWidth) * RP; }
 
+// The data gradient's launch has ended and its results are there.
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The share of the token blocks of CTA p of C.
 __device__ __forceinline__ int share(int blocks, int p, int C) {
   return static_cast<int>(static_cast<long long>(blocks) * p / C);
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
   if (lane == 0) atomicAdd(&s_misc[2], mine);
   if (__syncthreads_or(bad)) {
     if (tid == 0 && a.status != nullptr) atomicOr(a.status, kDevBadOffsets);
+    wait_for_launch_before();
     return;
   }
   const int blocks = s_misc[2];
@@ -165,11 +169,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
           const bool box = in_box(w.n - b * kTok);
           const uint32_t fb = bar_full(stage), sx = sbase + stage * stage_bytes(RP), q_bytes = 256u * RP;
           mbar_arrive_expect_tx(fb, (box ? static_cast<uint32_t>(kXBytes) : 0u) + q_bytes);
-          bulk_load(sx + kXBytes, job.q + (2ll * w.pad + b) * q_bytes, q_bytes, fb);
           if (box) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) tma_load_2d(sx + k * 8192, &job.tm, f0 + 64 * k, w.lo + b * kTok, fb);
           }
+          // Q comes from the launch before, X does not
+          if (filled == 0) wait_for_launch_before();
+          bulk_load(sx + kXBytes, job.q + (2ll * w.pad + b) * q_bytes, q_bytes, fb);
         }
         __syncwarp();
         ++filled;
@@ -348,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
         store4(e, i % kWidth, i / kWidth * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
     }
   }
+  wait_for_launch_before();  // also where this CTA had no rows: the stream goes on behind this launch
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -394,12 +401,15 @@ cudaLaunchConfig_t config(int cluster, long long items, size_t smem, cudaLaunchA
   cfg.gridDim = dim3(static_cast<unsigned>(items * cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // starts while the data gradient's launch ends (programmatic dependent launch)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -410,8 +420,8 @@ int clusters_at_once(int c) {
   static thread_local int active[kMaxCluster + 1];
   if (asked_ctx == 0 || asked_ctx != current_context_id()) {
     for (int k = 2; k <= kMaxCluster; ++k) {
-      cudaLaunchAttribute attr = {};
-      const cudaLaunchConfig_t cfg = config(k, 1, 227 * 1024, &attr);
+      cudaLaunchAttribute attr[2] = {};
+      const cudaLaunchConfig_t cfg = config(k, 1, 227 * 1024, attr);
       if (cudaOccupancyMaxActiveClusters(&active[k], lora_grad_kernel, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();  // a size that does not fit is no error of the call
         active[k] = 0;
@@ -450,10 +460,11 @@ cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream) {
   for (int k = 2; k <= most; ++k)
     if (items * k <= kSms && static_cast<long long>(k) * kTok <= a.M && items <= clusters_at_once(k)) c = k;
   a.cluster = c;
-  cudaLaunchAttribute attr = {};
+  cudaLaunchAttribute attr[2] = {};
   cudaLaunchConfig_t cfg =
-      config(c, items, static_cast<size_t>(a.stages) * stage_bytes(RP) + misc_bytes(a.E), &attr);
+      config(c, items, static_cast<size_t>(a.stages) * stage_bytes(RP) + misc_bytes(a.E), attr);
   cfg.stream = stream;
+  if (a.M == 0) cfg.numAttrs = 1;  // there was no launch before
   return cudaLaunchKernelEx(&cfg, lora_grad_kernel, a);
 }
 
