@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 import threading
 
@@ -905,286 +906,15 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: tor
     return dy, dweights
 
 
-# ------------------------------------------------------------------- low-rank adapters
-def _fit(dev: int, *specs) -> bool:
-    """All (tensor, dtype, shape) but None are contiguous, of that type and shape, on CUDA device
-    ``dev``: the usual call's check in one pass (4 us less for ten tensors).  Whoever gets False goes
-    through the single checks, which say what is wrong."""
-    for t, dtype, shape in specs:
-        if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.shape == shape
-                                  and t.is_contiguous()):
-            return False
-    return True
+# ------------------------------------------------------------- operators in modules of their own
+_ELSEWHERE = {"grouped_lora": "adapters", "grouped_lora_backward": "adapters",
+              "GradTable": "gradients", "grad_norm": "gradients", "clip_grads": "gradients"}
 
 
-def _adapters(a, b, adapter_off, scale, row_index, out_index):
-    """Checks the adapters and the row tables; returns (E, R, K, N)."""
-    _dev_tensor(a, torch.bfloat16, "a", 3)
-    E, R, K = a.shape
-    _dev_tensor(b, torch.bfloat16, "b", 3)
-    N = b.shape[1]
-    _shaped(b, (E, N, R), torch.bfloat16, "b")
-    _dev_tensor(adapter_off, torch.int32, "adapter_off", 1)
-    if adapter_off.numel() != E + 1:
-        raise MgwError(f"adapter_off has {adapter_off.numel()} entries; {E} adapters need {E + 1}")
-    if scale is not None:
-        _shaped(scale, (E,), torch.float32, "scale")
-    if row_index is not None:
-        _dev_tensor(row_index, torch.int32, "row_index", 1)
-    if out_index is not None:
-        _dev_tensor(out_index, torch.int32, "out_index", 1)
-        if row_index is not None and row_index.numel() != out_index.numel():
-            raise MgwError(f"row_index and out_index name {row_index.numel()} and {out_index.numel()} rows")
-    return E, R, K, N
-
-
-def _adapter_rows(x_rows: int, rows: int | None, row_index, out_index, of: str) -> tuple[int, int]:
-    """(M, the rows of ``of``): as many rows as an index names, or as x has; ``rows`` None: M."""
-    index = row_index if row_index is not None else out_index
-    M = x_rows if index is None else index.numel()
-    rows = M if rows is None else rows
-    if (row_index is None and x_rows < M) or (out_index is None and rows < M):
-        raise MgwError(f"{M} rows need an index, or as many rows of x ({x_rows}) and of {of} ({rows})")
-    if max(x_rows, rows, M) > MAX_SIZE:
-        raise MgwError("a number of rows exceeds the C ABI's 32-bit sizes")
-    return M, rows
-
-
-def _lora_fit(x, a, b, adapter_off, row_index, out_index, scale, base) -> bool:
-    try:
-        E, R, K = a.shape
-        N, index = b.shape[1], row_index if row_index is not None else out_index
-        return x.get_device() >= 0 and _fit(
-            x.get_device(), (x, torch.bfloat16, (x.shape[0], K)), (a, torch.bfloat16, (E, R, K)),
-            (b, torch.bfloat16, (E, N, R)), (adapter_off, torch.int32, (E + 1,)),
-            (row_index, torch.int32, None if index is None else index.shape),
-            (out_index, torch.int32, None if index is None else index.shape), (scale, torch.float32, (E,)),
-            (base, torch.bfloat16, None if base is None else (base.shape[0], N))) \
-            and (index is None or index.dim() == 1) and E * R * K <= MAX_SIZE and E * N * R <= MAX_SIZE
-    except (AttributeError, IndexError, TypeError, ValueError):
-        return False
-
-
-def grouped_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_off: torch.Tensor,
-                 row_index: torch.Tensor | None = None, out_index: torch.Tensor | None = None,
-                 scale: torch.Tensor | None = None, base: torch.Tensor | None = None,
-                 save_u: bool = False, out: torch.Tensor | None = None, u: torch.Tensor | None = None,
-                 status: torch.Tensor | None = None, stream=None):
-    """out[o] = base[o] + scale[e] * (x[t] a[e]^T) b[e]^T for every row of every adapter, x [rows, K]
-    bf16, a [E, R, K], b [E, N, R] -> out [rows of base, N] bf16; with ``save_u`` (or ``u``) also the
-    intermediate u = x a^T, fp32 [M, R], for :func:`grouped_lora_backward`.
-
-    Adapter e has the rows adapter_off[e] .. adapter_off[e+1]-1; row r reads x[row_index[r]] and is
-    out's row out_index[r] (r itself without an index).  Rows behind adapter_off[E] have no adapter
-    and keep their base.  For requests in token order both indices are the row_index of
-    :func:`moe_dispatch` (top_k 1; an extra last expert for tokens without an adapter, whose offset
-    is left out of ``adapter_off``).  ``base`` is 0 when not given, and may be ``out``.  Rows of out
-    that ``out_index`` does not name are not written."""
-    fit = _lora_fit(x, a, b, adapter_off, row_index, out_index, scale, base)
-    if not fit:
-        _dev_tensor(x, torch.bfloat16, "x", 2)
-        K = _adapters(a, b, adapter_off, scale, row_index, out_index)[2]
-        if x.shape[1] != K:
-            raise MgwError(f"x [rows, {x.shape[1]}] and a [E, R, {K}] must share the contraction width")
-        if base is not None:
-            _dev_tensor(base, torch.bfloat16, "base", 2)
-            _shaped(base, (base.shape[0], b.shape[1]), torch.bfloat16, "base")
-    E, R, K = a.shape
-    N = b.shape[1]
-    rows = None
-    if base is not None:
-        rows = base.shape[0]
-    elif isinstance(out, torch.Tensor) and out.dim() == 2:
-        rows = out.shape[0]
-    M, rows = _adapter_rows(x.shape[0], rows, row_index, out_index, "out")
-    _status(status)
-    dev = _one_device(x, out, u, status) if fit else \
-        _one_device(x, a, b, adapter_off, row_index, out_index, scale, base, out, u, status)
-    side = None if stream is None else _side(stream, dev)
-    out = _out(out, (rows, N), torch.bfloat16, dev, "out", side)
-    if save_u or u is not None:
-        u = _out(u, (M, R), torch.float32, dev, "u", side)
-    with _device(dev):
-        st = load().mgw_grouped_lora(x.data_ptr(), x.shape[0], _ptr(row_index), M, K, a.data_ptr(),
-                                     b.data_ptr(), _ptr(scale), adapter_off.data_ptr(), E, R, N,
-                                     _ptr(base), _ptr(out_index), rows, out.data_ptr(), _ptr(u),
-                                     _ptr(status), _stream(stream))
-    if st:
-        _check(st, "mgw_grouped_lora")
-    if side is not None:
-        _used_on(side, x, a, b, adapter_off, row_index, out_index, scale, base, out, u, status)
-    return out if u is None else (out, u)
-
-
-def grouped_lora_backward(dy: torch.Tensor, x: torch.Tensor | None, u: torch.Tensor | None,
-                          a: torch.Tensor, b: torch.Tensor, adapter_off: torch.Tensor,
-                          row_index: torch.Tensor | None = None, out_index: torch.Tensor | None = None,
-                          scale: torch.Tensor | None = None, dx_base: torch.Tensor | None = None,
-                          with_dx: bool = True, with_weights: bool = True,
-                          dx: torch.Tensor | None = None, da: torch.Tensor | None = None,
-                          db: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                          status: torch.Tensor | None = None, stream=None):
-    """-> (dx, da, db): the backward pass of :func:`grouped_lora` from dy [rows of out, N] bf16.
-    dx [rows of out, K] bf16 = dx_base + the adapters' share (rows without an adapter: dx_base, 0
-    when not given; ``dx_base`` may be ``dx``), da [E, R, K] and db [E, N, R] bf16; ``x`` and ``u``
-    as in the forward call.  Without ``with_dx`` dx is None; without ``with_weights`` da and db are,
-    and ``x`` and ``u`` may be None.  ``workspace`` (uint8) is allocated when none is given."""
-    if not with_dx and (dx is not None or dx_base is not None):
-        raise MgwError("dx and dx_base need with_dx")
-    if not with_weights and (da is not None or db is not None):
-        raise MgwError("da and db need with_weights")
-    if with_weights and (x is None or u is None):
-        raise MgwError("x and u are needed for the adapters' gradients")
-    if not with_weights:
-        x = u = None
-    fit = with_weights and _lora_fit(x, a, b, adapter_off, row_index, out_index, scale, dy)
-    if not fit:
-        _dev_tensor(dy, torch.bfloat16, "dy", 2)
-        _, _, K, N = _adapters(a, b, adapter_off, scale, row_index, out_index)
-        if dy.shape[1] != N:
-            raise MgwError(f"dy [rows, {dy.shape[1]}] does not match b [E, {N}, R]")
-        if x is not None:
-            _dev_tensor(x, torch.bfloat16, "x", 2)
-            if x.shape[1] != K:
-                raise MgwError(f"x [rows, {x.shape[1]}] and a [E, R, {K}] must share the contraction width")
-    E, R, K = a.shape
-    N = b.shape[1]
-    x_rows = dy.shape[0] if x is None else x.shape[0]
-    M, rows = _adapter_rows(x_rows, dy.shape[0], row_index, out_index, "dy")
-    if u is not None:
-        _shaped(u, (M, R), torch.float32, "u")
-    if dx_base is not None:
-        _shaped(dx_base, (rows, K), torch.bfloat16, "dx_base")
-    _status(status)
-    dev = _one_device(dy, u, dx_base, dx, da, db, workspace, status) if fit else \
-        _one_device(dy, x, u, a, b, adapter_off, row_index, out_index, scale, dx_base, dx, da, db,
-                    workspace, status)
-    side = None if stream is None else _side(stream, dev)
-    lib = load()
-    if with_dx:
-        dx = _out(dx, (rows, K), torch.bfloat16, dev, "dx", side)
-    if with_weights:
-        da = _out(da, (E, R, K), torch.bfloat16, dev, "da", side)
-        db = _out(db, (E, N, R), torch.bfloat16, dev, "db", side)
-        need = int(lib.mgw_grouped_lora_backward_workspace_bytes(E, M, K, N, R))
-        workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side)
-    with _device(dev):
-        st = lib.mgw_grouped_lora_backward(dy.data_ptr(), rows, _ptr(out_index), _ptr(x), x_rows,
-                                           _ptr(row_index), M, K, a.data_ptr(), b.data_ptr(),
-                                           _ptr(scale), adapter_off.data_ptr(), E, R, N, _ptr(u),
-                                           _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db),
-                                           _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                           _ptr(status), _stream(stream))
-    if st:
-        _check(st, "mgw_grouped_lora_backward")
-    if side is not None:
-        _used_on(side, dy, x, u, a, b, adapter_off, row_index, out_index, scale, dx_base, dx, da, db,
-                 workspace, status)
-    return dx, da, db
-
-
-# ------------------------------------------------------------------- gradient norm and clipping
-class GradTable:
-    """The gradients (bf16 and fp32 tensors, any sizes, contiguous, on one device) that
-    :func:`grad_norm` and :func:`clip_grads` take, checked once: for a program whose gradient buffers
-    stay where they are from step to step, and for captured calls.  ``out``: tensors of the same
-    types and sizes that the clipped gradients go to, the gradients themselves or memory that
-    overlaps none of the call's tensors (without it: in place).  Holds the tensors."""
-
-    def __init__(self, grads, out=None):
-        self.grads = list(grads)
-        self.out = None if out is None else list(out)
-        self.device, self._kinds, sizes = self._checked(self.grads, "grads")
-        n = self.n = len(self.grads)
-        at = [t.data_ptr() for t in self.grads]
-        self._grads = (ctypes.c_void_p * n)(*at)
-        self._sizes = (ctypes.c_int64 * n)(*sizes)
-        self._dtypes = (ctypes.c_int * n)(*self._kinds)
-        self._out = None
-        if self.out is not None:
-            dev, kinds, out_sizes = self._checked(self.out, "out")
-            if kinds != self._kinds or out_sizes != sizes or (n and dev != self.device):
-                raise MgwError("out must hold one tensor of the same type, size and device for every gradient")
-            at = [t.data_ptr() for t in self.out]
-            self._out = (ctypes.c_void_p * n)(*at)
-        used = [p for p, s in zip(at, sizes) if s]
-        self._twice = len(set(used)) != len(used)
-
-    @staticmethod
-    def _checked(ts, name):
-        dev, kinds, sizes = None, [], []
-        for t in ts:
-            kinds.append(_element_type(t, name))
-            if not _on_cuda(t):
-                raise MgwError(f"{name} must be CUDA tensors")
-            if not t.is_contiguous():
-                raise MgwError(f"{name} must be contiguous")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise MgwError(f"all tensors must be on one CUDA device, got {dev} and {t.device} in {name}")
-            sizes.append(t.numel())
-        return dev, kinds, sizes
-
-
-def _grad_call(grads, norm, workspace, stream):
-    """The table of ``grads`` and the checked or new buffers -> (table, device, side, norm, workspace)."""
-    table = grads if isinstance(grads, GradTable) else GradTable(grads)
-    dev = table.device
-    if dev is None:  # no gradients at all
-        dev = torch.device("cuda", torch.cuda.current_device())
-    if norm is not None:
-        _dev_tensor(norm, torch.float32, "norm")
-        _need(norm, 1, "norm")
-    if workspace is not None:
-        _dev_tensor(workspace, torch.uint8, "workspace")
-    for t in (norm, workspace):
-        if t is not None and t.device != dev:
-            raise MgwError(f"all tensors must be on one CUDA device, got {sorted({str(dev), str(t.device)})}")
-    side = None if stream is None else _side(stream, dev)
-    need = int(load().mgw_grad_workspace_bytes(_size(table.n, "the number of gradients")))
-    workspace = _out(workspace, (need,), torch.uint8, dev, "workspace", side)
-    return table, dev, side, workspace
-
-
-def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-              stream=None) -> torch.Tensor:
-    """The norm of all ``grads`` together (a :class:`GradTable` or a list of bf16 and fp32 tensors)
-    -> fp32 [1]: sqrt of the sum of all elements' squares, 0 for no elements."""
-    table, dev, side, workspace = _grad_call(grads, norm, workspace, stream)
-    norm = _out(norm, (1,), torch.float32, dev, "norm", side)
-    with _device(dev):
-        st = load().mgw_grad_norm(table._grads, table._sizes, table._dtypes, table.n, _ptr(norm),
-                                  _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(st, "mgw_grad_norm")
-    if side is not None:
-        _used_on(side, norm, workspace, *table.grads)
-    return norm
-
-
-def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, known_norm: torch.Tensor | None = None,
-               eps: float = 1e-6, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Multiplies all ``grads`` (a :class:`GradTable`, into its ``out`` if it has one, or a list) by
-    min(1, max_norm / (norm + eps)) -> their norm, fp32 [1], as :func:`grad_norm` gives it.
-    ``known_norm`` (fp32 [1]), where given, is taken for the norm and returned: that of several
-    processes' gradients, for example."""
-    table, dev, side, workspace = _grad_call(grads, norm, workspace, stream)
-    if table._twice:
-        raise MgwError("a tensor that is written is listed twice")
-    if known_norm is not None:
-        if norm is not None:
-            raise MgwError("norm is not computed where known_norm is given")
-        _dev_tensor(known_norm, torch.float32, "known_norm")
-        _need(known_norm, 1, "known_norm")
-        if known_norm.device != dev:
-            raise MgwError(f"all tensors must be on one CUDA device, got {dev} and {known_norm.device}")
-    else:
-        norm = _out(norm, (1,), torch.float32, dev, "norm", side)
-    with _device(dev):
-        st = load().mgw_grad_clip(table._grads, table._out, table._sizes, table._dtypes, table.n,
-                                  float(max_norm), float(eps), _ptr(known_norm), _ptr(norm),
-                                  _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(st, "mgw_grad_clip")
-    if side is not None:
-        _used_on(side, norm, known_norm, workspace, *table.grads, *(table.out or ()))
-    return norm if known_norm is None else known_norm
+def __getattr__(name):
+    """``mgw.grouped_lora`` and the others of :mod:`.adapters` and :mod:`.gradients`, which build on
+    this module."""
+    module = _ELSEWHERE.get(name)
+    if module is None:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    return getattr(importlib.import_module("." + module, __package__), name)
