@@ -1078,6 +1078,7 @@ mgw_status mgw_grad_norm(const void* const* grads, const int64_t* sizes, const i
   a.sums = static_cast<double*>(workspace);
   a.norm = norm;
   a.sms = dev.sms;
+  a.max_cluster = test_max_cluster();
   const cudaError_t err = mgw::launch_grad(a, false, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
 }
@@ -1110,6 +1111,7 @@ mgw_status mgw_grad_clip(const void* const* grads, void* const* outs, const int6
   a.max_norm = max_norm;
   a.eps = eps;
   a.sms = dev.sms;
+  a.max_cluster = test_max_cluster();
   const cudaError_t err = mgw::launch_grad(a, true, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MGW_OK : MGW_ERR_CUDA;
 }

@@ -279,6 +279,7 @@ struct GradArgs {
   float* norm;           // device; may be null when clipping
   float max_norm, eps;
   int sms;
+  int max_cluster;       // test hook, as DispatchArgs::max_cluster
 };
 size_t grad_workspace_bytes(int count);
 cudaError_t launch_grad(const GradArgs& a, bool clip, cudaStream_t stream);

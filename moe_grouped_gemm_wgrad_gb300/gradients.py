@@ -36,6 +36,7 @@ class GradTable:
                 raise mgw.MgwError("out must hold one tensor of the same type, size and device for every gradient")
             at = [t.data_ptr() for t in self.out]
             self._out = (ctypes.c_void_p * n)(*at)
+        self._workspace = int(mgw.load().mgw_grad_workspace_bytes(mgw._size(n, "the number of gradients")))
         used = [p for p, s in zip(at, sizes) if s]
         self._twice = len(set(used)) != len(used)
 
@@ -71,8 +72,7 @@ def _grad_call(grads, norm, workspace, stream):
         if t is not None and t.device != dev:
             raise mgw.MgwError(f"all tensors must be on one CUDA device, got {sorted({str(dev), str(t.device)})}")
     side = None if stream is None else mgw._side(stream, dev)
-    need = int(mgw.load().mgw_grad_workspace_bytes(mgw._size(table.n, "the number of gradients")))
-    workspace = mgw._out(workspace, (need,), torch.uint8, dev, "workspace", side)
+    workspace = mgw._out(workspace, (table._workspace,), torch.uint8, dev, "workspace", side)
     return table, dev, side, workspace
 
 
