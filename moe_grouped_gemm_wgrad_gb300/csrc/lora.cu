@@ -119,21 +119,32 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
   const int nt1 = out == nullptr ? nt0 : static_cast<int>(static_cast<long long>(ntiles) * (rank + 1) / C);
 
   if (t.e == a.E) {
-    // Rows without an adapter: their base, or zeros.
-    const int c0 = nt0 * kBk, c1 = min(nt1 * kBk, N);
-    for (int i = warp; i < t.nrows; i += kThreads / 32) {
-      const int r = t.row0 + i;
-      if (a.u != nullptr && rank == 0)
-        for (int j = static_cast<int>(lane); j < a.R; j += 32) a.u[static_cast<size_t>(r) * a.R + j] = 0.0f;
-      if (out == nullptr || out == base) continue;
-      const int o = row_place(a.out_index, r, a.out_rows, lane == 0 ? a.status : nullptr);
-      if (o < 0) continue;
-      for (int c = c0 + static_cast<int>(lane) * 8; c < c1; c += 256) {
-        const size_t at = static_cast<size_t>(o) * N + c;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (base != nullptr) v = *reinterpret_cast<const uint4*>(base + at);
-        *reinterpret_cast<uint4*>(out + at) = v;
+    // Rows without an adapter: their base, or zeros.  All rows' places first, then 16 bytes a thread and
+    // step, four steps on their way.
+    if (a.u != nullptr && rank == 0)
+      for (int i = tid; i < t.nrows * a.R; i += kThreads) a.u[static_cast<size_t>(t.row0) * a.R + i] = 0.0f;
+    const int wide = min(nt1 * kBk, N) / 8 - nt0 * (kBk / 8);  // 16-byte pieces of a row
+    if (out == nullptr || out == base || wide <= 0) return;
+    for (int i = tid; i < t.nrows; i += kThreads)
+      s_rows[i] = row_place(a.out_index, t.row0 + i, a.out_rows, rank == 0 ? a.status : nullptr);
+    __syncthreads();
+    constexpr int kSteps = 4;
+    for (int i0 = tid; i0 < t.nrows * wide; i0 += kSteps * kThreads) {
+      uint4 v[kSteps];
+      size_t at[kSteps];
+      bool there[kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int i = i0 + k * kThreads;
+        const int o = i < t.nrows * wide ? s_rows[i / wide] : -1;
+        there[k] = o >= 0;
+        at[k] = static_cast<size_t>(max(o, 0)) * N + nt0 * kBk + i % wide * 8;
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (base != nullptr && there[k]) v[k] = *reinterpret_cast<const uint4*>(base + at[k]);
       }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        if (there[k]) *reinterpret_cast<uint4*>(out + at[k]) = v[k];
     }
     return;
   }
@@ -166,21 +177,21 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
   auto bar_acc = [&](int s) { return bar0 + 8u * (4 * kMaxSlots + 1 + s); };
   auto bar_free = [&](int s) { return bar0 + 8u * (4 * kMaxSlots + 1 + kBufs + s); };
   const uint32_t bar_done = bar0 + 8u * (4 * kMaxSlots + 1 + 2 * kBufs);
-  if (tid == 0) {
-    for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(bar_full(s), in_box ? 1 : 1 + 128 * SETS);
-      mbar_init(bar_empty(s), 1);
-      mbar_init(bar_bfull(s), 1);
-      mbar_init(bar_bempty(s), 4);
+  if (tid < kMaxSlots) {
+    mbar_init(bar_full(tid), in_box ? 1 : 1 + 128 * SETS);
+    mbar_init(bar_empty(tid), 1);
+    mbar_init(bar_bfull(tid), 1);
+    mbar_init(bar_bempty(tid), 4);
+    if (tid < kBufs) {
+      mbar_init(bar_acc(tid), 1);
+      mbar_init(bar_free(tid), 4);
     }
-    mbar_init(bar_sum, 1);
-    for (int s = 0; s < kBufs; ++s) {
-      mbar_init(bar_acc(s), 1);
-      mbar_init(bar_free(s), 4);
+    if (tid == 0) {
+      mbar_init(bar_sum, 1);
+      mbar_init(bar_done, 1);
+      s_tmp[5] = 0;
     }
-    mbar_init(bar_done, 1);
     fence_mbar_init();
-    s_tmp[5] = 0;
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmp + 4), kTmemCols);
@@ -356,40 +367,32 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
         in.step(1, S1);
       }
     }
-    // Eight ranks of a row into its block of Q (see LoraArgs): two bytes at a time, a warp's rows side
-    // by side.
-    auto q_column = [&](uint8_t* q, int r, int j8, const float (&f)[8]) {
-      uint8_t* block = q + (2 * static_cast<size_t>(static_cast<int>(blockIdx.x) / C) + (r >> 6)) * (256u * RP);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        uint32_t hi, lo;
-        split2(f[j], f[j + 1], hi, lo);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t at = swz(8 * j8 + j + k, (r & 63) >> 3) + 2u * (r & 7);
-          *reinterpret_cast<uint16_t*>(block + at) = static_cast<uint16_t>(hi >> (16 * k));
-          *reinterpret_cast<uint16_t*>(block + RP * 128 + at) = static_cast<uint16_t>(lo >> (16 * k));
-        }
-      }
-    };
-    // Rows of the tile that Q's blocks need: they are read up to a multiple of 16.
+    // Rows of the tile that Q's blocks need (see LoraArgs): they are read up to a multiple of 16.
     const int q_rows = TRANS && a.qv != nullptr ? (t.nrows + 15) & ~15 : t.nrows;
+    // Q's blocks, a thread a rank and eight rows; the cluster's CTAs share the rows.
+    auto q_piece = [&](uint8_t* q, int octet, int j, int lo) {
+      return reinterpret_cast<uint4*>(q + (2 * static_cast<size_t>(static_cast<int>(blockIdx.x) / C) + (octet >> 3)) *
+                                              (256u * RP) + lo * RP * 128 + swz(j, octet & 7));
+    };
+    const int octets = (q_rows / 8 - rank + C - 1) / C;
     if constexpr (TRANS) {
-      // u's block, while the products run
+      // u's, while the products run
       if (a.qv != nullptr) {
-        const int per = (q_rows - rank + C - 1) / C;
-        for (int i = tid - 64; i < per * (RP / 8); i += 128 * SETS) {
-          const int r = rank + C * (i % per), j8 = i / per;
+        for (int i = tid - 64; i < octets * RP; i += 128 * SETS) {
+          const int j = i % RP, o = rank + C * (i / RP);
           float f[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-          if (r < t.nrows && 8 * j8 < a.R) {
-            const float4* u = reinterpret_cast<const float4*>(a.u_in + static_cast<size_t>(t.row0 + r) * a.R + 8 * j8);
-            const float4 x = u[0], y = u[1];
-            f[0] = scale * x.x, f[1] = scale * x.y, f[2] = scale * x.z, f[3] = scale * x.w;
-            f[4] = scale * y.x, f[5] = scale * y.y, f[6] = scale * y.z, f[7] = scale * y.w;
+          for (int k = 0; k < 8; ++k) {
+            const int r = 8 * o + k;
+            f[k] = r < t.nrows && j < a.R ? scale * a.u_in[static_cast<size_t>(t.row0 + r) * a.R + j] : 0.0f;
           }
-          q_column(a.qu, r, j8, f);
+          uint4 hi, lo;
+          split2(f[0], f[1], hi.x, lo.x);
+          split2(f[2], f[3], hi.y, lo.y);
+          split2(f[4], f[5], hi.z, lo.z);
+          split2(f[6], f[7], hi.w, lo.w);
+          *q_piece(a.qu, o, j, 0) = hi;
+          *q_piece(a.qu, o, j, 1) = lo;
         }
         __syncwarp();
       }
@@ -409,9 +412,6 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = live ? v[j] * scale : 0.0f;
-      if constexpr (TRANS) {
-        if (a.qv != nullptr) q_column(a.qv, r, j8, v);
-      }
       uint4 hi, lo;
       split2(v[0], v[1], hi.x, lo.x);
       split2(v[2], v[3], hi.y, lo.y);
@@ -433,13 +433,20 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
     const int chains = min(G, chunks);
     for (int j = 16 * set; j < RP; j += 16 * SETS) {
       float v[2][8];
-      uint32_t r[16];
-      for (int g = 0; g < chains && ok; ++g) {
-        tmem_ld_x16(tq + g * RP + j, r);
-        tmem_wait_ld();
+      uint32_t r[G][16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          v[k >> 3][k & 7] = g == 0 ? __uint_as_float(r[k]) : v[k >> 3][k & 7] + __uint_as_float(r[k]);
+      for (int g = 0; g < G; ++g)
+        if (g < chains) tmem_ld_x16(tq + g * RP + j, r[g]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int g = 0; g < G; ++g) tmem_loaded(r[g]);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float sum = __uint_as_float(r[0][k]);
+#pragma unroll
+        for (int g = 1; g < G; ++g)
+          if (g < chains) sum += __uint_as_float(r[g][k]);
+        v[k >> 3][k & 7] = sum;
       }
       if (C == 1) {
         finish(row, j / 8, v[0]);
@@ -546,6 +553,7 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
             if (base != nullptr && mine) b[c] = ld_shared_u4(tile + swz(row, 4 * h + c));
           }
           tmem_wait_ld();
+          tmem_loaded(r);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t* x = r + 8 * c;
@@ -601,6 +609,23 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
       }
       to.step(SETS, S2);
       acc.step(SETS, kBufs);
+    }
+    if constexpr (TRANS) {
+      // v's blocks, which the intermediate holds by rows
+      if (a.qv != nullptr && ok) {
+        for (int i = tid - 64; i < octets * RP * 2; i += 128 * SETS) {
+          const int j = i % RP, part_of = i / RP & 1, o = rank + C * (i / (2 * RP));
+          const uint32_t c = static_cast<uint32_t>(part_of * RQ + j);
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t r = 8u * o + 2 * k, at = su + (c >> 6) * kXBytes + 2u * (c & 7);
+            const uint32_t x = ld_shared_u16(at + swz(r, (c & 63) >> 3));
+            w[k] = x | ld_shared_u16(at + swz(r + 1, (c & 63) >> 3)) << 16;
+          }
+          *q_piece(a.qv, o, j, part_of) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
     }
     if (by_tma && lane == 0) bulk_wait_read0();
     copy_wait<0>();

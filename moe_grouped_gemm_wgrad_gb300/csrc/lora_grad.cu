@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
           tmem_ld_x16(ta, x);
           tmem_ld_x16(ta + RP, y);
           tmem_wait_ld();
+          tmem_loaded(x);
+          tmem_loaded(y);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float4 v = make_float4(__uint_as_float(x[4 * q]) + __uint_as_float(y[4 * q]),
