@@ -904,7 +904,7 @@ mgw_status lora_launch(const void* in, int in_rows, const int32_t* in_index, int
                        void* stream) {
   mgw::LoraArgs a;
   std::memset(&a, 0, sizeof(a));
-  const bool few = !transposed && M <= mgw::kFewRows;
+  const bool few = !transposed && mgw::lora_is_few(M, R);
   const uint32_t rp = static_cast<uint32_t>((R + 15) & ~15);
   if (!few) {
     const bool ok =

@@ -241,7 +241,7 @@ struct LoraArgs {
 };
 cudaError_t launch_lora(const LoraArgs& a, bool transposed, int num_sms, cudaStream_t stream);
 // The forward call for few rows (lora_few.cu); uses none of the maps.
-constexpr int kFewRows = 256;
+bool lora_is_few(int M, int R);
 cudaError_t launch_lora_few(const LoraArgs& a, cudaStream_t stream);
 
 // Gradients of the adapters (lora_grad.cu): grad = X^T Q over the rows of every adapter.

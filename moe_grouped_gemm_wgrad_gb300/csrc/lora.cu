@@ -502,16 +502,18 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         const uint32_t at = part + (2u * j8 * rows8 + r) * 16u;
         if (r < t.nrows) {
-          for (int p = 0; p < C; p += 4) {
-            float4 x[8];  // of four CTAs at a time: a load from another SM takes a while
+          constexpr int kAtOnce = SETS == 2 ? 8 : 4;  // CTAs: a load from another SM takes a while
+          for (int p = 0; p < C; p += kAtOnce) {
+            float4 x[2 * kAtOnce];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t from = map_to_cta(at, min(p + k, C - 1));
+            for (int k = 0; k < kAtOnce; ++k) {
+              if (p + k >= C) break;
+              const uint32_t from = map_to_cta(at, p + k);
               x[2 * k] = ld_cluster_f4(from);
               x[2 * k + 1] = ld_cluster_f4(from + rows8 * 16u);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kAtOnce; ++k) {
               if (p + k >= C) break;
               v[0] += x[2 * k].x, v[1] += x[2 * k].y, v[2] += x[2 * k].z, v[3] += x[2 * k].w;
               v[4] += x[2 * k + 1].x, v[5] += x[2 * k + 1].y, v[6] += x[2 * k + 1].z, v[7] += x[2 * k + 1].w;
