@@ -119,13 +119,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_few_kernel(const LoraArgs a)
   // Lane (g, q): ranks g and g + 8 of a 16-rank tile, row g of x, columns 8 q .. of a 32-column block.
   const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.w1) + static_cast<size_t>(t.e) * R * K;
   const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(a.w2) + static_cast<size_t>(t.e) * N * R;
-  // This CTA's part of B, one run of memory, on its way into L2 while A is read and the sums are exchanged.
-  const int first = n0 * F::kCols, wide = min(n1 * F::kCols, N) - first;
-  if (tid == 0 && wide > 0)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                     reinterpret_cast<uint64_t>(B + static_cast<size_t>(first) * R)),
-                 "r"(static_cast<uint32_t>(wide) * R * 2u)
-                 : "memory");
   const int xrow = g < t.nrows ? row_place(a.in_index, t.row0 + g, a.in_rows, rank == 0 && warp == 0 && q == 0 ? a.status : nullptr) : -1;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.in) + static_cast<size_t>(xrow < 0 ? 0 : xrow) * K;
   const int kblocks = (K + 31) / 32;
@@ -156,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_few_kernel(const LoraArgs a)
 #pragma unroll
       for (int m = 0; m < 2 * NB; ++m) mma_32(sum[m], top[h][m], bottom[h][m], xv[h]);
   }
-  // The first pieces of B and of base are on their way while the sums are exchanged.  Lane (g, q):
+  // The first pieces of B and of base are on their way while the sums are exchanged.  (All of B's part
+  // brought into L2 meanwhile, by bulk prefetch, cost 128 rows of 32 adapters of rank 64 17.2 -> 19.6 us.)  Lane (g, q):
   // columns g and g + 8 of a 16-column tile, ranks 8 q .. of a block.
   uint4 top[F::kTiles][NB], bottom[F::kTiles][NB], bv[kSteps];
   auto load_group = [&](int group) {
