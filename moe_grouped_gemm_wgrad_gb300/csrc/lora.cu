@@ -39,11 +39,12 @@ constexpr int kMaxSlots = 12;
 constexpr int kBufs = 4;              // accumulators of 64 columns
 constexpr uint32_t kTmemCols = 256;   // those; before them the partial sums
 constexpr int kBars = 4 * kMaxSlots + 1 + 2 * kBufs + 1;
-constexpr int kTmpBytes = 80;         // find_tile's ints (18 at most); then [4] TMEM [5] abort
+constexpr int kTmpBytes = 96;         // find_tile's ints (22 at most); then [4] TMEM [5] abort
 
 // Epilogue sets of four warps: two where one CTA fills an SM, one where two CTAs share it.  (Two CTAs of
 // two sets have 80 registers a thread; what did not fit, which no L1 holds beside this much shared
 // memory, made the output's half 1.6 times as long.)  Registers are given out to four warps at a time.
+constexpr int kManySets = 2;
 constexpr int threads_of(int sets) { return 64 + 128 * sets; }
 constexpr int bound_of(int sets) { return (threads_of(sets) + 127) / 128 * 128; }
 
@@ -89,6 +90,7 @@ template <bool TRANS, int RQ, int SETS>
 __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel(const __grid_constant__ LoraArgs a) {
   using P = Plan<RQ>;
   constexpr int G = P::kChains, kThreads = threads_of(SETS);
+  constexpr int COPY = SETS < 2 ? SETS : 2;  // sets that copy the input's rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
   auto bar_free = [&](int s) { return bar0 + 8u * (4 * kMaxSlots + 1 + kBufs + s); };
   const uint32_t bar_done = bar0 + 8u * (4 * kMaxSlots + 1 + 2 * kBufs);
   if (tid < kMaxSlots) {
-    mbar_init(bar_full(tid), in_box ? 1 : 1 + 128 * SETS);
+    mbar_init(bar_full(tid), in_box ? 1 : 1 + 128 * COPY);
     mbar_init(bar_empty(tid), 1);
     mbar_init(bar_bfull(tid), 1);
     mbar_init(bar_bempty(tid), 4);
@@ -335,11 +337,11 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
     const int ew = warp - 2, quarter = warp & 3, set = ew >> 2;
     const int sub = static_cast<int>(lane >> 3), ch = static_cast<int>(lane & 7);
     const float scale = a.scale != nullptr ? a.scale[t.e] : 1.0f;
-    if (!in_box) {
+    if (!in_box && set < COPY) {
       // ------------------------------------------- the input's rows: eight lanes a row
       // Rows behind the tile's last stay as they are: whatever they hold goes into rows that nobody
       // stores.
-      constexpr int kMine = 8 / SETS;  // times four rows a warp
+      constexpr int kMine = 8 / COPY;  // times four rows a warp
       const __nv_bfloat16* src[kMine];
       uint32_t dst[kMine];
       bool there[kMine];
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         const uint32_t at = part + (2u * j8 * rows8 + r) * 16u;
         if (r < t.nrows) {
-          constexpr int kAtOnce = SETS == 2 ? 8 : 4;  // CTAs: a load from another SM takes a while
+          constexpr int kAtOnce = SETS == 1 ? 4 : 8;  // CTAs: a load from another SM takes a while
           for (int p = 0; p < C; p += kAtOnce) {
             float4 x[2 * kAtOnce];
 #pragma unroll
@@ -549,25 +551,36 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
           uint32_t r[32];
           tmem_ld_32x32b_x32(tq + acc.slot * kBk + 32 * h, r);
           uint4 b[4];
+          if (base != nullptr && mine) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            b[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (base != nullptr && mine) b[c] = ld_shared_u4(tile + swz(row, 4 * h + c));
+            for (int c = 0; c < 4; ++c) b[c] = ld_shared_u4(tile + swz(row, 4 * h + c));
           }
           tmem_wait_ld();
           tmem_loaded(r);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t* x = r + 8 * c;
+          if (base != nullptr) {
             auto add2 = [](uint32_t u, uint32_t p, uint32_t q) {
               const float2 f = unpack_bf16(u);
               return pack_bf16(f.x + __uint_as_float(p), f.y + __uint_as_float(q));
             };
-            b[c].x = add2(b[c].x, x[0], x[1]);
-            b[c].y = add2(b[c].y, x[2], x[3]);
-            b[c].z = add2(b[c].z, x[4], x[5]);
-            b[c].w = add2(b[c].w, x[6], x[7]);
-            if (mine) st_shared_u4(tile + swz(row, 4 * h + c), b[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t* x = r + 8 * c;
+              b[c].x = add2(b[c].x, x[0], x[1]);
+              b[c].y = add2(b[c].y, x[2], x[3]);
+              b[c].z = add2(b[c].z, x[4], x[5]);
+              b[c].w = add2(b[c].w, x[6], x[7]);
+            }
+          } else {
+            auto pack2 = [](uint32_t p, uint32_t q) { return pack_bf16(__uint_as_float(p), __uint_as_float(q)); };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t* x = r + 8 * c;
+              b[c] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+            }
+          }
+          if (mine) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) st_shared_u4(tile + swz(row, 4 * h + c), b[c]);
           }
         }
       }
@@ -670,8 +683,8 @@ long long clusters_at_once(int c) {
   if (asked_ctx == 0 || asked_ctx != current_context_id()) {
     for (int k = 2; k <= kMaxCluster; ++k) {
       cudaLaunchAttribute attr = {};
-      const cudaLaunchConfig_t cfg = config(2, k, 1, P::smem(P::kLong), &attr);
-      if (cudaOccupancyMaxActiveClusters(&active[k], lora_kernel<TRANS, RQ, 2>, &cfg) != cudaSuccess) {
+      const cudaLaunchConfig_t cfg = config(kManySets, k, 1, P::smem(P::kLong), &attr);
+      if (cudaOccupancyMaxActiveClusters(&active[k], lora_kernel<TRANS, RQ, kManySets>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();  // a size that does not fit is no error of the call
         active[k] = 0;
       }
@@ -687,7 +700,7 @@ cudaError_t launch_sets(LoraArgs a, int cluster, long long tiles, cudaStream_t s
   const cudaError_t err = set_smem<TRANS, RQ, SETS>();
   if (err != cudaSuccess) return err;
   a.cluster = cluster;
-  a.ring = SETS == 2 ? P::kLong : P::kShort;
+  a.ring = SETS == 1 ? P::kShort : P::kLong;
   cudaLaunchAttribute attr = {};
   cudaLaunchConfig_t cfg = config(SETS, cluster, tiles, P::smem(a.ring), &attr);
   cfg.stream = stream;
@@ -696,7 +709,7 @@ cudaError_t launch_sets(LoraArgs a, int cluster, long long tiles, cudaStream_t s
 
 template <bool TRANS, int RQ>
 cudaError_t launch(const LoraArgs& a, int num_sms, cudaStream_t stream) {
-  cudaError_t err = set_smem<TRANS, RQ, 2>();
+  cudaError_t err = set_smem<TRANS, RQ, kManySets>();
   if (err != cudaSuccess) return err;
   // The exact number of tiles is known on the device only: at most this many, one more for rows without
   // an adapter included; about half a tile of each adapter's is empty.
@@ -713,7 +726,7 @@ cudaError_t launch(const LoraArgs& a, int num_sms, cudaStream_t stream) {
   // More tiles than SMs: two CTAs to an SM, one's loads under the other's exchange.
   if constexpr (RQ < 128)
     if (likely > num_sms) return launch_sets<TRANS, RQ, 1>(a, 1, tiles, stream);
-  return launch_sets<TRANS, RQ, 2>(a, c, tiles, stream);
+  return launch_sets<TRANS, RQ, kManySets>(a, c, tiles, stream);
 }
 
 template <bool TRANS>
