@@ -52,9 +52,9 @@ constexpr size_t part_floats(int RP) { return static_cast<size_t>(kWidth) * RP; 
 // The data gradient's launch has ended and its results are there.
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The share of the token blocks of CTA p of C.
+// The share of the token blocks of CTA p of C.  (At most 2^25 + 1024 blocks, C at most 8.)
 __device__ __forceinline__ int share(int blocks, int p, int C) {
-  return static_cast<int>(static_cast<long long>(blocks) * p / C);
+  return static_cast<int>(static_cast<uint32_t>(blocks) * static_cast<uint32_t>(p) / static_cast<uint32_t>(C));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_constant__ LoraGradArgs a) {
@@ -247,16 +247,22 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     int stage = 0;
     uint32_t phase = 0;
     while (ok && w.next(t0, t1, E)) {
-      // this lane's token of a block: its row of X, loaded a block ahead and looked at when it is needed
+      // this lane's token of a block: its row of X, loaded four blocks ahead (a block is copied faster than
+      // a load comes back) and looked at when it is needed
       auto place_of = [&](int b) {
         const int r = b * kTok + q0 + static_cast<int>(lane & 15u);
         return r < w.n ? (job.index != nullptr ? job.index[w.lo + r] : w.lo + r) : -1;
       };
-      int ahead = place_of(w.b0);
+      constexpr int kAhead = 4;
+      int ahead[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) ahead[k] = place_of(w.b0 + k);
       for (int b = w.b0; b < w.b1; ++b) {
         const int left = w.n - b * kTok;
-        int place = ahead;
-        ahead = place_of(b + 1);
+        int place = ahead[0];
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) ahead[k] = ahead[k + 1];
+        ahead[kAhead - 1] = place_of(b + kAhead);
         if (q0 + static_cast<int>(lane & 15u) < left && (place < 0 || place >= job.rows)) {
           if (a.status != nullptr && lane < 16 && f0 == 0) atomicOr(a.status, kDevBadIndex);
           place = -1;
@@ -371,24 +377,41 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     if (v.at >= t0 && end <= t1) continue;
     // the CTAs with blocks of this adapter
     uint32_t with = 0;
-    for (int p = 0; p < C; ++p) {
-      const int p0 = share(blocks, p, C), p1 = share(blocks, p + 1, C);
+    const float4* from[kMaxCluster];
+    int p0 = 0;
+#pragma unroll
+    for (int p = 0; p < kMaxCluster; ++p) {
+      if (p == C) break;
+      const int p1 = share(blocks, p + 1, C);
       if (p0 < p1 && p0 < end && p1 > v.at) with |= 1u << p;
+      from[p] = partial(p, v.at < p0 ? 0 : 1);
+      p0 = p1;
     }
     const int count = __popc(with), k = __popc(with & ((1u << rank) - 1u));
     const int g0 = kWidth * k / count, per = kWidth * (k + 1) / count - g0;
-    for (int i = tid; i < per * (RP / 4); i += kThreads) {
-      const int f = g0 + i % per, j4 = i / per;
-      // every CTA's sums at once: a load in turn for each took longer than the rest of the sum
-      float4 x[kMaxCluster];
+    // Several sums at a time, each of up to eight CTAs' parts: their loads are what this takes.
+    constexpr int kSums = 2;
+    const int items = per * (RP / 4);
+    for (int i0 = tid; i0 < items; i0 += kSums * kThreads) {
+      float4 x[kSums][kMaxCluster];
+      int f[kSums], j4[kSums];
 #pragma unroll
-      for (int p = 0; p < kMaxCluster; ++p)
-        if ((with >> p) & 1u) x[p] = __ldcg(partial(p, v.at < share(blocks, p, C) ? 0 : 1) + j4 * kWidth + f);
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int q = 0; q < kSums; ++q) {
+        const int i = min(i0 + q * kThreads, items - 1);
+        j4[q] = i / per;
+        f[q] = g0 + i - j4[q] * per;
 #pragma unroll
-      for (int p = 0; p < kMaxCluster; ++p)
-        if ((with >> p) & 1u) s.x += x[p].x, s.y += x[p].y, s.z += x[p].z, s.w += x[p].w;
-      store4(v.e, f, 4 * j4, s);
+        for (int p = 0; p < kMaxCluster; ++p)
+          if ((with >> p) & 1u) x[q][p] = __ldcg(from[p] + j4[q] * kWidth + f[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kSums; ++q) {
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p)
+          if ((with >> p) & 1u) sum.x += x[q][p].x, sum.y += x[q][p].y, sum.z += x[q][p].z, sum.w += x[q][p].w;
+        if (i0 + q * kThreads < items) store4(v.e, f[q], 4 * j4[q], sum);
+      }
     }
   }
 }
