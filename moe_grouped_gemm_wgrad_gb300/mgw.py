@@ -909,12 +909,16 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, row_of: tor
 # ------------------------------------------------------------- operators in modules of their own
 _ELSEWHERE = {"grouped_lora": "adapters", "grouped_lora_backward": "adapters",
               "GradTable": "gradients", "grad_norm": "gradients", "clip_grads": "gradients"}
+_found = {}
 
 
 def __getattr__(name):
     """``mgw.grouped_lora`` and the others of :mod:`.adapters` and :mod:`.gradients`, which build on
     this module."""
-    module = _ELSEWHERE.get(name)
-    if module is None:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    return getattr(importlib.import_module("." + module, __package__), name)
+    f = _found.get(name)
+    if f is None:
+        module = _ELSEWHERE.get(name)
+        if module is None:
+            raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        f = _found[name] = getattr(importlib.import_module("." + module, __package__), name)
+    return f
