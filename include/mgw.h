@@ -13,8 +13,8 @@
  * then leave their outputs untouched.
  * No entry point aborts, traps or blocks the host.
  *
- * Limits common to every entry point: device pointers 16-byte aligned (else
- * MGW_ERR_INVALID_ARG); a padded token or row axis Mcap (or Mw) of at most 2^31
+ * Limits common to every entry point: device pointers 16-byte aligned (those of gradients to
+ * be clipped: to their element; else MGW_ERR_INVALID_ARG); a padded token or row axis Mcap (or Mw) of at most 2^31
  * (else MGW_ERR_CAPACITY); 1 <= E <= MGW_MAX_EXPERTS.  The current device must be
  * compute capability 10.3 (else MGW_ERR_ARCH).
  *
@@ -50,7 +50,7 @@ typedef int mgw_status;
 /* Bits OR-ed into *status_dev by the kernels (the caller zeroes it). */
 #define MGW_DEV_BAD_OFFSETS 1 /* expert_off[0] != 0, decreasing, or expert_off[E] != M/rows */
 #define MGW_DEV_TIMEOUT 2     /* an internal pipeline wait exceeded 1 s; outputs undefined */
-#define MGW_DEV_BAD_INDEX 4   /* a row index (quantizers, combine) or expert index (router, dispatch) out of range */
+#define MGW_DEV_BAD_INDEX 4   /* a row index (quantizers, combine, adapters) or expert index (router, dispatch) out of range */
 #define MGW_DEV_BOUNDS 8      /* diagnostic library only (mgw_diag.h): a computed address outside its tensor */
 #define MGW_DEV_BAD_LOGIT 16  /* mgw_moe_route: a logit that is not a number */
 
@@ -60,7 +60,7 @@ typedef int mgw_status;
 #define MGW_SCALE_FLOOR 0    /* OCP MX: 2^(floor(log2 amax) - 8), saturate to +-448 */
 #define MGW_SCALE_CEIL_448 1 /* post-attn page's RoundUp: ceil_pow2(amax * fp32(1/448)) */
 
-/* Element types of the router's logits and of the combine's rows. */
+/* Element types of the router's logits, of the combine's rows and of gradients. */
 #define MGW_TYPE_BF16 0
 #define MGW_TYPE_F32 1
 
@@ -500,8 +500,8 @@ mgw_status mgw_moe_combine_backward(const void *dout, const void *y, int dtype, 
  *             rows of out that no row names are not written.
  * out         device, bf16 [out_rows, N].
  * u           device fp32 [M, R], nullable: the intermediate, for the backward pass.
- * K, N, R multiples of 8 (pad an adapter's rank with zeros), R <= MGW_MAX_RANK, K, N <= 2^23 (else
- * MGW_ERR_UNSUPPORTED).  An index out of range sets MGW_DEV_BAD_INDEX: a row of x then counts as
+ * K, N, R multiples of 8 (pad an adapter's rank with zeros), R <= MGW_MAX_RANK, K, N <= 2^23, M <=
+ * 2^30 (else MGW_ERR_UNSUPPORTED).  An index out of range sets MGW_DEV_BAD_INDEX: a row of x then counts as
  * zeros, a row of out is not written. */
 mgw_status mgw_grouped_lora(const void *x_bf16, int x_rows, const int32_t *row_index, int M, int K,
                             const void *a_bf16, const void *b_bf16, const float *scale,
@@ -516,7 +516,8 @@ mgw_status mgw_grouped_lora(const void *x_bf16, int x_rows, const int32_t *row_i
  *   db[e, n, j] = scale[e] * sum over the rows r of adapter e of dy[o(r), n] * u[r, j]
  * (the gradient to base is dy).  dx has the rows of dy: a layer that gathers rows of x several
  * times adds them up with mgw_moe_combine.  Adapters without rows get zeros; rows without an
- * adapter dx_base.  All sums are fp32 in an order that the sizes fix; each output is rounded once.
+ * adapter dx_base.  All sums are fp32, in an order that the sizes and the device fix; each output is
+ * rounded once.
  * dy, dx_base device, bf16 [out_rows, N] and [out_rows, K] (dx_base nullable (0); may be dx).
  * dx          device, bf16 [out_rows, K], nullable.
  * da, db      device, bf16 [E, R, K] and [E, N, R], fully written; both or (null) neither.

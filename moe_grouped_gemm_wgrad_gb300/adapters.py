@@ -73,8 +73,7 @@ def _fit(x, a, b, adapter_off, row_index, out_index, scale, out_like, u=None, x_
                 and (u is None or u.get_device() == d and u.dtype is _F32 and u.size() == (M, R)
                      and u.is_contiguous())
                 and (x_like is None or x_like.get_device() == d and x_like.dtype is _BF16
-                     and x_like.size() == (out_like.size(0), K) and x_like.is_contiguous())
-                and E * R * K <= mgw.MAX_SIZE and E * N * R <= mgw.MAX_SIZE)
+                     and x_like.size() == (out_like.size(0), K) and x_like.is_contiguous()))
     except (AttributeError, IndexError, TypeError, ValueError):
         return False
 

@@ -873,7 +873,8 @@ mgw_status lora_check(const void* x, int x_rows, const int32_t* row_index, int M
   if (!a || !b || !adapter_off || (M > 0 && !x)) return MGW_ERR_INVALID_ARG;
   if (M < 0 || K <= 0 || N <= 0 || R <= 0 || x_rows < 0 || out_rows < 0 || E < 1 || E > MGW_MAX_EXPERTS)
     return MGW_ERR_INVALID_ARG;
-  if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0 || R > MGW_MAX_RANK || K > (1 << 23) || N > (1 << 23))
+  if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0 || R > MGW_MAX_RANK || K > (1 << 23) || N > (1 << 23) ||
+      M > (1 << 30))
     return MGW_ERR_UNSUPPORTED;
   // row r is row r where there is no index
   if ((!row_index && x_rows < M) || (!out_index && out_rows < M)) return MGW_ERR_INVALID_ARG;

@@ -14,11 +14,17 @@
 // backward pass wants it), one launch does it all, and few rows still use many SMs: a decode step's
 // rows stream their adapters through eight SMs each.
 //
+// HBM bounds it: the input once, base and out once, the adapters from L2.  16384 rows of one adapter,
+// 4096 x 4096, rank 64, u saved: 75 us, 5.4 TB/s; of these 25 us the input's half (a bare TMA read of the
+// same boxes takes 24.5), 36 the output's (half of its traffic is writes), the rest launch, setup and
+// the exchange between the halves, when HBM is idle.  65536 gathered rows of 64 adapters, 4096 x 1536,
+// rank 32: 134 us, bound by L2 in the input's half (every row of x is read eight times).
+//
 // Both halves stream through one ring of shared-memory slots: 64 columns of 128 rows (the input's,
 // then the base's, which become the output's in place) and the weight's tile that goes with them.
 // Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-5 (where one CTA fills an SM, 6-9 too, a
 // second set) have a TMEM lane quarter each.  They copy the input's rows where these are few or lie apart (16 bytes a
-// lane; gathered by TMA, four rows an instruction, 65536 rows took 1.5 times as long), turn the
+// lane; gathered by TMA, four rows an instruction, 65536 rows took 236 us in all instead of 159), turn the
 // partial sums into the intermediate, and take the output's tiles in turns: accumulator + base, rounded
 // once, stored by TMA, or as whole 128-byte row pieces where rows lie apart.
 #include <cuda_runtime.h>

@@ -32,7 +32,8 @@ def test_lora_refusals(lib):
                 dict(ri=OK, x_rows=0), dict(oi=OK, out_rows=0), dict(x=ODD), dict(ri=ODD), dict(a=ODD), dict(b=ODD),
                 dict(scale=ODD), dict(off=ODD), dict(base=ODD), dict(oi=ODD), dict(out=ODD), dict(u=ODD)):
         assert _call(lib.mgw_grouped_lora, base, **bad) == -1, bad
-    for bad in (dict(K=60), dict(N=4), dict(R=12), dict(R=136), dict(K=(1 << 23) + 8), dict(N=(1 << 23) + 8)):
+    for bad in (dict(K=60), dict(N=4), dict(R=12), dict(R=136), dict(K=(1 << 23) + 8), dict(N=(1 << 23) + 8),
+                dict(M=(1 << 30) + 1, x_rows=2 ** 31 - 1, out_rows=2 ** 31 - 1)):
         assert _call(lib.mgw_grouped_lora, base, **bad) == -2, bad
 
 
