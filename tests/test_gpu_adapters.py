@@ -114,6 +114,12 @@ CASES = [
     dict(counts=[63, 64, 65, 100], R=56, K=264, N=520, mode="plain", none=1), dict(counts=[400], R=128, K=264, N=200, base=False),
     dict(counts=[200, 0, 201], R=80, K=72, N=1000, none=17), dict(counts=[17] * 40, R=8, K=2048, N=8),
     dict(counts=[700], R=24, K=8, N=328, mode="gather"), dict(counts=[0, 0, 0], R=32, K=64, N=64, none=400, mode="plain"),
+    # the last rows of the kernel for few, and more than it takes, forward and backward
+    dict(counts=[1024], R=32, K=64, N=72), dict(counts=[513, 511, 1], R=32, K=200, N=136, mode="plain"),
+    dict(counts=[500, 12], R=40, K=96, N=64), dict(counts=[500, 0, 13], R=40, K=1032, N=520, mode="gather"),
+    dict(counts=[1, 1200, 0, 127], R=8, K=520, N=264, none=9), dict(counts=[130] * 9, R=16, K=1000, N=8, base=False),
+    dict(counts=[0, 1023], R=24, K=8, N=1032, none=129, mode="gather"), dict(counts=[9] * 150, R=32, K=136, N=88),
+    dict(counts=[0, 0], R=16, K=64, N=328, none=1100, mode="plain"), dict(counts=[600], R=56, K=72, N=200, none=3),
 ]
 
 
@@ -133,7 +139,7 @@ def test_forward_and_backward(case):
     assert c.status.item() == 0
 
 
-@pytest.mark.parametrize("M", [40, 900])
+@pytest.mark.parametrize("M", [40, 900, 3000])
 def test_in_place_and_rows_that_nobody_names(M):
     """base may be out (and dx_base dx); rows of out that no row names stay as they were."""
     c = Case([M // 2, M // 4], 16, 128, 192, none=M // 8, mode="tokens")
@@ -156,7 +162,7 @@ def test_in_place_and_rows_that_nobody_names(M):
     assert c.status.item() == 0
 
 
-@pytest.mark.parametrize("M", [30, 600])
+@pytest.mark.parametrize("M", [30, 600, 1800])
 def test_not_a_number_stays_in_its_row_and_adapter(M):
     """Infinities and NaN in one row of x, in an unused adapter and in rows without one reach nobody else."""
     c = Case([M // 3, 0, M // 3], 16, 128, 136, none=M // 3, mode="tokens")
@@ -181,7 +187,7 @@ def test_not_a_number_stays_in_its_row_and_adapter(M):
     assert torch.isnan(got[1][0][:, 5]).any() and torch.equal(got[1][0][:, :5], want[1][0][:, :5])
 
 
-@pytest.mark.parametrize("M", [24, 500])
+@pytest.mark.parametrize("M", [24, 500, 1400])
 def test_bad_tables_are_reported(M):
     c = Case([M // 2, M // 2], 16, 64, 128, mode="tokens")
     want, u = c.forward()
@@ -208,14 +214,15 @@ def test_bad_tables_are_reported(M):
     rest = [r for r in range(c.M) if r not in (3, 5)]
     assert torch.equal(out[c.o[rest]], want[c.o[rest]])
     c.status.zero_()
-    _, da, db = mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, c.a.cuda(), c.b.cuda(), dev(c.off),
+    dx = torch.full((c.M, c.K), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, da, db = mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, c.a.cuda(), c.b.cuda(), dev(c.off), dx=dx,
                                           **dict(c.tables(), row_index=rows, out_index=place))
     assert c.status.item() == mgw.MGW_DEV_BAD_INDEX
-    c.t, c.o = c.t.copy(), c.o.copy()
+    assert (dx[c.o[5]] == 7).all()
+    dx[c.o[5]] = 0
+    c.t, c.o, c.dx_base = c.t.copy(), c.o.copy(), None
     c.t[3], c.o[5] = -1, -1
-    want = ref.lora_backward(f64(c.dy), f64(c.x), f64(u), f64(c.a), f64(c.b), c.off, c.t, c.o, c.scale.astype(np.float64),
-                             np.zeros((c.M, c.K)))
-    assert np.allclose(f64(da), want[1], rtol=2 * EPS, atol=EPS) and np.allclose(f64(db), want[2], rtol=2 * EPS, atol=EPS)
+    c.check_backward(u, dx, da, db)
 
 
 def test_no_rows():
@@ -235,7 +242,7 @@ def test_many_adapters(E):
     c.check_backward(u, *c.backward(u))
 
 
-@pytest.mark.parametrize("M", [17, 400])
+@pytest.mark.parametrize("M", [17, 400, 1300])
 def test_captured_calls_replay_on_new_data(M):
     """Two graphs, each with its own workspace, replayed in turn on inputs that change between."""
     c = Case([M // 2, M - M // 2], 32, 128, 136, mode="tokens")
@@ -285,7 +292,7 @@ def test_two_streams_at_once(M):
 
 
 @pytest.mark.parametrize("most", [1, 2, 3, 5, 8])
-@pytest.mark.parametrize("case", [CASES[2], CASES[5], CASES[12], CASES[13], CASES[16]], ids=lambda c: str(c["counts"]))
+@pytest.mark.parametrize("case", [CASES[2], CASES[5], CASES[12], CASES[13], CASES[16], CASES[21], CASES[24]], ids=lambda c: str(c["counts"]))
 def test_smaller_clusters(monkeypatch, most, case):
     """Where a context cannot run clusters of eight (the test build of the library takes the limit)."""
     hooks = mgw.bind(ctypes.CDLL(build.LIB_TESTHOOKS))

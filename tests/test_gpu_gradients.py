@@ -4,12 +4,14 @@ Tolerances: a thread's squares are summed in fp32 in chains of eight and a tree 
 each, of a sum of positive numbers), everything after in more bits, so the sum of squares is right to
 11 2^-24 and the norm, with its own rounding, to 6.5 2^-24: 2^-21.  The factor adds three roundings, an
 output its own (half a step of its type); below the type's smallest normal number a step is absolute."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import adapter_reference as ref
-from moe_grouped_gemm_wgrad_gb300 import mgw
+from moe_grouped_gemm_wgrad_gb300 import build, mgw
 
 pytestmark = pytest.mark.gpu
 TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -54,6 +56,23 @@ def test_norm_and_clip(sizes, kinds):
         mine = [t.clone() for t in grads]
         assert torch.equal(mgw.clip_grads(mine, max_norm), norm)
         assert all(torch.equal(p, q) for p, q in zip(mine, outs))
+
+
+@pytest.mark.parametrize("sizes", [[1], [9, 0, 70001], [3] * 129], ids=lambda s: f"{len(s)}x{s[0]}")
+def test_few_gradients_without_clusters(monkeypatch, sizes):
+    """Where a context runs no clusters a few gradients go by the kernels for many (the test build takes the limit)."""
+    rng = np.random.default_rng(sum(sizes))
+    host = [values(rng, n, "bf16" if i % 2 else "f32") for i, n in enumerate(sizes)]
+    grads = [t.cuda() for t in host]
+    want = mgw.grad_norm(grads)
+    hooks = mgw.bind(ctypes.CDLL(build.LIB_TESTHOOKS))
+    monkeypatch.setattr(mgw, "load", lambda: hooks)
+    for most in (1, 2, 3):
+        monkeypatch.setenv("MGW_TEST_MAX_CLUSTER", str(most))
+        outs = [torch.full_like(t, 9.0) for t in grads]
+        norm = mgw.clip_grads(mgw.GradTable(grads, out=outs), 0.25)
+        check(host, outs, norm, 0.25)
+        assert (norm - want).abs().item() <= 2.0 ** -20 * want.item() and torch.equal(norm, mgw.grad_norm(grads))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
