@@ -20,8 +20,8 @@
 // 5.1 TB/s; 8192 rows of 16 adapters, scattered, 8192 and 4096 features, rank 16: 52 us, 3.9 TB/s (96 CTAs:
 // 48 feature blocks fit two to a cluster).
 //
-// Roles (320 threads): warp 0 loads by TMA, warps 6-9 copy rows that lie apart and an adapter's last
-// rows, warp 1 issues the MMAs, warps 2-5 are the epilogue, which overlaps the next adapter's blocks
+// Roles (448 threads): warp 0 loads by TMA, warps 6-13 copy rows that lie apart and an adapter's last
+// rows (with four warps, which is too few loads in flight, 8192 scattered rows took 4 us more), warp 1 issues the MMAs, warps 2-5 are the epilogue, which overlaps the next adapter's blocks
 // where two accumulators fit into TMEM (rank up to 64).
 #include <cuda_runtime.h>
 
@@ -34,7 +34,7 @@ namespace {
 
 using namespace lora;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
 constexpr int kTok = 64;           // tokens per stage
 constexpr int kWidth = 256;        // features per CTA
 constexpr int kXBytes = 4 * 8192;  // 64 tokens of 256 features
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
   if (tid == 0) {
     tma_prefetch_desc(&job.tm);
     for (int s = 0; s < S; ++s) {
-      mbar_init(bar_full(s), 1 + 128);
+      mbar_init(bar_full(s), 1 + 256);
       mbar_init(bar_empty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     __syncwarp();
   } else if (warp >= 6) {
     // ------------------------------------------------- rows that lie apart
-    // A warp has 16 of a block's tokens, all lanes one row at a time (512 bytes).  Blocks that come
+    // A warp has 8 of a block's tokens, all lanes one row at a time (512 bytes).  Blocks that come
     // as a box it only passes on, in step.
-    const int q0 = (warp - 6) * 16, ch = static_cast<int>(lane & 7);
+    const int q0 = (warp - 6) * 8, ch = static_cast<int>(lane & 7);
     const uint32_t part = (lane >> 3) * 8192u;
     const int col = f0 + 8 * static_cast<int>(lane);
     const bool there = col < cols;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
       // this lane's token of a block: its row of X, loaded four blocks ahead (a block is copied faster than
       // a load comes back) and looked at when it is needed
       auto place_of = [&](int b) {
-        const int r = b * kTok + q0 + static_cast<int>(lane & 15u);
+        const int r = b * kTok + q0 + static_cast<int>(lane & 7u);
         return r < w.n ? (job.index != nullptr ? job.index[w.lo + r] : w.lo + r) : -1;
       };
       constexpr int kAhead = 4;
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k + 1 < kAhead; ++k) ahead[k] = ahead[k + 1];
         ahead[kAhead - 1] = place_of(b + kAhead);
-        if (q0 + static_cast<int>(lane & 15u) < left && (place < 0 || place >= job.rows)) {
-          if (a.status != nullptr && lane < 16 && f0 == 0) atomicOr(a.status, kDevBadIndex);
+        if (q0 + static_cast<int>(lane & 7u) < left && (place < 0 || place >= job.rows)) {
+          if (a.status != nullptr && lane < 8 && f0 == 0) atomicOr(a.status, kDevBadIndex);
           place = -1;
         }
         ok = wait_all(bar_empty(stage), phase ^ 1u, abort_flag);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
           const int rows = ((min(left, kTok) + 15) & ~15) - q0;  // those that the MMAs read
           if (rows > 0) {
 #pragma unroll
-            for (int p = 0; p < 16; ++p) {
+            for (int p = 0; p < 8; ++p) {
               const int o = __shfl_sync(0xffffffffu, place, p);
               copy16(sx + swz(q0 + p, ch), x + static_cast<size_t>(max(o, 0)) * cols, there && o >= 0);
             }
