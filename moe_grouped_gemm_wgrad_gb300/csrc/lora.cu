@@ -500,11 +500,11 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
     __syncwarp();
     cluster_wait();
     if (C > 1) {
-      // This CTA's rows of the tile, summed over the CTAs in their order.  Rows are dealt out one by
-      // one, so that few rows are many CTAs' work too.
-      const int per = (q_rows - rank + C - 1) / C;
+      // This CTA's rows of the tile, summed over the CTAs in their order.  Neighbouring lanes have
+      // neighbouring rows, which lie in different banks of either tile.
+      const int r0 = q_rows * rank / C, per = q_rows * (rank + 1) / C - r0;
       for (int i = tid - 64; i < per * (RP / 8); i += 128 * SETS) {
-        const int r = rank + C * (i % per), j8 = i / per;
+        const int r = r0 + i % per, j8 = i / per;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
