@@ -483,11 +483,13 @@ cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream) {
   const long long items = items_of(a.job[0].cols) + items_of(a.job[1].cols);
   a.first1 = static_cast<int>(items_of(a.job[0].cols));
   a.stages = stages_of(RP);
-  // As many CTAs to a feature block as run at once: 15 clusters of eight, 36 of four.
+  // As many CTAs to a feature block as run at once (15 clusters of eight, 36 of four) and have work: the
+  // exact number of token blocks is known on the device only, up to one block of each adapter's is empty.
+  const long long some = a.M < a.E ? a.M : a.E, likely = a.M / kTok + some / 2;
   const int most = a.max_cluster > 0 && a.max_cluster < kMaxCluster ? a.max_cluster : kMaxCluster;
   int c = 1;
   for (int k = 2; k <= most; ++k)
-    if (items * k <= kSms && static_cast<long long>(k) * kTok <= a.M && items <= clusters_at_once(k)) c = k;
+    if (items * k <= kSms && k <= likely && items <= clusters_at_once(k)) c = k;
   a.cluster = c;
   cudaLaunchAttribute attr[2] = {};
   cudaLaunchConfig_t cfg =
