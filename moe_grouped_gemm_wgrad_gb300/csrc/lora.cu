@@ -718,10 +718,10 @@ cudaError_t launch(const LoraArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t err = set_smem<TRANS, RQ, kManySets>();
   if (err != cudaSuccess) return err;
   // The exact number of tiles is known on the device only: at most this many, one more for rows without
-  // an adapter included; about half a tile of each adapter's is empty.
+  // an adapter included; about half a tile of each adapter's is empty, or more where rows are few.
   const long long some = a.M < a.E ? a.M : a.E;
   const long long tiles = (a.M + kRows - 1) / kRows + some + 1;
-  const long long likely = (a.M + kRows - 1) / kRows + some / 2;
+  const long long full = (a.M + kRows - 1) / kRows, likely = full + some / 2 > some ? full + some / 2 : some;
   // Where the tiles leave SMs idle: as many CTAs to a tile, each with some columns of its own, as run at
   // once (a cluster that waits for another one's end costs as much again).
   const int nch = (a.K + kBk - 1) / kBk;
