@@ -528,10 +528,11 @@ cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream) {
   const long long items = items_of(a.job[0].cols) + items_of(a.job[1].cols);
   a.first1 = static_cast<int>(items_of(a.job[0].cols));
   a.stages = stages_of(RP);
-  // As many CTAs to a feature block as run at once (15 clusters of eight, 36 of four) and have work: the
-  // exact number of token blocks is known on the device only, about half a block of each adapter's is empty.
-  const long long some = a.M < a.E ? a.M : a.E;
-  const long long likely = a.M / kTok + some / 2 > some ? a.M / kTok + some / 2 : some;
+  // As many CTAs to a feature block as run at once (15 clusters of eight, 36 of four) and as have two
+  // token blocks each, or one adapter's: sums that several CTAs share cost as much as a block or two (512
+  // rows of four adapters, rank 128, 2048 and 1536 features: 21 us by four CTAs, 28 by eight).
+  const long long some = a.M < a.E ? a.M : a.E, pairs = (a.M / kTok + 1) / 2;
+  const long long likely = pairs > some ? pairs : some;
   const int most = a.max_cluster > 0 && a.max_cluster < kMaxCluster ? a.max_cluster : kMaxCluster;
   int c = 1;
   for (int k = 2; k <= most; ++k)
