@@ -300,9 +300,10 @@ cudaError_t launch(LoraArgs a, cudaStream_t stream) {
 
 }  // namespace
 
-// Rank 16, eight adapters, 4096 x 4096: 1024 rows 16 us here and 18 in lora.cu, 2048 rows 27 and 22; rank
-// 64, 64 adapters: 512 rows 27 and 39; rank 128, eight adapters: 256 rows 16 and 21.
-bool lora_is_few(int M, int R) { return M <= (R <= 32 ? 1024 : (R <= 64 ? 512 : 256)); }
+// Here and in lora.cu, 4096 x 4096: eight adapters of rank 16, 1024 rows 13.1 and 14.2 us, 2048 rows 25 and 18;
+// rank 64, 512 rows 14.4 and 14.6, 1024 rows 22 and 17.5; rank 128, 512 rows 21 and 17.6, 1024 rows 35 and 22.5,
+// but of 64 adapters 512 rows 34 and 43, and 2048 x 1536 12.5 and 12.7.
+bool lora_is_few(int M, int R) { return M <= (R <= 32 ? 1024 : 512); }
 
 cudaError_t launch_lora_few(const LoraArgs& a, cudaStream_t stream) {
   if (a.R > 64) return launch<4>(a, stream);

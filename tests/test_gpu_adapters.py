@@ -120,6 +120,11 @@ CASES = [
     dict(counts=[1, 1200, 0, 127], R=8, K=520, N=264, none=9), dict(counts=[130] * 9, R=16, K=1000, N=8, base=False),
     dict(counts=[0, 1023], R=24, K=8, N=1032, none=129, mode="gather"), dict(counts=[9] * 150, R=32, K=136, N=88),
     dict(counts=[0, 0], R=16, K=64, N=328, none=1100, mode="plain"), dict(counts=[600], R=56, K=72, N=200, none=3),
+    dict(counts=[500, 0, 12], R=128, K=264, N=200, base=False), dict(counts=[530, 7], R=104, K=520, N=136, none=1),
+    dict(counts=[300, 0, 300], R=128, K=1000, N=264, mode="gather", base=False), dict(counts=[30] * 20, R=72, K=72, N=1000),
+    # many adapters, few rows each: clusters whose CTAs have an adapter or two
+    dict(counts=[1, 0, 2, 1] * 8, R=128, K=520, N=264), dict(counts=[64] * 8, R=96, K=264, N=72, mode="plain"),
+    dict(counts=[0, 70, 1, 0, 130, 5], R=40, K=1000, N=328, none=40), dict(counts=[3] * 100, R=24, K=136, N=520),
 ]
 
 
@@ -292,7 +297,7 @@ def test_two_streams_at_once(M):
 
 
 @pytest.mark.parametrize("most", [1, 2, 3, 5, 8])
-@pytest.mark.parametrize("case", [CASES[2], CASES[5], CASES[12], CASES[13], CASES[16], CASES[21], CASES[24]], ids=lambda c: str(c["counts"]))
+@pytest.mark.parametrize("case", [CASES[2], CASES[5], CASES[12], CASES[13], CASES[16], CASES[21], CASES[24], CASES[32], CASES[35], CASES[37]], ids=lambda c: str(c["counts"]))
 def test_smaller_clusters(monkeypatch, most, case):
     """Where a context cannot run clusters of eight (the test build of the library takes the limit)."""
     hooks = mgw.bind(ctypes.CDLL(build.LIB_TESTHOOKS))
