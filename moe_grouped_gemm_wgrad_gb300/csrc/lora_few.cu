@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_few_kernel(const LoraArgs a)
   // Lane (g, q): ranks g and g + 8 of a 16-rank tile, row g of x, columns 8 q .. of a 32-column block.
   const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.w1) + static_cast<size_t>(t.e) * R * K;
   const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(a.w2) + static_cast<size_t>(t.e) * N * R;
-  const int xrow = g < t.nrows ? row_place(a.in_index, t.row0 + g, a.in_rows, rank == 0 && warp == 0 && q == 0 ? a.status : nullptr) : -1;
+  const int xrow = g < t.nrows ? row_place(a.in_index, t.row0 + g, a.in_rows,
+                                           rank == 0 && warp == 0 && q == 0 ? a.status : nullptr)
+                               : -1;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.in) + static_cast<size_t>(xrow < 0 ? 0 : xrow) * K;
   const int kblocks = (K + 31) / 32;
   const int b0 = static_cast<int>(static_cast<long long>(kblocks) * rank / C);

@@ -16,13 +16,16 @@
 // in the order of the shares, a part of the features each.  No atomics, no second launch, the same
 // bits on every run.
 //
-// HBM bounds it: dy and x once.  16384 rows of one adapter, 4096 and 4096 features, rank 64: 55 us,
-// 5.1 TB/s; 8192 rows of 16 adapters, scattered, 8192 and 4096 features, rank 16: 52 us, 3.9 TB/s (96 CTAs:
-// 48 feature blocks fit two to a cluster).
+// HBM bounds it: dy and x once.  16384 rows of one adapter, 4096 and 4096 features, rank 64: 53 us,
+// 5.1 TB/s; 8192 rows of 16 adapters, scattered, 8192 and 4096 features, rank 16: 49 us, 4.1 TB/s (96 CTAs:
+// 48 feature blocks fit two to a cluster).  Shares of all 152 SMs that cross the feature blocks' borders,
+// their sums added up by the last CTA to come, took 6 us off the latter, but 4 to 19 us more with 64
+// feature blocks (8192 rows, ranks 16 to 128) and half as much again with 1024 rows of 14 (rank 128).
 //
-// Roles (448 threads): warp 0 loads by TMA, warps 6-13 copy rows that lie apart and an adapter's last
-// rows (with four warps, which is too few loads in flight, 8192 scattered rows took 4 us more), warp 1 issues the MMAs, warps 2-5 are the epilogue, which overlaps the next adapter's blocks
-// where two accumulators fit into TMEM (rank up to 64).
+// Roles (448 threads): warp 0 loads by TMA, warps 6-13 copy rows that lie apart and an adapter's last rows
+// (four warps, too few loads in flight, took 4 us more for 8192 scattered rows) and then zero the gradients
+// of adapters without rows, warp 1 issues the MMAs, warps 2-5 are the epilogue, which overlaps the next
+// adapter's blocks where two accumulators fit into TMEM (rank up to 64).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -323,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     }
   };
   // Stores ranks j .. j + 15 of feature f0 + f of adapter e, f the lane's: neighbouring lanes exchange
-  // halves, so that each has eight ranks of two features and a store touches half the lines.  (64 rows
-  // of 32 adapters, rank 128, 4096 and 4096 features: 88 us in all where each lane stores four ranks of its own, 62 so.)
+  // halves, so that each has eight ranks of two features and a store touches half the lines.  (A backward
+  // call of 64 rows of 32 adapters, rank 128, 4096 and 4096 features, took 88 us where each lane stored four
+  // ranks of its own, 62 so.)
   auto store16 = [&](int e, int f, int j, const float (&v)[16]) {
     const bool odd = lane & 1u;
     uint32_t p[8], even_f[4], odd_f[4];
