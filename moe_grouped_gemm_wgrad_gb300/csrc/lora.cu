@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
     tma_prefetch_desc(&a.tm_w1);
     tma_prefetch_desc(&a.tm_w2);
   }
+  wait_for_launch_before();
 
   RowTile t;
   if (!find_tile<kThreads, kRows>(a.off, a.E, a.M, static_cast<int>(blockIdx.x) / C, s_tmp, a.status, t)) return;
@@ -669,12 +670,13 @@ cudaLaunchConfig_t config(int sets, int cluster, long long tiles, size_t smem, c
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(threads_of(sets)));
   cfg.dynamicSmemBytes = smem;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = dependent_launch();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -688,8 +690,8 @@ long long clusters_at_once(int c) {
   static thread_local int active[kMaxCluster + 1];
   if (asked_ctx == 0 || asked_ctx != current_context_id()) {
     for (int k = 2; k <= kMaxCluster; ++k) {
-      cudaLaunchAttribute attr = {};
-      const cudaLaunchConfig_t cfg = config(kManySets, k, 1, P::smem(P::kLong), &attr);
+      cudaLaunchAttribute attr[2] = {};
+      const cudaLaunchConfig_t cfg = config(kManySets, k, 1, P::smem(P::kLong), attr);
       if (cudaOccupancyMaxActiveClusters(&active[k], lora_kernel<TRANS, RQ, kManySets>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();  // a size that does not fit is no error of the call
         active[k] = 0;
@@ -707,8 +709,8 @@ cudaError_t launch_sets(LoraArgs a, int cluster, long long tiles, cudaStream_t s
   if (err != cudaSuccess) return err;
   a.cluster = cluster;
   a.ring = SETS == 1 ? P::kShort : P::kLong;
-  cudaLaunchAttribute attr = {};
-  cudaLaunchConfig_t cfg = config(SETS, cluster, tiles, P::smem(a.ring), &attr);
+  cudaLaunchAttribute attr[2] = {};
+  cudaLaunchConfig_t cfg = config(SETS, cluster, tiles, P::smem(a.ring), attr);
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, lora_kernel<TRANS, RQ, SETS>, a);
 }

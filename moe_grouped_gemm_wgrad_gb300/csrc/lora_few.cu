@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_few_kernel(const LoraArgs a)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int C = a.cluster;
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  wait_for_launch_before();
   RowTile t;
   if (!find_tile<kThreads, kRows>(a.off, a.E, a.M, static_cast<int>(blockIdx.x) / C, s_tmp, a.status, t)) return;
   if (t.nrows == 0) return;
@@ -248,12 +249,13 @@ cudaLaunchConfig_t config(int cluster, long long tiles, size_t smem, cudaLaunchA
   cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cluster));
   cfg.blockDim = dim3(kThreads);
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = dependent_launch();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -265,8 +267,8 @@ long long clusters_at_once(int c) {
   static thread_local int active[kMaxCluster + 1];
   if (asked_ctx == 0 || asked_ctx != current_context_id()) {
     for (int k = 2; k <= kMaxCluster; ++k) {
-      cudaLaunchAttribute attr = {};
-      const cudaLaunchConfig_t cfg = config(k, 1, Few<NB>::kSmem, &attr);
+      cudaLaunchAttribute attr[2] = {};
+      const cudaLaunchConfig_t cfg = config(k, 1, Few<NB>::kSmem, attr);
       if (cudaOccupancyMaxActiveClusters(&active[k], lora_few_kernel<NB>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();  // a size that does not fit is no error of the call
         active[k] = 0;
@@ -294,8 +296,8 @@ cudaError_t launch(LoraArgs a, cudaStream_t stream) {
   for (int k = 2; k <= most; k *= 2)
     if (likely <= clusters_at_once<NB>(k)) c = k;
   a.cluster = c;
-  cudaLaunchAttribute attr = {};
-  cudaLaunchConfig_t cfg = config(c, tiles, Few<NB>::kSmem, &attr);
+  cudaLaunchAttribute attr[2] = {};
+  cudaLaunchConfig_t cfg = config(c, tiles, Few<NB>::kSmem, attr);
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, lora_few_kernel<NB>, a);
 }

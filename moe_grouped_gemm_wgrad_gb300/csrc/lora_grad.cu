@@ -56,9 +56,6 @@ constexpr int stages_of(int RP) {
 static_assert(stages_of(128) == 3 && stages_of(64) == 4 && stages_of(16) == 6, "ring");
 constexpr size_t part_floats(int RP) { return static_cast<size_t>(kWidth) * RP; }
 
-// The data gradient's launch has ended and its results are there.
-__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The share of the token blocks of CTA p of C.  (At most 2^25 + 1024 blocks, C at most 8.)
 __device__ __forceinline__ int share(int blocks, int p, int C) {
   return static_cast<int>(static_cast<uint32_t>(blocks) * static_cast<uint32_t>(p) / static_cast<uint32_t>(C));
@@ -483,9 +480,7 @@ cudaLaunchConfig_t config(int cluster, long long items, size_t smem, cudaLaunchA
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  // starts while the data gradient's launch ends (programmatic dependent launch)
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1] = dependent_launch();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cfg;
@@ -546,7 +541,7 @@ cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg =
       config(c, items, static_cast<size_t>(a.stages) * stage_bytes(RP) + misc_bytes(a.E), attr);
   cfg.stream = stream;
-  if (a.M == 0) cfg.numAttrs = 1;  // there was no launch before
+  if (a.M == 0) cfg.numAttrs = 1;  // no launch before has seen to it that the offsets are there
   return cudaLaunchKernelEx(&cfg, lora_grad_kernel, a);
 }
 

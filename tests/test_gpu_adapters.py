@@ -367,3 +367,76 @@ def test_rows_past_32_bits():
     got = mgw.grouped_lora_backward(want, x, wu, a, b, small, row_index=index)
     ex = mgw.grouped_lora_backward(want, x[-300:].contiguous(), wu, a, b, small)
     assert all(torch.equal(p, q) for p, q in zip(got, ex))
+
+
+@pytest.mark.parametrize("M", [16, 700, 5000])
+def test_inputs_written_just_before_and_read_just_after(M):
+    """Launches that begin while the one before ends: inputs written, outputs overwritten and read by the
+    launches next to a call's, eagerly, captured, and captured behind a join of two streams."""
+    c = Case([M // 2, M // 3], 32, 512, 520, none=M // 6, mode="tokens")
+    a, b, off, tables = c.a.cuda(), c.b.cuda(), dev(c.off), c.tables()
+    xs = [torch.randn(M // 2 + M // 3 + M // 6, 512, device="cuda").bfloat16() for _ in range(4)]
+    dys = [torch.randn(len(xs[0]), 520, device="cuda").bfloat16() for _ in range(4)]
+    want = []
+    for x, dy in zip(xs, dys):
+        out, u = mgw.grouped_lora(x, a, b, off, save_u=True, **tables)
+        torch.cuda.synchronize()
+        grads = mgw.grouped_lora_backward(dy, x, u, a, b, off, **tables)
+        norm = mgw.clip_grads(list(grads), 0.5)
+        torch.cuda.synchronize()
+        want.append((out, u, *grads, norm))
+    x, dy, noise = torch.empty_like(xs[0]), torch.empty_like(dys[0]), torch.randn(1 << 22, device="cuda")
+    out, u = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+
+    def step(x_now, dy_now, side=None):
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                noise.mul_(1.0)
+                dy.copy_(dy_now)
+        else:
+            dy.copy_(dy_now)
+        out.fill_(9.0)
+        x.copy_(x_now)
+        if side is not None:
+            torch.cuda.current_stream().wait_stream(side)
+        mgw.grouped_lora(x, a, b, off, out=out, u=u, **tables)
+        kept = [out.clone(), u.clone()]
+        out.fill_(7.0)
+        grads = mgw.grouped_lora_backward(dy, x, u, a, b, off, **tables)
+        u.zero_()
+        norm = mgw.clip_grads(list(grads), 0.5)
+        result = (*kept, *[t.clone() for t in grads], norm.clone())
+        for t in grads:
+            t.zero_()
+        return result
+
+    def same(got, ex):
+        return all(torch.equal(p, q) for p, q in zip(got, ex))
+
+    side = torch.cuda.Stream()
+    got = [step(xs[i % 4], dys[i % 4], side if i % 3 == 0 else None) for i in range(24)]
+    torch.cuda.synchronize()
+    assert all(same(g, want[i % 4]) for i, g in enumerate(got))
+    in_x, in_dy = xs[0].clone(), dys[0].clone()
+    for fork in (None, side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(in_x, in_dy, fork)
+        for i in range(8):
+            in_x.copy_(xs[i % 4])
+            in_dy.copy_(dys[i % 4])
+            graph.replay()
+            assert same(got, want[i % 4])
+    # a call as a graph's first node, alone, and two calls in a row
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = mgw.grouped_lora(in_x, a, b, off, save_u=True, **tables)
+        second = mgw.grouped_lora_backward(in_dy, in_x, first[1], a, b, off, **tables)
+    for i in range(4):
+        in_x.copy_(xs[i % 4])
+        in_dy.copy_(dys[i % 4])
+        graph.replay()
+        norm = mgw.clip_grads(list(second), 0.5)
+        assert same((*first, *second, norm), want[i % 4])
+    assert c.status.item() == 0
