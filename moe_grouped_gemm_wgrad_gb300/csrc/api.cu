@@ -90,6 +90,22 @@ MapCache& map_cache() {
 }
 
 // Tiled tensor map of rank 2 or 3: dims[0] contiguous elements, strides in bytes of dims 1, 2.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,
+                const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                CUtensorMapSwizzle swz) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gd[3], gs[2];
+  cuuint32_t bx[3], estr[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) gd[i] = dims[i], bx[i] = box[i];
+  for (int i = 0; i + 1 < rank; ++i) gs[i] = strides[i];
+  std::memset(m, 0, sizeof(*m));
+  return fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), gd, gs, bx, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same through the table.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,
               const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
               CUtensorMapSwizzle swz) {
@@ -110,17 +126,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank
         return true;
       }
   }
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t gd[3], gs[2];
-  cuuint32_t bx[3], estr[3] = {1, 1, 1};
-  for (int i = 0; i < rank; ++i) gd[i] = dims[i], bx[i] = box[i];
-  for (int i = 0; i + 1 < rank; ++i) gs[i] = strides[i];
-  std::memset(m, 0, sizeof(*m));
-  if (fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), gd, gs, bx, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  if (!encode_map(m, dt, base, rank, dims, strides, box, swz)) return false;
   std::lock_guard<std::mutex> lock(c.mu);
   const int slot = c.used < kMapCacheSize ? c.used++ : (c.next++ % kMapCacheSize);
   c.key[slot] = k;
@@ -886,15 +892,16 @@ mgw_status lora_check(const void* x, int x_rows, const int32_t* row_index, int M
 
 // 64-column boxes of `rows` rows of a bf16 matrix [total, cols].
 bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t total, uint32_t rows) {
-  return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, total, cols * 2, 64, rows,
-                     CU_TENSOR_MAP_SWIZZLE_128B);
+  const uint64_t dims[2] = {cols, total}, strides[1] = {cols * 2};
+  const uint32_t box[2] = {64, rows};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // 64 x `rows` boxes of the bf16 matrices [E, outer, inner]: a box never reaches into the next one.
 bool stack_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t E, uint32_t rows) {
   const uint64_t dims[3] = {inner, outer, E};
   const uint64_t strides[2] = {inner * 2, inner * outer * 2};
   const uint32_t box[3] = {64, rows, 1};
-  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The kernel of lora.cu on W1 [E, R, K] and W2 [E, N, R] (transposed: [E, K, R] and [E, R, N]).
