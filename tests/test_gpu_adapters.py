@@ -19,6 +19,16 @@ import adapter_reference as ref
 from moe_grouped_gemm_wgrad_gb300 import build, mgw
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def own_random_numbers():
+    """Leaves torch's generators as it found them: other tests draw their inputs from them."""
+    with torch.random.fork_rng(devices=[0]):
+        torch.manual_seed(1)
+        yield
+
+
 EPS = 2.0 ** -8  # half a step of bf16
 
 

@@ -14,6 +14,16 @@ import adapter_reference as ref
 from moe_grouped_gemm_wgrad_gb300 import build, mgw
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def own_random_numbers():
+    """Leaves torch's generators as it found them: other tests draw their inputs from them."""
+    with torch.random.fork_rng(devices=[0]):
+        torch.manual_seed(1)
+        yield
+
+
 TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
