@@ -104,9 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
   __syncthreads();
   int bad = 0, mine = 0;
   for (int i = tid; i < E; i += kThreads) {
-    const int n = s_off[i + 1] - s_off[i];
-    bad |= n < 0;
-    mine += (n + kTok - 1) / kTok;
+    // compared, not subtracted: the difference of offsets that are none may wrap to a positive number
+    bad |= s_off[i + 1] < s_off[i];
+    mine += (s_off[i + 1] - s_off[i] + kTok - 1) / kTok;
   }
   if (tid == 0) bad |= s_off[0] != 0 || s_off[E] > a.M;
   mine = __reduce_add_sync(0xffffffffu, mine);
