@@ -180,9 +180,9 @@ __global__ void __launch_bounds__(kWarps * 32) act_dbias_kernel(ActBwdArgs a) {
   // the expert's first tile on the padded axis, and the offsets' check, in one pass
   int bad = threadIdx.x == 0 && (a.expert_off[0] != 0 || a.expert_off[a.E] != a.M), before = 0;
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
-    const int c = a.expert_off[i + 1] - a.expert_off[i];
-    bad |= c < 0;
-    if (i < e) before += (c + 127) & ~127;
+    const int lo = a.expert_off[i], hi = a.expert_off[i + 1];
+    bad |= hi < lo;  // not hi - lo < 0, which may wrap
+    if (i < e) before += (hi - lo + 127) & ~127;
   }
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane_id() == 0 && before != 0) atomicAdd(&s_first, before);
