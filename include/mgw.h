@@ -498,8 +498,10 @@ mgw_status mgw_moe_combine_backward(const void *dout, const void *y, int dtype, 
  * base        device, bf16 [out_rows, N], nullable (0); may be out itself.
  * out_index   device int32 [M], nullable (then out_rows >= M).  No two rows name one row of out;
  *             rows of out that no row names are not written.
- * out         device, bf16 [out_rows, N].
+ * out         device, bf16 [out_rows, N]; may lie in x's matrix (out == x, K == N) where no row
+ *             reads a row of x that another row writes.
  * u           device fp32 [M, R], nullable: the intermediate, for the backward pass.
+ * Otherwise out and u overlap neither each other nor an input (else MGW_ERR_INVALID_ARG).
  * K, N, R multiples of 8 (pad an adapter's rank with zeros), R <= MGW_MAX_RANK, K, N <= 2^23, M <=
  * 2^30 (else MGW_ERR_UNSUPPORTED).  An index out of range sets MGW_DEV_BAD_INDEX: a row of x then counts as
  * zeros, a row of out is not written. */
@@ -519,11 +521,13 @@ mgw_status mgw_grouped_lora(const void *x_bf16, int x_rows, const int32_t *row_i
  * adapter dx_base.  All sums are fp32, in an order that the sizes and the device fix; each output is
  * rounded once.
  * dy, dx_base device, bf16 [out_rows, N] and [out_rows, K] (dx_base nullable (0); may be dx).
- * dx          device, bf16 [out_rows, K], nullable.
+ * dx          device, bf16 [out_rows, K], nullable; may be dy itself (K == N) where da and db are null.
  * da, db      device, bf16 [E, R, K] and [E, N, R], fully written; both or (null) neither.
  * x, u        (fp32 [M, R] from the forward call) are needed with da and db only.
  * workspace   device, 16-byte aligned, mgw_grouped_lora_backward_workspace_bytes bytes, when da and
  *             db are given; need not be initialised.  Calls sharing it must not overlap.
+ * Otherwise outputs and workspace overlap neither each other nor an input that the call reads
+ * (else MGW_ERR_INVALID_ARG).
  * Everything else as in the forward call. */
 mgw_status mgw_grouped_lora_backward(const void *dy_bf16, int out_rows, const int32_t *out_index,
                                      const void *x_bf16, int x_rows, const int32_t *row_index,

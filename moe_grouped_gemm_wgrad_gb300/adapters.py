@@ -91,8 +91,9 @@ def grouped_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_off:
     out's row out_index[r] (r itself without an index).  Rows behind adapter_off[E] have no adapter
     and keep their base.  For requests in token order both indices are the row_index of
     :func:`moe_dispatch` (top_k 1; an extra last expert for tokens without an adapter, whose offset
-    is left out of ``adapter_off``).  ``base`` is 0 when not given, and may be ``out``.  Rows of out
-    that ``out_index`` does not name are not written."""
+    is left out of ``adapter_off``).  ``base`` is 0 when not given, and may be ``out``, as may x (of
+    as many columns) where no row reads a row of x that another writes; other overlaps of outputs and
+    inputs are refused.  Rows of out that ``out_index`` does not name are not written."""
     fit = _fit(x, a, b, adapter_off, row_index, out_index, scale, base)
     if not fit:
         mgw._dev_tensor(x, torch.bfloat16, "x", 2)
@@ -141,7 +142,8 @@ def grouped_lora_backward(dy: torch.Tensor, x: torch.Tensor | None, u: torch.Ten
     dx [rows of out, K] bf16 = dx_base + the adapters' share (rows without an adapter: dx_base, 0
     when not given; ``dx_base`` may be ``dx``), da [E, R, K] and db [E, N, R] bf16; ``x`` and ``u``
     as in the forward call.  Without ``with_dx`` dx is None; without ``with_weights`` da and db are,
-    and ``x`` and ``u`` may be None.  ``workspace`` (uint8) is allocated when none is given."""
+    and ``x`` and ``u`` may be None, and ``dx`` may be dy (of as many columns).  Other overlaps of
+    outputs and inputs are refused.  ``workspace`` (uint8) is allocated when none is given."""
     if not with_dx and (dx is not None or dx_base is not None):
         raise mgw.MgwError("dx and dx_base need with_dx")
     if not with_weights and (da is not None or db is not None):

@@ -890,6 +890,30 @@ mgw_status lora_check(const void* x, int x_rows, const int32_t* row_index, int M
   return MGW_OK;
 }
 
+// Memory that a call reads or writes.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+Span span(const void* at, int64_t count, int64_t width, size_t size) {
+  return {at, at ? static_cast<size_t>(count) * static_cast<size_t>(width) * size : 0};
+}
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+  return a.bytes > 0 && b.bytes > 0 && p < q + b.bytes && q < p + a.bytes;
+}
+// True where a written span meets another of them or one that is read.
+template <size_t W, size_t R>
+bool clash(const Span (&written)[W], const Span (&read)[R]) {
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(written[i], written[j])) return true;
+    for (const Span& r : read)
+      if (overlap(written[i], r)) return true;
+  }
+  return false;
+}
+
 // 64-column boxes of `rows` rows of a bf16 matrix [total, cols].
 bool rows_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t total, uint32_t rows) {
   const uint64_t dims[2] = {cols, total}, strides[1] = {cols * 2};
@@ -963,6 +987,16 @@ mgw_status mgw_grouped_lora(const void* x_bf16, int x_rows, const int32_t* row_i
   if (st != MGW_OK) return st;
   if (M > 0 && (!out_bf16 || x_rows < 1 || out_rows < 1)) return MGW_ERR_INVALID_ARG;
   if (!aligned16(base_bf16) || !aligned16(out_bf16) || !aligned16(u)) return MGW_ERR_INVALID_ARG;
+  if (M > 0) {
+    // out may be base itself, and x's matrix: a tile has read its rows before it writes any
+    const Span written[] = {span(out_bf16, out_rows, N, 2), span(u, M, R, 4)};
+    const Span read[] = {span(x_bf16 == out_bf16 && K == N ? nullptr : x_bf16, x_rows, K, 2),
+                         span(base_bf16 == out_bf16 ? nullptr : base_bf16, out_rows, N, 2),
+                         span(a_bf16, E, int64_t(R) * K, 2), span(b_bf16, E, int64_t(N) * R, 2),
+                         span(scale, E, 1, 4), span(adapter_off, E + 1, 1, 4), span(row_index, M, 1, 4),
+                         span(out_index, M, 1, 4)};
+    if (clash(written, read)) return MGW_ERR_INVALID_ARG;
+  }
   DeviceInfo dev;
   st = current_device(&dev);
   if (st != MGW_OK || M == 0) return st;
@@ -995,6 +1029,19 @@ mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const in
     const size_t need = mgw_grouped_lora_backward_workspace_bytes(E, M, K, N, R);
     if (need > 0 && !workspace) return MGW_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MGW_ERR_CAPACITY;
+  }
+  {
+    // dx may be dx_base itself, and dy where nothing reads that again
+    const bool dy_again = weights || dx_bf16 != dy_bf16 || K != N;
+    const Span written[] = {span(dx_bf16, out_rows, K, 2), span(da_bf16, E, int64_t(R) * K, 2),
+                            span(db_bf16, E, int64_t(N) * R, 2), span(weights ? workspace : nullptr, workspace_bytes, 1, 1)};
+    const Span read[] = {span(dy_again ? dy_bf16 : nullptr, out_rows, N, 2),
+                         span(dx_base_bf16 == dx_bf16 ? nullptr : dx_base_bf16, out_rows, K, 2),
+                         span(weights ? x_bf16 : nullptr, x_rows, K, 2), span(weights ? u : nullptr, M, R, 4),
+                         span(a_bf16, E, int64_t(R) * K, 2), span(b_bf16, E, int64_t(N) * R, 2),
+                         span(scale, E, 1, 4), span(adapter_off, E + 1, 1, 4), span(row_index, M, 1, 4),
+                         span(out_index, M, 1, 4)};
+    if (clash(written, read)) return MGW_ERR_INVALID_ARG;
   }
   DeviceInfo dev;
   st = current_device(&dev);

@@ -27,3 +27,46 @@ def test_offsets_whose_differences_wrap_are_reported(M):
                                   db=outs[3], **c.tables())
         assert c.status.item() == mgw.MGW_DEV_BAD_OFFSETS and (uu == 7).all() and all((t == 7).all() for t in outs)
         c.status.zero_()
+
+
+@pytest.mark.parametrize("M", [30, 900, 3000])
+@pytest.mark.parametrize("mode", ["tokens", "plain"])
+def test_outputs_that_may_lie_on_an_input(M, mode):
+    """x's own matrix (and base's at once) for out, dy's for dx without the adapters' gradients; rows in order,
+    whose base and output go through one slot, and rows that lie apart."""
+    c = Case([M // 2, 0, M // 3], 24, 264, 264, none=M // 6, mode=mode)
+    want, u = c.forward()
+    c.check_forward(want, u)
+    a, b, off, tables = c.a.cuda(), c.b.cuda(), torch.from_numpy(c.off).cuda(), c.tables()
+    for base in (c.base.cuda(), None, "x"):
+        x = c.x.cuda()
+        ex, eu = mgw.grouped_lora(x, a, b, off, base=c.x.cuda() if base == "x" else base, save_u=True, **tables)
+        got, gu = mgw.grouped_lora(x, a, b, off, base=x if base == "x" else base, out=x, save_u=True, **tables)
+        assert got is x and torch.equal(got, ex) and torch.equal(gu, eu)
+    out = c.base.cuda()
+    assert torch.equal(mgw.grouped_lora(c.x.cuda(), a, b, off, base=out, out=out, **tables), want)
+    wdx = c.backward(u)[0]
+    dx = c.dx_base.cuda()
+    got = mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, a, b, off, dx_base=dx, dx=dx, **tables)
+    assert torch.equal(got[0], wdx)
+    dy = c.dy.cuda()
+    got = mgw.grouped_lora_backward(dy, None, None, a, b, off, dx_base=c.dx_base.cuda(), dx=dy, with_weights=False, **tables)
+    assert got[0] is dy and torch.equal(dy, wdx) and c.status.item() == 0
+
+
+def test_outputs_that_may_not():
+    c = Case([20, 11], 16, 64, 64, mode="plain")
+    out, u = c.forward()
+    a, b, off, x, dy, tables = c.a.cuda(), c.b.cuda(), torch.from_numpy(c.off).cuda(), c.x.cuda(), c.dy.cuda(), c.tables()
+    twice = torch.empty(2 * c.M - 5, 64, dtype=torch.bfloat16, device="cuda")
+    kept = [t.clone() for t in (x, dy, a, b, u)]
+    for call in (lambda: mgw.grouped_lora_backward(dy, x, u, a, b, off, dx=dy, **tables),
+                 lambda: mgw.grouped_lora_backward(dy, x, u, a, b, off, dx=x, **tables),
+                 lambda: mgw.grouped_lora_backward(dy, x, u, a, b, off, da=a, **tables),
+                 lambda: mgw.grouped_lora_backward(dy, x, u, a, b, off, db=b, **tables),
+                 lambda: mgw.grouped_lora_backward(dy, x, u, a, b, off, dx_base=twice[:c.M], dx=twice[c.M - 5:], **tables),
+                 lambda: mgw.grouped_lora(x, a, b, off, base=twice[:c.M], out=twice[c.M - 5:], **tables),
+                 lambda: mgw.grouped_lora(twice[:c.M], a, b, off, out=twice[c.M - 5:], **tables)):
+        with pytest.raises(mgw.MgwError, match="invalid"):
+            call()
+    assert all(torch.equal(p, q) for p, q in zip(kept, (x, dy, a, b, u))) and c.status.item() == 0
