@@ -561,8 +561,9 @@ mgw_status mgw_grad_norm(const void *const *grads, const int64_t *sizes, const i
  * norm_in    device fp32, nullable: a norm known already (of several processes' gradients, say).
  *            Null: the norm of the gradients, which is written to `norm`; exactly one of the two
  *            is given.
- * An infinite norm gives factor 0 (and infinities times 0 are none); a norm that is not a number
- * makes every gradient none.
+ * An infinite norm gives factor 0 (and infinities times 0 are none), also for an infinite max_norm,
+ * which otherwise gives 1; max_norm = 0 gives 0, also for a norm of 0 without eps; a norm that is
+ * not a number makes every gradient none.
  * workspace  as for mgw_grad_norm. */
 mgw_status mgw_grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
                          const int *dtypes, int n, float max_norm, float eps,

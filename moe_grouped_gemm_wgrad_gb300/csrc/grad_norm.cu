@@ -263,7 +263,11 @@ __device__ __forceinline__ Share sum_chunks(const Table<CAP>& a, int c0, int c1,
 }
 
 // min(1, max_norm / (norm + eps)), but not for a norm that is not a number: then every gradient is none.
+// Where the quotient would be none for numbers: an infinite norm gives 0 whatever max_norm, max_norm = 0
+// gives 0 whatever the norm, and an infinite max_norm limits nothing.
 __device__ __forceinline__ float clip_factor(float max_norm, float norm, float eps) {
+  if (norm == INFINITY || (max_norm == 0.0f && norm == norm)) return 0.0f;
+  if (max_norm == INFINITY && norm == norm) return 1.0f;
   const float f = max_norm / (norm + eps);
   return f > 1.0f ? 1.0f : f;
 }
