@@ -490,7 +490,8 @@ mgw_status mgw_moe_combine_backward(const void *dout, const void *y, int dtype, 
  * o(r) = out_index[r], or r itself without the index.  Rows behind adapter_off[E] have no
  * adapter: out = base there, and u = 0.
  * Sums are fp32, out is rounded once; the intermediate enters the second product as two bf16
- * parts (17 bits).
+ * parts (17 bits).  The tensor core cuts each addition (of 16 products) off below its accumulator's
+ * last bit: u may be off by (K / 32 + 16) 2^-23 of sum |x| |a|.
  * x           device, bf16 [x_rows, K]; row_index device int32 [M], nullable (then x_rows >= M).
  * a           device, bf16 [E, R, K];  b: device, bf16 [E, N, R].
  * scale       device fp32 [E], nullable (1).
@@ -519,7 +520,9 @@ mgw_status mgw_grouped_lora(const void *x_bf16, int x_rows, const int32_t *row_i
  * (the gradient to base is dy).  dx has the rows of dy: a layer that gathers rows of x several
  * times adds them up with mgw_moe_combine.  Adapters without rows get zeros; rows without an
  * adapter dx_base.  All sums are fp32, in an order that the sizes and the device fix; each output is
- * rounded once.
+ * rounded once.  The tensor core cuts each addition (of 16 products) off below its accumulator's last
+ * bit: v may be off by (N / 32 + 16) 2^-23 of sum |dy| |b|, a gradient besides by 2^-13 of its sum
+ * of absolute values, and by 2^-24 of that for every 16384 rows, which are added up in fp32.
  * dy, dx_base device, bf16 [out_rows, N] and [out_rows, K] (dx_base nullable (0); may be dx).
  * dx          device, bf16 [out_rows, K], nullable; may be dy itself (K == N) where da and db are null.
  * da, db      device, bf16 [E, R, K] and [E, N, R], fully written; both or (null) neither.

@@ -1006,7 +1006,7 @@ mgw_status mgw_grouped_lora(const void* x_bf16, int x_rows, const int32_t* row_i
 
 size_t mgw_grouped_lora_backward_workspace_bytes(int E, int M, int K, int N, int R) {
   if (E < 1 || E > MGW_MAX_EXPERTS || M < 0 || K <= 0 || N <= 0 || R <= 0 || R > MGW_MAX_RANK) return 0;
-  return 2 * mgw::lora_q_bytes(M, E, R) + mgw::lora_partial_bytes(K, N, R);
+  return 2 * mgw::lora_q_bytes(M, E, R) + mgw::lora_partial_bytes(M, K, N, R);
 }
 
 mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const int32_t* out_index,

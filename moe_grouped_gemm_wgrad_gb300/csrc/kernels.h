@@ -263,7 +263,7 @@ struct LoraGradArgs {
   int* status;
 };
 size_t lora_q_bytes(int M, int E, int R);
-size_t lora_partial_bytes(int K, int N, int R);
+size_t lora_partial_bytes(int M, int K, int N, int R);
 cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream);
 
 // Gradient norm and clipping (grad_norm.cu): host arrays of `count` tensors.

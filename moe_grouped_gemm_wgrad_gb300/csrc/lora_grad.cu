@@ -43,6 +43,13 @@ constexpr int kWidth = 256;        // features per CTA
 constexpr int kXBytes = 4 * 8192;  // 64 tokens of 256 features
 constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 8;
+// Token blocks that one accumulator takes.  The tensor core cuts each addition's low bits off, always
+// downwards: of a sum that only grows 1.1e-7 an addition, one for every 16 rows.  In one accumulator a
+// million rows came out 0.7% too small, four million 2.8%; 16384 rows are off by 1e-4, where half a step of a
+// bf16 gradient is 2e-3 to 4e-3.  Longer runs are added up in fp32 in the workspace: the sums of 256 features
+// (64 KB at rank 64) read and written once for every 8 MB of X.  65536 rows, 8192 and 8192 features, rank 64:
+// backward 832 -> 836 us, rank 128 1028 -> 1038 (there is one accumulator, and the products wait for it).
+constexpr int kChain = 256;
 constexpr int kSms = 152;          // of a GB300: the workspace's size has no device to ask
 constexpr int kBarBytes = 8 * (2 * kMaxStages + 4);
 
@@ -201,32 +208,35 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     bool ok = true;
     int stage = 0, i = 0;
     uint32_t phase = 0;
-    for (; ok && w.next(t0, t1, E); ++i) {
-      const int buf = bufs == 2 ? i & 1 : 0, use = bufs == 2 ? i >> 1 : i;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_free(buf), (use & 1) ^ 1u, abort_flag));
-      const uint32_t d = tmem + static_cast<uint32_t>(buf * 4 * RP);
-      for (int b = w.b0; ok && b < w.b1; ++b) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag));
-        if (!ok) break;
-        fence_async_smem();  // copied rows are generic writes
-        tc_fence_after();
-        const uint32_t sx = sbase + stage * stage_bytes(RP);
-        const int steps = (min(kTok, w.n - b * kTok) + 15) >> 4;
-        if (issue) {
-          const uint64_t bd = sdesc_kmajor_sw128(sx + kXBytes);
+    while (ok && w.next(t0, t1, E)) {
+      for (int c0 = w.b0; ok && c0 < w.b1; c0 += kChain, ++i) {
+        const int c1 = min(w.b1, c0 + kChain);
+        const int buf = bufs == 2 ? i & 1 : 0, use = bufs == 2 ? i >> 1 : i;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_free(buf), (use & 1) ^ 1u, abort_flag));
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * 4 * RP);
+        for (int b = c0; ok && b < c1; ++b) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(stage), phase, abort_flag));
+          if (!ok) break;
+          fence_async_smem();  // copied rows are generic writes
+          tc_fence_after();
+          const uint32_t sx = sbase + stage * stage_bytes(RP);
+          const int steps = (min(kTok, w.n - b * kTok) + 15) >> 4;
+          if (issue) {
+            const uint64_t bd = sdesc_kmajor_sw128(sx + kXBytes);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t ad = sdesc_mn_sw128(sx + h * 16384, 8192);
-            for (int k = 0; k < steps; ++k)
-              mma_bf16(d + h * 2 * RP, ad + kStepMn * k, bd + kStepK * k, idesc, b != w.b0 || k != 0);
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t ad = sdesc_mn_sw128(sx + h * 16384, 8192);
+              for (int k = 0; k < steps; ++k)
+                mma_bf16(d + h * 2 * RP, ad + kStepMn * k, bd + kStepK * k, idesc, b != c0 || k != 0);
+            }
+            mma_commit(bar_empty(stage));
           }
-          mma_commit(bar_empty(stage));
+          __syncwarp();
+          if (++stage == S) stage = 0, phase ^= 1u;
         }
+        if (ok && issue) mma_commit(bar_acc(buf));
         __syncwarp();
-        if (++stage == S) stage = 0, phase ^= 1u;
       }
-      if (ok && issue) mma_commit(bar_acc(buf));
-      __syncwarp();
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -365,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     }
   };
   // Partial sums of a CTA: those of the adapter that reaches in from the share before (0) and of the
-  // one that reaches out into the next (1), [RP / 4][256 features] of four ranks.
+  // one that reaches out into the next (1; before it, of long adapters within the share in turn),
+  // [RP / 4][256 features] of four ranks.
   auto partial = [&](int p, int slot) {
     return reinterpret_cast<float4*>(a.partial) +
            ((static_cast<size_t>(blockIdx.x) / C * C + p) * 2 + slot) * (part_floats(RP) / 4);
@@ -374,38 +385,55 @@ __global__ void __launch_bounds__(kThreads, 1) lora_grad_kernel(const __grid_con
     // ------------------------------------------------------------ epilogue
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     bool ok = true;
-    for (int i = 0; ok && w.next(t0, t1, E); ++i) {
-      const int buf = bufs == 2 ? i & 1 : 0, use = bufs == 2 ? i >> 1 : i;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_acc(buf), use & 1, abort_flag)) && !*abort_flag;
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
+    int i = 0;
+    while (ok && w.next(t0, t1, E)) {
       const bool whole = w.b0 == 0 && w.b1 == (w.n + kTok - 1) / kTok;
       float4* to = partial(rank, w.b0 > 0 ? 0 : 1);
-      for (int h = 0; h < 2; ++h) {
-        const int f = h * 128 + static_cast<int>(quarter * 32 + lane);
-        for (int j = 0; j < RP; j += 16) {
-          uint32_t x[16], y[16];
-          const uint32_t ta = tmem + (quarter * 32u << 16) + buf * 4 * RP + h * 2 * RP + j;
-          tmem_ld_x16(ta, x);
-          tmem_ld_x16(ta + RP, y);
-          tmem_wait_ld();
-          tmem_loaded(x);
-          tmem_loaded(y);
-          float v[16];
+      for (int c0 = w.b0; c0 < w.b1; c0 += kChain, ++i) {
+        const int buf = bufs == 2 ? i & 1 : 0, use = bufs == 2 ? i >> 1 : i;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_acc(buf), use & 1, abort_flag)) && !*abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool store = whole && c0 + kChain >= w.b1;
+        for (int h = 0; h < 2; ++h) {
+          const int f = h * 128 + static_cast<int>(quarter * 32 + lane);
+          for (int j = 0; j < RP; j += 16) {
+            uint32_t x[16], y[16];
+            const uint32_t ta = tmem + (quarter * 32u << 16) + buf * 4 * RP + h * 2 * RP + j;
+            tmem_ld_x16(ta, x);
+            tmem_ld_x16(ta + RP, y);
+            float4 before[4];  // this thread's own sums of the runs before
+            if (c0 != w.b0) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(x[q]) + __uint_as_float(y[q]);
-          if (whole) {
-            store16(w.e, f, j, v);
-          } else {
+              for (int q = 0; q < 4; ++q) before[q] = to[(j / 4 + q) * kWidth + f];
+            }
+            tmem_wait_ld();
+            tmem_loaded(x);
+            tmem_loaded(y);
+            float v[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              to[(j / 4 + q) * kWidth + f] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(x[q]) + __uint_as_float(y[q]);
+            if (c0 != w.b0) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[4 * q] += before[q].x, v[4 * q + 1] += before[q].y;
+                v[4 * q + 2] += before[q].z, v[4 * q + 3] += before[q].w;
+              }
+            }
+            if (store) {
+              store16(w.e, f, j, v);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                to[(j / 4 + q) * kWidth + f] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_free(buf));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_free(buf));
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -514,10 +542,13 @@ size_t lora_q_bytes(int M, int E, int R) {
   return static_cast<size_t>(tiles) * 2 * 256 * padded_rank(R);
 }
 
-size_t lora_partial_bytes(int K, int N, int R) {
-  // clusters of several CTAs only where all CTAs together are at most kSms
-  if (2 * (items_of(K) + items_of(N)) > kSms) return 0;
-  return sizeof(float) * kSms * 2 * part_floats(padded_rank(R));
+size_t lora_partial_bytes(int M, int K, int N, int R) {
+  // Clusters of several CTAs only where all CTAs together are at most kSms; a CTA by itself needs room where
+  // an adapter's rows take several runs.
+  const long long items = items_of(K) + items_of(N);
+  long long ctas = 2 * items <= kSms ? kSms : 0;
+  if (M > kChain * kTok && ctas < items) ctas = items;
+  return sizeof(float) * static_cast<size_t>(ctas) * 2 * part_floats(padded_rank(R));
 }
 
 cudaError_t launch_lora_grad(LoraGradArgs a, cudaStream_t stream) {

@@ -1,12 +1,39 @@
 """The adapter operators at the limits of what a call may name: tables that are none, aliases, long sums,
 every build of the kernels; against 64 bits with the tolerances of test_gpu_adapters.py."""
+import ctypes
+
 import pytest
 import torch
 
-from moe_grouped_gemm_wgrad_gb300 import mgw
-from test_gpu_adapters import Case, own_random_numbers  # noqa: F401 (a fixture)
+from moe_grouped_gemm_wgrad_gb300 import build, mgw
+from test_gpu_adapters import EPS, Case, own_random_numbers  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def clusters(monkeypatch):
+    """A function that limits the clusters' size (the test build of the library takes the limit)."""
+    def limit(most):
+        hooks = mgw.bind(ctypes.CDLL(build.LIB_TESTHOOKS))
+        monkeypatch.setattr(mgw, "load", lambda: hooks)
+        monkeypatch.setenv("MGW_TEST_MAX_CLUSTER", str(most))
+    return limit
+
+
+def gradients_64(dy, x, u, b, off, index=None):
+    """[(value, sum of absolute values)] of da and of db, on the GPU, scale 1."""
+    grads = []
+    rows = torch.arange(int(off[-1]), device="cuda") if index is None else index.long()
+    for f in (lambda t: t.double(), lambda t: t.double().abs()):
+        da, db = [], []
+        for e in range(len(off) - 1):
+            r = slice(int(off[e]), int(off[e + 1]))
+            g, xe = f(dy[rows[r]]), f(x[rows[r]])
+            da.append((g @ f(b[e])).t() @ xe)
+            db.append(g.t() @ f(u[r]))
+        grads.append((torch.stack(da), torch.stack(db)))
+    return [(grads[0][i], grads[1][i]) for i in range(2)]
 
 
 @pytest.mark.parametrize("M", [24, 500, 1400])
@@ -70,3 +97,87 @@ def test_outputs_that_may_not():
         with pytest.raises(mgw.MgwError, match="invalid"):
             call()
     assert all(torch.equal(p, q) for p, q in zip(kept, (x, dy, a, b, u))) and c.status.item() == 0
+
+
+# A run of 256 blocks of 64 rows: 1024 additions of the tensor core, each cut off below 2^-23 of a sum no
+# larger than that of the absolute values; a few, and one for every run, in fp32.
+def run_error(runs):
+    return (1024 + 64) * 2.0 ** -23 + runs * 2.0 ** -24
+
+
+@pytest.mark.parametrize("most", [1, 8])
+@pytest.mark.parametrize("M,R", [(1 << 22, 8), (1 << 20, 128)])
+def test_long_sums_of_one_sign(clusters, M, R, most):
+    """Sums that only grow, where additions that cut off would add up: one adapter, millions of rows."""
+    clusters(most)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = (torch.rand(M, 16, generator=g, device="cuda") + 1).bfloat16()
+    dy = (torch.rand(M, 24, generator=g, device="cuda") + 1).bfloat16()
+    u = torch.rand(M, R, generator=g, device="cuda") + 1
+    a = (torch.rand(1, R, 16, generator=g, device="cuda") + 1).bfloat16()
+    b = (torch.rand(1, 24, R, generator=g, device="cuda") + 1).bfloat16()
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    _, da, db = mgw.grouped_lora_backward(dy, x, u, a, b, off, with_dx=False)
+    first = (24 + 64) * 2.0 ** -23
+    for got, (want, size), before in zip((da, db), gradients_64(dy, x, u, b, off.tolist()), (first, 0.0)):
+        err = (before + 2.0 ** -16 + run_error(M // 16384 + 1)) * size
+        assert ((got.double() - want).abs() <= EPS * (want.abs() + err) + err).all()
+
+
+@pytest.mark.parametrize("most", [1, 2, 3, 8])
+@pytest.mark.parametrize("R", [8, 64, 72, 128])
+@pytest.mark.parametrize("gathered", [False, True])
+def test_adapters_around_a_run(clusters, R, most, gathered):
+    """Adapters of one run and a row, of several, and of few rows, within a CTA's share and across shares."""
+    clusters(most)
+    counts = [16384, 5, 16385, 40001, 0, 16383, 70000, 1, 300, 33000]
+    g = torch.Generator(device="cuda").manual_seed(R)
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    M = off[-1]
+    x = torch.randn(M, 264, generator=g, device="cuda").bfloat16()
+    dy = torch.randn(M, 72, generator=g, device="cuda").bfloat16()
+    a = (torch.randn(len(counts), R, 264, generator=g, device="cuda") / 16).bfloat16()
+    b = (torch.randn(len(counts), 72, R, generator=g, device="cuda") / 8).bfloat16()
+    perm = torch.randperm(M, generator=g, device="cuda").int() if gathered else None
+    table = torch.tensor(off, dtype=torch.int32, device="cuda")
+    u = torch.randn(M, R, generator=g, device="cuda")
+    need = mgw.load().mgw_grouped_lora_backward_workspace_bytes(len(counts), M, 264, 72, R)
+    room = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")   # nothing is read before it is written
+    dx, da, db = mgw.grouped_lora_backward(dy, x, u, a, b, table, row_index=perm, out_index=perm, workspace=room[:need])
+    first = (72 + 64) * 2.0 ** -23 + 2.0 ** -16
+    for got, (want, size), before in zip((da, db), gradients_64(dy, x, u, b, off, perm), (first, 2.0 ** -16)):
+        err = (before + run_error(5)) * size
+        assert ((got.double() - want).abs() <= EPS * (want.abs() + err) + err).all()
+    assert (room[need:] == 171).all()
+    again = mgw.grouped_lora_backward(dy, x, u, a, b, table, row_index=perm, out_index=perm)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], da) and torch.equal(again[2], db)
+
+
+def test_long_adapters_of_many_features():
+    """More feature blocks than a cluster each leaves room for: CTAs by themselves, with sums in the workspace."""
+    M, K, N, R = 16500, 16384, 4096, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    dy = torch.randn(M, N, generator=g, device="cuda").bfloat16()
+    u = torch.randn(M, R, generator=g, device="cuda")
+    a = (torch.randn(2, R, K, generator=g, device="cuda") / 128).bfloat16()
+    b = (torch.randn(2, N, R, generator=g, device="cuda") / 8).bfloat16()
+    off = torch.tensor([0, 60, M], dtype=torch.int32, device="cuda")
+    need = mgw.load().mgw_grouped_lora_backward_workspace_bytes(2, M, K, N, R)
+    assert need - mgw.load().mgw_grouped_lora_backward_workspace_bytes(2, 16384, K, N, R) >= 80 * 2 * 256 * R * 4
+    room = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    _, da, db = mgw.grouped_lora_backward(dy, x, u, a, b, off, with_dx=False, workspace=room[:need])
+    assert (room[need:] == 171).all()
+    first = (N + 64) * 2.0 ** -23 + 2.0 ** -16
+    cols = torch.cat([torch.arange(300), torch.arange(K - 300, K)]).cuda()   # 64-bit products are slow: some columns
+    wants = gradients_64(dy[:, :256].contiguous(), x[:, :8].contiguous(), u, b[:, :256].contiguous(), [0, 60, M])
+    got, (want, size) = db[:, :256], wants[1]
+    err = (2.0 ** -16 + run_error(2)) * size
+    assert ((got.double() - want).abs() <= EPS * (want.abs() + err) + err).all()
+    for e, r in ((0, slice(0, 60)), (1, slice(60, M))):
+        v, vs = dy[r].double() @ b[e].double(), dy[r].double().abs() @ b[e].double().abs()
+        want, size = v.t() @ x[r][:, cols].double(), vs.t() @ x[r][:, cols].double().abs()
+        err = (first + run_error(2)) * size
+        assert ((da[e][:, cols].double() - want).abs() <= EPS * (want.abs() + err) + err).all()
