@@ -181,3 +181,27 @@ def test_long_adapters_of_many_features():
         want, size = v.t() @ x[r][:, cols].double(), vs.t() @ x[r][:, cols].double().abs()
         err = (first + run_error(2)) * size
         assert ((da[e][:, cols].double() - want).abs() <= EPS * (want.abs() + err) + err).all()
+
+
+@pytest.mark.parametrize("R", [24, 64, 128])
+@pytest.mark.parametrize("mode", ["plain", "tokens", "gather"])
+def test_every_build_with_more_tiles_than_sms(R, mode):
+    """Two CTAs to an SM (one of rank 128, in several waves), with base and dx_base, in order and apart, in
+    place too; tiles that end before, at and behind 64 rows."""
+    counts = [9000, 63, 64, 65, 128 + 63, 128 + 64, 128 + 65, 0, 10100, 127, 1, 1300]
+    c = Case(counts, R, 200, 456, none=77, mode=mode)
+    out, u = c.forward()
+    c.check_forward(out, u)
+    got = c.backward(u)
+    c.check_backward(u, *got)
+    base, dx = c.base.cuda(), c.dx_base.cuda()
+    a, b, off = c.a.cuda(), c.b.cuda(), torch.from_numpy(c.off).cuda()
+    assert torch.equal(mgw.grouped_lora(c.x.cuda(), a, b, off, base=base, out=base, **c.tables()), out)
+    if mode != "gather":
+        again = mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, a, b, off, dx_base=dx, dx=dx, **c.tables())
+        assert all(torch.equal(p, q) for p, q in zip(again, got))
+    none = torch.full_like(out, 3.0)
+    mgw.grouped_lora(c.x.cuda(), a, b, off, out=none, **c.tables())
+    c.base = None
+    c.check_forward(none, u)
+    assert c.status.item() == 0
