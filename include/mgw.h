@@ -492,6 +492,8 @@ mgw_status mgw_moe_combine_backward(const void *dout, const void *y, int dtype, 
  * Sums are fp32, out is rounded once; the intermediate enters the second product as two bf16
  * parts (17 bits).  The tensor core cuts each addition (of 16 products) off below its accumulator's
  * last bit: u may be off by (K / 32 + 16) 2^-23 of sum |x| |a|.
+ * An infinite b meets both parts, which may differ in sign or be 0: out is infinite or not a number
+ * there.  (So in the backward pass for an infinite a in dx, x in da and dy in db.)
  * x           device, bf16 [x_rows, K]; row_index device int32 [M], nullable (then x_rows >= M).
  * a           device, bf16 [E, R, K];  b: device, bf16 [E, N, R].
  * scale       device fp32 [E], nullable (1).

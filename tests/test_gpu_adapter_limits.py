@@ -205,3 +205,54 @@ def test_every_build_with_more_tiles_than_sms(R, mode):
     c.base = None
     c.check_forward(none, u)
     assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("M", [30, 900, 3000])
+def test_infinities_that_meet_the_intermediate(M):
+    """An infinite b (a, x, dy) beside finite intermediates: what the formula makes infinite is infinite or not a
+    number (the intermediate's two parts may differ in sign, or one be 0), and all else has the same bits."""
+    c = Case([M // 3, M // 3], 40, 136, 200, none=M // 3, mode="tokens")
+    out, u = c.forward()
+    dx, da, db = c.backward(u)
+    first, second = c.o[:M // 3], c.o[M // 3:2 * (M // 3)]
+    inf = float("inf")
+
+    def same_but(got, want, hit):
+        assert not got[hit].isfinite().any() and torch.equal(got[~hit], want[~hit])
+
+    def where(t, *at):
+        hit = torch.zeros_like(t, dtype=torch.bool)
+        hit[at] = True
+        return hit
+
+    col = torch.arange(c.N, device="cuda")
+    c.b[0, 7, 3], c.b[1, 9, 5] = inf, -inf
+    got, gu = c.forward()
+    hit = where(out, torch.from_numpy(first).cuda()) & (col == 7) | where(out, torch.from_numpy(second).cuda()) & (col == 9)
+    same_but(got, out, hit)
+    assert torch.equal(gu, u)
+    c.b[0, 7, 3], c.b[1, 9, 5] = 0.5, 0.25
+
+    out, u = c.forward()
+    dx, da, db = c.backward(u)
+    c.a[0, 4, 11] = inf
+    got = c.backward(u)
+    same_but(got[0], dx, where(dx, torch.from_numpy(first).cuda()) & (torch.arange(c.K, device="cuda") == 11))
+    assert torch.equal(got[1], da) and torch.equal(got[2], db)
+    c.a[0, 4, 11] = 0.5
+
+    _, u = c.forward()
+    dx, da, db = c.backward(u)
+    c.x[c.t[2], 13] = -inf                     # a row of the first adapter
+    got = c.backward(u)
+    same_but(got[1], da, where(da, 0, slice(None), 13))
+    assert torch.equal(got[0], dx) and torch.equal(got[2], db)
+    c.x[c.t[2], 13] = 1.0
+
+    dx, da, db = c.backward(u)
+    c.dy[c.o[2], 21] = inf                     # its v is infinite, and with it that row of dx and all of da
+    got = c.backward(u)
+    same_but(got[0], dx, where(dx, int(c.o[2])))
+    same_but(got[1], da, where(da, 0))
+    same_but(got[2], db, where(db, 0, 21))
+    assert c.status.item() == 0
