@@ -133,9 +133,10 @@ __global__ void __launch_bounds__(bound_of(SETS), SETS == 1 ? 2 : 1) lora_kernel
     if (a.u != nullptr && rank == 0)
       for (int i = tid; i < t.nrows * a.R; i += kThreads) a.u[static_cast<size_t>(t.row0) * a.R + i] = 0.0f;
     const int wide = min(nt1 * kBk, N) / 8 - nt0 * (kBk / 8);  // 16-byte pieces of a row
-    if (out == nullptr || out == base || wide <= 0) return;
+    // (looked at even where nothing is copied: an index out of range is reported)
     for (int i = tid; i < t.nrows; i += kThreads)
       s_rows[i] = row_place(a.out_index, t.row0 + i, a.out_rows, rank == 0 ? a.status : nullptr);
+    if (out == nullptr || out == base || wide <= 0) return;
     __syncthreads();
     constexpr int kSteps = 4;
     for (int i0 = tid; i0 < t.nrows * wide; i0 += kSteps * kThreads) {

@@ -256,3 +256,26 @@ def test_infinities_that_meet_the_intermediate(M):
     same_but(got[1], da, where(da, 0))
     same_but(got[2], db, where(db, 0, 21))
     assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("M", [30, 900, 3000])
+def test_a_bad_place_of_a_row_without_an_adapter_is_reported(M):
+    """Also where nothing is to be copied for it: in place, and without dx."""
+    c = Case([M // 3, M // 3], 16, 64, 128, none=M // 3, mode="tokens")
+    want, u = c.forward()
+    bad = c.out_index.clone()
+    bad[-1] = c.M
+    a, b, off = c.a.cuda(), c.b.cuda(), torch.from_numpy(c.off).cuda()
+    tables = dict(c.tables(), out_index=bad)
+    assert c.status.item() == 0
+    base, dx = c.base.cuda(), c.dx_base.cuda()
+    calls = {"copied": lambda: mgw.grouped_lora(c.x.cuda(), a, b, off, base=base, **tables),
+             "in place": lambda: mgw.grouped_lora(c.x.cuda(), a, b, off, base=base, out=base, **tables),
+             "dx": lambda: mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, a, b, off, **tables),
+             "dx in place": lambda: mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, a, b, off, dx_base=dx, dx=dx, **tables),
+             "no dx": lambda: mgw.grouped_lora_backward(c.dy.cuda(), c.x.cuda(), u, a, b, off, with_dx=False, **tables)}
+    for name, call in calls.items():
+        call()
+        assert c.status.item() == mgw.MGW_DEV_BAD_INDEX, name
+        c.status.zero_()
+    assert torch.equal(base[c.o[:-1]], want[c.o[:-1]])
