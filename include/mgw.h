@@ -551,15 +551,17 @@ size_t mgw_grouped_lora_backward_workspace_bytes(int E, int M, int K, int N, int
  * to their element, elements (>= 0), MGW_TYPE_*.  At most 2^42 bytes and 2^24 tensors. */
 
 /* mgw_grad_norm -- norm = sqrt(sum over all tensors and elements of g^2), 0 for no elements.
- * The sum's order is fixed by the sizes and alignments; right to a few fp32 roundings wherever
- * the norm is an fp32 number, however large or small the elements' squares.
+ * The sum's order is fixed by the sizes, the alignments, the device and whether the context can run
+ * clusters; right to a few fp32 roundings wherever the norm is an fp32 number, however large or small
+ * the elements' squares.
  * norm       device fp32, one number.
  * workspace  device, 16-byte aligned, mgw_grad_workspace_bytes(n) bytes; need not be initialised.
  *            Calls sharing it must not overlap. */
 mgw_status mgw_grad_norm(const void *const *grads, const int64_t *sizes, const int *dtypes, int n,
                          float *norm, void *workspace, size_t workspace_bytes, void *stream);
 
-/* mgw_grad_clip -- outs[i] = grads[i] * min(1, max_norm / (norm + eps)), each rounded once.
+/* mgw_grad_clip -- outs[i] = grads[i] * min(1, max_norm / (norm + eps)), an fp32 product,
+ * which for bf16 is rounded again.
  * outs       null: in place.  Otherwise each of its tensor's type and size; the tensor itself, or
  *            memory that overlaps no tensor of the call.  No tensor is listed twice.
  * max_norm, eps >= 0.

@@ -211,7 +211,6 @@ cudaError_t launch_combine_backward(const CombineBwdArgs& a, bool f32, cudaStrea
 // Low-rank adapters (lora.cu): out = base + scale (in W1^T) W2^T over the rows of adapter e.
 // Forward: in = x, W1 = A [E, R, K], W2 = B [E, N, R].  Transposed, the data gradient: in = dy,
 // W1 = B and W2 = A as they are stored; then K is B's axis of N and the other way round.
-constexpr int kMaxRank = 128;
 struct LoraArgs {
   CUtensorMap tm_x;    // in bf16 [in_rows, K], box 64 columns x 128 rows, 128B swizzle
   CUtensorMap tm_w1;   // [E, R, K]: box 64 x padded rank; transposed [E, K, R]: box 64 x 64

@@ -45,7 +45,7 @@ constexpr int kMaxSlots = 12;
 constexpr int kBufs = 4;              // accumulators of 64 columns
 constexpr uint32_t kTmemCols = 256;   // those; before them the partial sums
 constexpr int kBars = 4 * kMaxSlots + 1 + 2 * kBufs + 1;
-constexpr int kTmpBytes = 96;         // find_tile's ints (22 at most); then [4] TMEM [5] abort
+constexpr int kTmpBytes = 96;         // find_tile's ints (18 of ten warps, the most); then [4] TMEM [5] abort
 
 // Epilogue sets of four warps: two where one CTA fills an SM, one where two CTAs share it.  (Two CTAs of
 // two sets have 80 registers a thread; what did not fit, which no L1 holds beside this much shared

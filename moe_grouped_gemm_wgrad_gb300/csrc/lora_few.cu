@@ -12,7 +12,8 @@
 // tiles in shared memory, TMEM and four more waits: 16 rows of 16 adapters, rank 16, 4096 x 4096, take
 // lora.cu's kernel 19 us and this one 6, which is launch and four loads that wait for one another
 // (offsets, row index, x and A, the other CTAs' sums).  128 rows of 32 adapters, rank 64, 4096 x 8192: 17 us
-// for 55 MB.
+// for 55 MB.  B's first pieces are in registers while A's sums are exchanged, which takes all 128 that two CTAs
+// an SM have: the build for rank 33 to 64 spills 36 bytes a thread, that for more 12.
 #include <cuda_runtime.h>
 
 #include <cstdint>
