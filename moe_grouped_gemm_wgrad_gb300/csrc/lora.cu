@@ -18,7 +18,8 @@
 // 4096 x 4096, rank 64, u saved: 75 us, 5.4 TB/s; of these 25 us the input's half (a bare TMA read of the
 // same boxes takes 24.5), 36 the output's (half of its traffic is writes), the rest launch, setup and
 // the exchange between the halves, when HBM is idle.  65536 gathered rows of 64 adapters, 4096 x 1536,
-// rank 32: 134 us, bound by L2 in the input's half (every row of x is read eight times).
+// rank 32 (every row of x is read eight times): 135 us, with HBM at 49% and L2 at 35% of their peaks: what
+// bounds it are the loads that two CTAs an SM have in flight in either half.
 //
 // Both halves stream through one ring of shared-memory slots: 64 columns of 128 rows (the input's,
 // then the base's, which become the output's in place) and the weight's tile that goes with them.
