@@ -1025,8 +1025,8 @@ mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const in
   if (!aligned16(dy_bf16) || !aligned16(u) || !aligned16(dx_base_bf16) || !aligned16(dx_bf16) ||
       !aligned16(da_bf16) || !aligned16(db_bf16) || !aligned16(workspace))
     return MGW_ERR_INVALID_ARG;
+  const size_t need = weights ? mgw_grouped_lora_backward_workspace_bytes(E, M, K, N, R) : 0;
   if (weights) {
-    const size_t need = mgw_grouped_lora_backward_workspace_bytes(E, M, K, N, R);
     if (need > 0 && !workspace) return MGW_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MGW_ERR_CAPACITY;
   }
@@ -1034,7 +1034,7 @@ mgw_status mgw_grouped_lora_backward(const void* dy_bf16, int out_rows, const in
     // dx may be dx_base itself, and dy where nothing reads that again
     const bool dy_again = weights || dx_bf16 != dy_bf16 || K != N;
     const Span written[] = {span(dx_bf16, out_rows, K, 2), span(da_bf16, E, int64_t(R) * K, 2),
-                            span(db_bf16, E, int64_t(N) * R, 2), span(weights ? workspace : nullptr, workspace_bytes, 1, 1)};
+                            span(db_bf16, E, int64_t(N) * R, 2), span(workspace, need, 1, 1)};
     const Span read[] = {span(dy_again ? dy_bf16 : nullptr, out_rows, N, 2),
                          span(dx_base_bf16 == dx_bf16 ? nullptr : dx_base_bf16, out_rows, K, 2),
                          span(weights ? x_bf16 : nullptr, x_rows, K, 2), span(weights ? u : nullptr, M, R, 4),

@@ -279,3 +279,17 @@ def test_a_bad_place_of_a_row_without_an_adapter_is_reported(M):
         assert c.status.item() == mgw.MGW_DEV_BAD_INDEX, name
         c.status.zero_()
     assert torch.equal(base[c.o[:-1]], want[c.o[:-1]])
+
+
+def test_outputs_behind_the_workspace_in_one_buffer():
+    """Only the bytes that the call needs of a larger workspace are its own."""
+    c = Case([200, 300], 16, 64, 128, mode="tokens")
+    _, u = c.forward()
+    want = c.backward(u)
+    need = mgw.load().mgw_grouped_lora_backward_workspace_bytes(c.E, c.M, c.K, c.N, c.R)
+    arena = torch.empty(need + c.M * c.K * 2, dtype=torch.uint8, device="cuda")
+    assert need % 16 == 0
+    got = c.backward(u, dx=arena[need:].view(torch.bfloat16).view(c.M, c.K), workspace=arena)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    with pytest.raises(mgw.MgwError):
+        c.backward(u, dx=arena[need - 16:-16].view(torch.bfloat16).view(c.M, c.K), workspace=arena)
